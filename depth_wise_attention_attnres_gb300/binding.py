@@ -18,6 +18,7 @@ import torch
 from . import build as _build
 
 F32, BF16 = 0, 1
+GATE_IDENTITY, GATE_SIGMOID = 0, 1
 _STATUS = {0: "ATTNRES_OK", 1: "ATTNRES_ERR_INVALID_ARG", 2: "ATTNRES_ERR_UNSUPPORTED",
            3: "ATTNRES_ERR_CUDA", 4: "ATTNRES_ERR_TIMEOUT"}
 
@@ -57,6 +58,16 @@ _SIGNATURES = {
                            _I32, _VP, _VP, _VP, _VP, _I64, _VP],
     "attnres_block_pass_noalloc": [_VP, _I64, _I32, _I32, _I64, _I32, _I32, _VP, _VP, _F, _VP,
                                    _I64, _I32, _VP, _I64, _VP],
+    "attnres_gated_residual": [_VP, _VP, _VP, _F, _VP, _I64, _I32, _I32, _F, _I64, _I32, _I32, _I32, _VP, _VP, _F,
+                               _VP, _VP],
+    "attnres_gated_residual_bwd": [_VP, _VP, _F, _VP, _I64, _I32, _I32, _F, _I64, _I32, _I32, _I32, _VP, _VP, _F, _VP,
+                                   _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _I64, _VP],
+    "attnres_gated_residual_bwd_scratch_floats": [_I64, _I32, _I64],
+    "attnres_rmsnorm_bwd": [_VP, _I64, _I32, _I32, _VP, _F, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _I64, _VP],
+    "attnres_rmsnorm_bwd_scratch_floats": [_I64, _I32],
+    "attnres_grad_norm": [_VP, _VP, _VP, _I32, _VP, _VP, _I64, _VP],
+    "attnres_grad_clip": [_VP, _VP, _VP, _VP, _VP, _I32, _F, _VP, _VP, _I64, _VP],
+    "attnres_grad_norm_scratch_floats": [_I32],
     "attnres_device_status": [_VP],
     "attnres_selftest_wait_timeout": [_VP],
     "attnres_test_fail_launch": [_I64],
@@ -93,8 +104,8 @@ def lib() -> ctypes.CDLL:
                 fn = getattr(handle, name)
                 fn.argtypes = args
                 fn.restype = (ctypes.c_char_p if name == "attnres_status_string" else
-                              ctypes.c_int64 if name in ("attnres_block_bwd_scratch_floats",
-                                                         "attnres_test_fail_launch") else ctypes.c_int)
+                              ctypes.c_int64 if name.endswith("_scratch_floats") or
+                              name == "attnres_test_fail_launch" else ctypes.c_int)
             _lib = handle
     return _lib
 
@@ -333,6 +344,208 @@ def attnres_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, out: torch
     _check("attnres_rmsnorm", lib().attnres_rmsnorm(
         _ptr(x), T, d, _dtype(x), _ptr(gamma), eps, _ptr(out), _stream(stream)))
     return out
+
+
+def _like(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: int) -> int:
+    """The pointer of a contiguous tensor of a shape and type on a device."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return t.data_ptr()
+
+
+def _scratch(scratch, need: int, device: int, stream) -> torch.Tensor:
+    """A call's scratch: the caller's, checked, or a new one that lives until `stream` is done with it."""
+    if scratch is None:
+        scratch = torch.empty(need, device=torch.device("cuda", device), dtype=torch.float32)
+        if stream is not None:
+            scratch.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                  torch.cuda.ExternalStream(int(stream)))
+    elif (scratch.dtype != torch.float32 or scratch.numel() < need or not scratch.is_contiguous() or
+          scratch.get_device() != device):
+        raise ValueError(f"scratch must be contiguous fp32 of at least {need} elements on the current CUDA device")
+    return scratch
+
+
+def _gate(gate: torch.Tensor | None, gate_rows: int, T: int, d: int, device: int) -> tuple[int | None, int]:
+    """(pointer, dtype code) of a gate [ceil(T / gate_rows), d]."""
+    if gate is None:
+        return None, F32
+    if gate_rows < 1:
+        raise ValueError("gate_rows must be at least 1")
+    return _like("gate", gate, (-(-T // gate_rows), d), gate.dtype, device), _dtype(gate)
+
+
+def attnres_gated_residual(f: torch.Tensor, x: torch.Tensor | None, gamma_post: torch.Tensor | None, eps_post: float,
+                           gate: torch.Tensor | None, gate_rows: int, gate_act: int, scale: float,
+                           x_out: torch.Tensor, gamma_pre: torch.Tensor | None = None, eps_pre: float = 0.0,
+                           normed: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """x_out = x + scale * act(gate) * RMSNorm_post(f) and, with gamma_pre, normed = RMSNorm_pre(x_out).
+
+    f, normed [T, d] of one type; x, x_out [T, d] of one type (fp32 if f is; x
+    may be None for 0, and x_out may be x); gate [ceil(T / gate_rows), d], token
+    t taking row t // gate_rows, or None; gamma_post None for no post-norm."""
+    T, d = _rows(f)
+    device, shape = torch.cuda.current_device(), f.shape
+    gptr, gcode = _gate(gate, gate_rows, T, d, device)
+    _check("attnres_gated_residual", lib().attnres_gated_residual(
+        _like("f", f, shape, f.dtype, device), None if x is None else _like("x", x, shape, x_out.dtype, device),
+        None if gamma_post is None else _like("gamma_post", gamma_post, (d,), torch.float32, device), eps_post,
+        gptr, gate_rows, gcode, gate_act, scale, T, d, _dtype(f), _dtype(x_out),
+        _like("x_out", x_out, shape, x_out.dtype, device),
+        None if gamma_pre is None else _like("gamma_pre", gamma_pre, (d,), torch.float32, device), eps_pre,
+        None if normed is None else _like("normed", normed, shape, f.dtype, device), _stream(stream)))
+    return x_out
+
+
+def attnres_gated_residual_bwd_scratch_floats(T: int, d: int, gate_rows: int = 1) -> int:
+    """fp32 scratch elements attnres_gated_residual_bwd needs (gate_rows 1 without a gate)."""
+    return int(lib().attnres_gated_residual_bwd_scratch_floats(T, d, gate_rows))
+
+
+def attnres_gated_residual_bwd(f: torch.Tensor, gamma_post: torch.Tensor | None, eps_post: float,
+                               gate: torch.Tensor | None, gate_rows: int, gate_act: int, scale: float,
+                               x_out: torch.Tensor | None, gamma_pre: torch.Tensor | None, eps_pre: float,
+                               dx_out: torch.Tensor | None, dnormed: torch.Tensor | None,
+                               df: torch.Tensor | None, dx: torch.Tensor | None = None,
+                               dgate: torch.Tensor | None = None, dgamma_post: torch.Tensor | None = None,
+                               dgamma_pre: torch.Tensor | None = None, accumulate: bool = True,
+                               scratch: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of attnres_gated_residual from dL/dx_out and dL/dnormed (either may be None; without dnormed
+    x_out may be None too).
+
+    Writes df (like f), dx (like dx_out; may be it) and dgate (like gate), each
+    None if not wanted; dgamma_post and dgamma_pre (fp32 [d] or None) are added
+    to, or with accumulate False written. scratch: fp32, at least
+    attnres_gated_residual_bwd_scratch_floats(T, d, gate_rows) elements
+    (allocated here if None)."""
+    T, d = _rows(f)
+    device, shape = torch.cuda.current_device(), f.shape
+    grad = dx_out if dx_out is not None else dx
+    gdt = torch.float32 if grad is None else grad.dtype
+    code = F32 if grad is None else _dtype(grad)
+    rows = 1 if gate is None else gate_rows
+    gptr, gcode = _gate(gate, gate_rows, T, d, device)
+    if dgate is not None and gate is None:
+        raise ValueError("dgate needs a gate")
+
+    def rowwise(name, t, dtype):
+        return None if t is None else _like(name, t, shape, dtype, device)
+
+    def gain(name, t):
+        return None if t is None else _like(name, t, (d,), torch.float32, device)
+
+    need = attnres_gated_residual_bwd_scratch_floats(T, d, rows)
+    scratch = _scratch(scratch, need, device, stream)
+    _check("attnres_gated_residual_bwd", lib().attnres_gated_residual_bwd(
+        _like("f", f, shape, f.dtype, device), gain("gamma_post", gamma_post), eps_post, gptr, rows, gcode, gate_act,
+        scale, T, d, _dtype(f), _dtype(f if x_out is None else x_out),
+        None if x_out is None else rowwise("x_out", x_out, x_out.dtype), gain("gamma_pre", gamma_pre),
+        eps_pre, rowwise("dx_out", dx_out, gdt), code, rowwise("dnormed", dnormed, f.dtype), rowwise("df", df, f.dtype),
+        rowwise("dx", dx, gdt), None if dgate is None else _like("dgate", dgate, gate.shape, gate.dtype, device),
+        gain("dgamma_post", dgamma_post), gain("dgamma_pre", dgamma_pre), int(bool(accumulate)), scratch.data_ptr(),
+        scratch.numel(), _stream(stream)))
+
+
+def attnres_rmsnorm_bwd_scratch_floats(T: int, d: int) -> int:
+    """fp32 scratch elements attnres_rmsnorm_bwd needs."""
+    return int(lib().attnres_rmsnorm_bwd_scratch_floats(T, d))
+
+
+def attnres_rmsnorm_bwd(x: torch.Tensor, gamma: torch.Tensor, eps: float, dy: torch.Tensor,
+                        dres: torch.Tensor | None, dx: torch.Tensor, dgamma: torch.Tensor | None = None,
+                        accumulate: bool = True, scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradients of attnres_rmsnorm (and of a pre-norm of the row x): dx = dres + dL/dx, and dgamma
+    (fp32 [d] or None) added to, or with accumulate False written. x and dy [T, d] of one type; dres (or
+    None) and dx of one type, dx may be dres. scratch: fp32, at least
+    attnres_rmsnorm_bwd_scratch_floats(T, d) elements (allocated here if None)."""
+    T, d = _rows(x)
+    device, shape = torch.cuda.current_device(), x.shape
+    scratch = _scratch(scratch, attnres_rmsnorm_bwd_scratch_floats(T, d), device, stream)
+    _check("attnres_rmsnorm_bwd", lib().attnres_rmsnorm_bwd(
+        _like("x", x, shape, x.dtype, device), T, d, _dtype(x), _like("gamma", gamma, (d,), torch.float32, device), eps,
+        _like("dy", dy, shape, x.dtype, device), None if dres is None else _like("dres", dres, shape, dx.dtype, device),
+        _dtype(dx), _like("dx", dx, shape, dx.dtype, device),
+        None if dgamma is None else _like("dgamma", dgamma, (d,), torch.float32, device), int(bool(accumulate)),
+        scratch.data_ptr(), scratch.numel(), _stream(stream)))
+    return dx
+
+
+class GradList:
+    """The gradients of attnres_grad_norm and attnres_grad_clip, checked and laid out for the call once.
+
+    Holds its tensors (contiguous fp32 or bf16, of any shape) and, for clipping
+    out of place, where each goes. A program whose gradients stay in the same
+    buffers keeps one; the values are read anew in every call. Tensors must not
+    be given other storage (set_, resize_) while it is in use."""
+
+    def __init__(self, grads, outs=None):
+        self.grads, self.outs = list(grads), None if outs is None else list(outs)
+        n = len(self.grads)
+        if self.outs is not None and len(self.outs) != n:
+            raise ValueError("outs must hold one tensor per gradient")
+        devices = set()
+        for t in self.grads + (self.outs or []):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("gradients must be contiguous tensors on a CUDA device")
+            devices.add(t.get_device())
+        if len(devices) > 1:
+            raise ValueError("gradients must be on one device")
+        self.device = devices.pop() if devices else None
+        for g, o in zip(self.grads, self.outs or []):
+            if g.numel() != o.numel():
+                raise ValueError("outs must hold as many elements as their gradients")
+        pointers, counts, codes = _VP * max(n, 1), _I64 * max(n, 1), _I32 * max(n, 1)
+        self.n = n
+        self.pointers = pointers(*[t.data_ptr() for t in self.grads])
+        self.counts = counts(*[t.numel() for t in self.grads])
+        self.codes = codes(*[_dtype(t) for t in self.grads])
+        self.out_pointers = self.out_codes = None
+        if self.outs is not None:
+            self.out_pointers = pointers(*[t.data_ptr() for t in self.outs])
+            self.out_codes = codes(*[_dtype(t) for t in self.outs])
+        self.scratch_floats = attnres_grad_norm_scratch_floats(n)
+
+
+def _grad_call(grads, outs, norm, scratch, stream) -> tuple[GradList, torch.Tensor]:
+    """The list, its scratch and checks of a gradient call."""
+    if not isinstance(grads, GradList):
+        grads = GradList(grads, outs)
+    elif outs is not None:
+        raise ValueError("a GradList already holds where its gradients go")
+    device = torch.cuda.current_device()
+    if grads.device is not None and grads.device != device:
+        raise ValueError("gradients must be on the current CUDA device")
+    if norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != device:
+        raise ValueError("norm must be one fp32 element on the current CUDA device")
+    return grads, _scratch(scratch, grads.scratch_floats, device, stream)
+
+
+def attnres_grad_norm_scratch_floats(n: int) -> int:
+    """fp32 scratch elements attnres_grad_norm and attnres_grad_clip need for n tensors."""
+    return int(lib().attnres_grad_norm_scratch_floats(n))
+
+
+def attnres_grad_norm(grads, norm: torch.Tensor, scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """norm (fp32, one element) = sqrt of the sum of squares of every element of a list of tensors or a GradList."""
+    grads, scratch = _grad_call(grads, None, norm, scratch, stream)
+    _check("attnres_grad_norm", lib().attnres_grad_norm(
+        grads.pointers, grads.counts, grads.codes, grads.n, norm.data_ptr(), scratch.data_ptr(), scratch.numel(),
+        _stream(stream)))
+    return norm
+
+
+def attnres_grad_clip(grads, max_norm: float, norm: torch.Tensor, outs=None, scratch: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """The gradients times max_norm / norm where their norm (returned in `norm`, before clipping) is finite and
+    above max_norm, else times 1: in place, or into `outs` (fp32 or bf16, all elements written; a GradList holds
+    its own)."""
+    grads, scratch = _grad_call(grads, outs, norm, scratch, stream)
+    _check("attnres_grad_clip", lib().attnres_grad_clip(
+        grads.pointers, grads.counts, grads.codes, grads.out_pointers, grads.out_codes, grads.n, max_norm,
+        norm.data_ptr(), scratch.data_ptr(), scratch.numel(), _stream(stream)))
+    return norm
 
 
 def attnres_block_stage1(Src: torch.Tensor, n_src: int, W: torch.Tensor, Gamma: torch.Tensor,

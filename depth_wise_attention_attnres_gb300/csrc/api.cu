@@ -5,9 +5,12 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <map>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <tuple>
 
 #include "attnres.h"
@@ -183,6 +186,130 @@ template <typename F>
 int launched(F&& launch) {
   if (injected_failure()) return ATTNRES_ERR_CUDA;
   return status_of(launch());
+}
+
+Range range_if(const void* p, int64_t bytes) { return p ? range_of(p, bytes) : Range{}; }
+
+// Whether an output overlaps another output or an input (none for a null pointer).
+template <int NO, int NI>
+bool any_overlap(const Range (&out)[NO], const Range (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return true;
+    for (int j = 0; j < NI; ++j)
+      if (overlap(out[i], in[j])) return true;
+  }
+  return false;
+}
+
+// Whether a pointer is off the boundary of its elements.
+bool off_element(const void* p, int64_t es) { return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(es - 1)) != 0; }
+
+// Elements of one tensor beyond which byte offsets would not fit (none is that large).
+constexpr int64_t kMaxElements = int64_t{1} << 56;
+// And elements of one gradient list (their units are counted in 32 bits).
+constexpr int64_t kMaxGradElements = int64_t{1} << 42;
+
+int64_t groups_of(int64_t T, int64_t gate_rows) { return T == 0 ? 0 : (T - 1) / gate_rows + 1; }
+
+// The arguments that the gated residual and its backward share.
+int check_residual(int64_t T, int32_t d, int32_t dtype, int32_t x_dtype, float eps_post, float eps_pre,
+                   const void* gate, int64_t gate_rows, int32_t gate_dtype, int32_t gate_act, float scale) {
+  if (d < 1 || T < 0 || T > kMaxElements / d || !valid_dtype(dtype) || !valid_dtype(x_dtype) ||
+      (dtype == ATTNRES_F32 && x_dtype != ATTNRES_F32) || !valid_eps(eps_post) || !valid_eps(eps_pre) ||
+      !(scale > -3.4e38f && scale < 3.4e38f))
+    return ATTNRES_ERR_INVALID_ARG;
+  if (gate_act != ATTNRES_GATE_IDENTITY && gate_act != ATTNRES_GATE_SIGMOID) return ATTNRES_ERR_INVALID_ARG;
+  if (gate && (gate_rows < 1 || !valid_dtype(gate_dtype))) return ATTNRES_ERR_INVALID_ARG;
+  return ATTNRES_OK;
+}
+
+int check_and_run_residual_bwd(const ResidualBwdArgs& a, int64_t scratch_floats, void* stream) {
+  const int64_t need = residual_bwd_scratch(a.T, a.d, a.gate_rows);
+  if (scratch_floats < need || (need > 0 && !a.scratch)) return ATTNRES_ERR_INVALID_ARG;
+  const int64_t E = a.T * a.d, es = a.f_bf16 ? 2 : 4, xs = a.x_bf16 ? 2 : 4, ds = a.dx_bf16 ? 2 : 4;
+  const int64_t gates = a.gate ? groups_of(a.T, a.gate_rows) * a.d * (a.g_bf16 ? 2 : 4) : 0, gains = a.d * 4ll;
+  const Range in[] = {range_if(a.f, E * es), range_if(a.gate, gates), range_if(a.gpost, gains), range_if(a.gpre, gains),
+                      range_if(a.xo, E * xs), a.dxo == a.dx ? Range{} : range_if(a.dxo, E * ds), range_if(a.dn, E * es)};
+  const Range out[] = {range_if(a.df, E * es), range_if(a.dx, E * ds), range_if(a.dgate, gates),
+                       range_if(a.dgpost, gains), range_if(a.dgpre, gains),
+                       range_if(a.scratch, scratch_floats * 4)};
+  const int64_t gs = a.g_bf16 ? 2 : 4;
+  if (any_overlap(out, in) || off_element(a.f, es) || off_element(a.dn, es) || off_element(a.df, es) ||
+      off_element(a.xo, xs) || off_element(a.dxo, ds) || off_element(a.dx, ds) || off_element(a.gate, gs) ||
+      off_element(a.dgate, gs) || off_element(a.gpost, 4) || off_element(a.gpre, 4) || off_element(a.dgpost, 4) ||
+      off_element(a.dgpre, 4) || off_element(a.scratch, 4))
+    return ATTNRES_ERR_INVALID_ARG;
+  return run_residual_bwd(a, as_stream(stream));
+}
+
+// Checks a gradient list: pointers, types, and that outputs overlap no other
+// tensor of the list. Ranges are walked in address order; a list whose
+// storage does not come in that order is sorted first (its indices on the
+// stack, or on the heap for a long list; without memory the call is refused).
+struct Span {
+  uintptr_t lo, hi;
+  int32_t tensor;
+  bool written;
+};
+int check_grads(const GradArgs& a, int64_t scratch_floats) {
+  if (a.n < 0 || !a.norm || !a.scratch || scratch_floats < grads_scratch(a.n)) return ATTNRES_ERR_INVALID_ARG;
+  if (a.n > 0 && (!a.grads || !a.counts || !a.dtypes)) return ATTNRES_ERR_INVALID_ARG;
+  if (off_element(a.norm, 4) || off_element(a.scratch, 4)) return ATTNRES_ERR_INVALID_ARG;
+  const Range rn = range_of(a.norm, 4), rs = range_of(a.scratch, scratch_floats * 4);
+  if (overlap(rn, rs)) return ATTNRES_ERR_INVALID_ARG;
+  int64_t total = 0;
+  for (int i = 0; i < a.n; ++i) {
+    const int64_t c = a.counts[i];
+    if (c < 0 || c > kMaxGradElements || !valid_dtype(a.dtypes[i])) return ATTNRES_ERR_INVALID_ARG;
+    if (a.outs && !valid_dtype(a.out_dtypes[i])) return ATTNRES_ERR_INVALID_ARG;
+    if (c == 0) continue;
+    total += c;
+    if (total > kMaxGradElements) return ATTNRES_ERR_INVALID_ARG;
+    const int gs = elem_size(a.dtypes[i]);
+    if (!a.grads[i] || off_element(a.grads[i], gs)) return ATTNRES_ERR_INVALID_ARG;
+    const Range rg = range_of(a.grads[i], c * gs);
+    if (overlap(rn, rg) || overlap(rs, rg)) return ATTNRES_ERR_INVALID_ARG;
+    if (!a.outs) continue;
+    const int os = elem_size(a.out_dtypes[i]);
+    if (!a.outs[i] || off_element(a.outs[i], os)) return ATTNRES_ERR_INVALID_ARG;
+    if (a.outs[i] == a.grads[i] && os != gs) return ATTNRES_ERR_INVALID_ARG;
+    const Range ro = range_of(a.outs[i], c * os);
+    if (overlap(rn, ro) || overlap(rs, ro)) return ATTNRES_ERR_INVALID_ARG;
+  }
+  if (!a.outs || a.n == 0) return ATTNRES_OK;
+  constexpr int kOnStack = 512;
+  Span local[2 * kOnStack];
+  Span* span = local;
+  std::unique_ptr<Span[]> heap;
+  if (a.n > kOnStack) {
+    heap.reset(new (std::nothrow) Span[2 * static_cast<size_t>(a.n)]);
+    if (!heap) return ATTNRES_ERR_UNSUPPORTED;
+    span = heap.get();
+  }
+  int m = 0;
+  bool sorted = true;
+  for (int i = 0; i < a.n; ++i) {
+    if (a.counts[i] == 0) continue;
+    const bool in_place = a.outs[i] == a.grads[i];
+    const Range rg = range_of(a.grads[i], a.counts[i] * elem_size(a.dtypes[i]));
+    span[m++] = Span{rg.lo, rg.hi, i, in_place};
+    if (!in_place) {
+      const Range ro = range_of(a.outs[i], a.counts[i] * elem_size(a.out_dtypes[i]));
+      span[m++] = Span{ro.lo, ro.hi, i, true};
+    }
+  }
+  for (int i = 1; i < m && sorted; ++i) sorted = span[i - 1].lo <= span[i].lo;
+  if (!sorted) std::sort(span, span + m, [](const Span& p, const Span& q) { return p.lo < q.lo; });
+  // Overlaps with a written span: against the furthest end of any span so far,
+  // and for a written span also of any read one (two read ones may overlap).
+  uintptr_t end_all = 0, end_written = 0;
+  for (int i = 0; i < m; ++i) {
+    if (span[i].lo < (span[i].written ? end_all : end_written)) return ATTNRES_ERR_INVALID_ARG;
+    end_all = std::max(end_all, span[i].hi);
+    if (span[i].written) end_written = std::max(end_written, span[i].hi);
+  }
+  return ATTNRES_OK;
 }
 
 // Checks and fills the arguments of one full read. Returns a status.
@@ -411,6 +538,12 @@ void running_sum_plan(int S, int es, int* stored) {
 
 }  // namespace
 
+namespace attnres {
+int launched_status(cudaError_t (*fn)(void*), void* arg) {
+  return launched([&] { return fn(arg); });
+}
+}  // namespace attnres
+
 extern "C" {
 
 int attnres_abi_version(void) { return 1; }
@@ -572,6 +705,100 @@ int attnres_rmsnorm(const void* x, int64_t T, int32_t d, int32_t dtype, const fl
   // In place (out == x) is allowed; a partial overlap is not.
   if (out != x && overlap(range_of(x, bytes), range_of(out, bytes))) return ATTNRES_ERR_INVALID_ARG;
   return launched([&] { return launch_rmsnorm(x, T, d, dtype == ATTNRES_BF16, gamma, eps, out, as_stream(stream)); });
+}
+
+int attnres_gated_residual(const void* f, const void* x, const float* gamma_post, float eps_post, const void* gate,
+                           int64_t gate_rows, int32_t gate_dtype, int32_t gate_act, float scale, int64_t T, int32_t d,
+                           int32_t dtype, int32_t x_dtype, void* x_out, const float* gamma_pre, float eps_pre,
+                           void* normed, void* stream) {
+  int st = check_residual(T, d, dtype, x_dtype, eps_post, eps_pre, gate, gate_rows, gate_dtype, gate_act, scale);
+  if (st != ATTNRES_OK || T == 0) return st;
+  if (!f || !x_out || !gamma_pre != !normed) return ATTNRES_ERR_INVALID_ARG;
+  const int64_t E = T * d, es = elem_size(dtype), xs = elem_size(x_dtype);
+  const Range in[] = {range_of(f, E * es), x == x_out ? Range{} : range_if(x, E * xs), range_if(gamma_post, d * 4ll),
+                      range_if(gamma_pre, d * 4ll),
+                      range_if(gate, gate ? groups_of(T, gate_rows) * d * elem_size(gate_dtype) : 0)};
+  const Range out[] = {range_of(x_out, E * xs), range_if(normed, E * es)};
+  if (any_overlap(out, in) || off_element(f, es) || off_element(normed, es) || off_element(x, xs) ||
+      off_element(x_out, xs) || off_element(gamma_post, 4) || off_element(gamma_pre, 4) ||
+      off_element(gate, elem_size(gate_dtype)))
+    return ATTNRES_ERR_INVALID_ARG;
+  const ResidualArgs a{f, x, gate, gate ? gate_rows : 1, gamma_post, gamma_pre, eps_post, eps_pre, scale, T, d,
+                       dtype == ATTNRES_BF16, x_dtype == ATTNRES_BF16, gate_dtype == ATTNRES_BF16,
+                       gate_act == ATTNRES_GATE_SIGMOID, x_out, normed};
+  return run_residual(a, as_stream(stream));
+}
+
+int64_t attnres_gated_residual_bwd_scratch_floats(int64_t T, int32_t d, int64_t gate_rows) {
+  if (T < 0 || d < 1 || gate_rows < 1 || T > kMaxElements / d) return -1;
+  return residual_bwd_scratch(T, d, gate_rows);
+}
+
+int64_t attnres_rmsnorm_bwd_scratch_floats(int64_t T, int32_t d) {
+  return attnres_gated_residual_bwd_scratch_floats(T, d, 1);
+}
+
+int attnres_gated_residual_bwd(const void* f, const float* gamma_post, float eps_post, const void* gate,
+                               int64_t gate_rows, int32_t gate_dtype, int32_t gate_act, float scale, int64_t T,
+                               int32_t d, int32_t dtype, int32_t x_dtype, const void* x_out, const float* gamma_pre,
+                               float eps_pre, const void* dx_out, int32_t dx_dtype, const void* dnormed, void* df,
+                               void* dx, void* dgate, float* dgamma_post, float* dgamma_pre, int32_t accumulate,
+                               float* scratch, int64_t scratch_floats, void* stream) {
+  int st = check_residual(T, d, dtype, x_dtype, eps_post, eps_pre, gate, gate_rows, gate_dtype, gate_act, scale);
+  if (st != ATTNRES_OK) return st;
+  if (!valid_dtype(dx_dtype) || (dtype == ATTNRES_F32 && dx_dtype != ATTNRES_F32)) return ATTNRES_ERR_INVALID_ARG;
+  if (T > 0 && (!f || (!dx_out && !dnormed) || (dnormed && (!x_out || !gamma_pre)) || (dgate && !gate)))
+    return ATTNRES_ERR_INVALID_ARG;
+  const ResidualBwdArgs a{f, gate, gate ? gate_rows : 1, gamma_post, dnormed ? x_out : nullptr, gamma_pre, dx_out,
+                          dnormed, eps_post, eps_pre, scale, T, d, dtype == ATTNRES_BF16, x_dtype == ATTNRES_BF16,
+                          gate_dtype == ATTNRES_BF16, gate_act == ATTNRES_GATE_SIGMOID, dx_dtype == ATTNRES_BF16, df,
+                          dx, dgate, dgamma_post, dgamma_pre, accumulate != 0, scratch};
+  return check_and_run_residual_bwd(a, scratch_floats, stream);
+}
+
+int attnres_rmsnorm_bwd(const void* x, int64_t T, int32_t d, int32_t dtype, const float* gamma, float eps,
+                        const void* dy, const void* dres, int32_t dx_dtype, void* dx, float* dgamma,
+                        int32_t accumulate, float* scratch, int64_t scratch_floats, void* stream) {
+  int st = check_residual(T, d, dtype, dtype, eps, eps, nullptr, 1, ATTNRES_F32, ATTNRES_GATE_IDENTITY, 1.0f);
+  if (st != ATTNRES_OK) return st;
+  if (!valid_dtype(dx_dtype) || (dtype == ATTNRES_F32 && dx_dtype != ATTNRES_F32)) return ATTNRES_ERR_INVALID_ARG;
+  if (T > 0 && (!x || !gamma || !dy || !dx)) return ATTNRES_ERR_INVALID_ARG;
+  ResidualBwdArgs a{};
+  a.gate_rows = 1;
+  a.xo = x;
+  a.gpre = gamma;
+  a.dxo = dres;
+  a.dn = dy;
+  a.eps_pre = eps;
+  a.T = T;
+  a.d = d;
+  a.f_bf16 = a.x_bf16 = dtype == ATTNRES_BF16;
+  a.dx_bf16 = dx_dtype == ATTNRES_BF16;
+  a.dx = dx;
+  a.dgpre = dgamma;
+  a.accumulate = accumulate != 0;
+  a.scratch = scratch;
+  return check_and_run_residual_bwd(a, scratch_floats, stream);
+}
+
+int64_t attnres_grad_norm_scratch_floats(int32_t n) { return n < 0 ? -1 : grads_scratch(n); }
+
+int attnres_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int32_t n, float* norm,
+                      float* scratch, int64_t scratch_floats, void* stream) {
+  GradArgs a{grads, counts, dtypes, nullptr, nullptr, n, 0.f, norm, scratch};
+  const int st = check_grads(a, scratch_floats);
+  return st != ATTNRES_OK ? st : run_grads(a, as_stream(stream));
+}
+
+int attnres_grad_clip(const void* const* grads, const int64_t* counts, const int32_t* dtypes, void* const* outs,
+                      const int32_t* out_dtypes, int32_t n, float max_norm, float* norm, float* scratch,
+                      int64_t scratch_floats, void* stream) {
+  if (!(max_norm >= 0.f) || (outs && n > 0 && !out_dtypes)) return ATTNRES_ERR_INVALID_ARG;
+  // In place: the gradients are their own outputs.
+  GradArgs a{grads, counts, dtypes, outs ? outs : const_cast<void* const*>(grads), outs ? out_dtypes : dtypes, n,
+             max_norm, norm, scratch};
+  const int st = check_grads(a, scratch_floats);
+  return st != ATTNRES_OK ? st : run_grads(a, as_stream(stream));
 }
 
 int attnres_full_bwd(const void* V, int64_t src_stride, int32_t n_src, int64_t T, int32_t d,

@@ -1,0 +1,310 @@
+// The global norm of a list of gradients, and the list scaled to a norm.
+//
+// norm = sqrt(sum g^2) over every element of every tensor; clipping multiplies
+// by max_norm / norm where norm exceeds max_norm. Two launches either way: the
+// first leaves one partial sum per CTA, the second adds them (in fp64, in a
+// fixed order, every CTA for itself) and writes the norm, or the norm and the
+// scaled tensors. Bound by memory: the norm reads every gradient once, the
+// scaling reads them again and writes them.
+//
+// Squares are summed in three scales at once, of g, g 2^80 and g 2^-80: fp32
+// holds g^2 only for 2^-63 < |g| < 2^63, and bf16 and fp32 gradients go far
+// beyond both ends. The sum of g^2 serves unless it overflowed (then the
+// scaled-down sum does: what it loses, |g| < 2^17, is below 2^-53 of a sum
+// over 2^127) or is under 2^-60 (then the scaled-up one, which is below 2^100).
+//
+// The tensors' addresses travel as kernel arguments, so a call needs no table
+// in device memory; the tensors are cut into units of kUnit elements and every
+// CTA takes one run of consecutive units, wherever tensors begin and end.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace attnres {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kUnit = 2048;        // elements
+constexpr int kMaxCtas = 304;      // partial sums of one launch
+constexpr int kMaxTensors = 1024;  // of one launch: 29 KB of the 32,764 bytes of arguments
+
+template <int N>
+struct Table {
+  const void* src[N];
+  void* dst[N];
+  int64_t count[N];
+  uint32_t first[N + 1];  // first unit of each tensor; first[n]: all units
+  uint8_t kind[N];        // 1: src is bf16, 2: dst is bf16
+  int n;
+};
+
+struct Sums {
+  float2 mid, big, small;
+};
+
+__device__ __forceinline__ void add2(Sums& s, float2 x) {
+  const float2 down = make_float2(0x1p-80f, 0x1p-80f), up = make_float2(0x1p80f, 0x1p80f);
+  s.mid = ffma2(x, x, s.mid);
+  const float2 b = fmul2(x, down), t = fmul2(x, up);
+  s.big = ffma2(b, b, s.big);
+  s.small = ffma2(t, t, s.small);
+}
+__device__ __forceinline__ void add_vec(Sums& s, const bf16*, uint4 v) {
+  add2(s, make_float2(bf16_lo(v.x), bf16_hi(v.x)));
+  add2(s, make_float2(bf16_lo(v.y), bf16_hi(v.y)));
+  add2(s, make_float2(bf16_lo(v.z), bf16_hi(v.z)));
+  add2(s, make_float2(bf16_lo(v.w), bf16_hi(v.w)));
+}
+__device__ __forceinline__ void add_vec(Sums& s, const float*, uint4 v) {
+  add2(s, make_float2(__uint_as_float(v.x), __uint_as_float(v.y)));
+  add2(s, make_float2(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+
+// Elements before the first 16-byte boundary at or after p.
+template <typename T>
+__device__ __forceinline__ int64_t head_of(const T* p, int64_t n) {
+  const int64_t h = static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / static_cast<int64_t>(sizeof(T));
+  return h < n ? h : n;
+}
+
+template <typename T>
+__device__ __forceinline__ void sum_segment(Sums& s, const T* p, int64_t n) {
+  constexpr int kV = 16 / sizeof(T), kU = 8;
+  const int64_t head = head_of(p, n);
+  if (threadIdx.x < head) add2(s, make_float2(to_f32(p[threadIdx.x]), 0.f));
+  const uint4* v = reinterpret_cast<const uint4*>(p + head);
+  const int64_t nv = (n - head) / kV;
+  int64_t i = threadIdx.x;
+  for (; i + (kU - 1) * kThreads < nv; i += kU * kThreads) {
+    uint4 x[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) x[u] = v[i + u * kThreads];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) add_vec(s, p, x[u]);
+  }
+  for (; i < nv; i += kThreads) add_vec(s, p, v[i]);
+  for (int64_t k = head + nv * kV + threadIdx.x; k < n; k += kThreads) add2(s, make_float2(to_f32(p[k]), 0.f));
+}
+
+// Runs fn(tensor, first element, elements) over the CTA's share of the units.
+template <int N, typename F>
+__device__ __forceinline__ void for_segments(const Table<N>& t, F&& fn) {
+  const uint32_t units = t.first[t.n];
+  uint32_t u = static_cast<uint32_t>(static_cast<uint64_t>(units) * blockIdx.x / gridDim.x);
+  const uint32_t end = static_cast<uint32_t>(static_cast<uint64_t>(units) * (blockIdx.x + 1) / gridDim.x);
+  if (u >= end) return;
+  int lo = 0, hi = t.n - 1;  // the last tensor whose first unit is at or before u
+  while (lo < hi) {
+    const int m = (lo + hi + 1) / 2;
+    if (t.first[m] <= u) lo = m; else hi = m - 1;
+  }
+  for (int i = lo; u < end; ++i) {
+    const uint32_t stop = min(end, t.first[i + 1]);
+    const int64_t a = static_cast<int64_t>(u - t.first[i]) * kUnit;
+    const int64_t b = min(static_cast<int64_t>(stop - t.first[i]) * kUnit, t.count[i]);
+    fn(i, a, b - a);
+    u = stop;
+  }
+}
+
+__device__ __forceinline__ double warp_sum_f64(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Sums over the CTA; every thread gets them.
+__device__ __forceinline__ void block_sum3(double (&v)[3], double* red) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    v[i] = warp_sum_f64(v[i]);
+    if (lane == 0) red[warp * 3 + i] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    v[i] = 0.0;
+    for (int w = 0; w < kThreads / 32; ++w) v[i] += red[w * 3 + i];
+  }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) grad_sums_kernel(const __grid_constant__ Table<N> t, float* part) {
+  __shared__ double red[3 * kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  Sums s{};
+  for_segments(t, [&](int i, int64_t a, int64_t n) {
+    if (t.kind[i] & 1)
+      sum_segment(s, static_cast<const bf16*>(t.src[i]) + a, n);
+    else
+      sum_segment(s, static_cast<const float*>(t.src[i]) + a, n);
+  });
+  double v[3] = {static_cast<double>(s.mid.x) + s.mid.y, static_cast<double>(s.big.x) + s.big.y,
+                 static_cast<double>(s.small.x) + s.small.y};
+  block_sum3(v, red);
+  if (threadIdx.x < 3) part[3 * blockIdx.x + threadIdx.x] = static_cast<float>(v[threadIdx.x]);
+}
+
+// The norm from the partial sums (the same bits in every CTA).
+__device__ __forceinline__ double norm_of(const float* part, int parts, double* red) {
+  double v[3] = {0.0, 0.0, 0.0};
+  for (int p = threadIdx.x; p < parts; p += kThreads)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] += part[3 * p + i];
+  block_sum3(v, red);
+  if (isinf(v[0])) return sqrt(v[1]) * 0x1p80;
+  if (v[0] < 0x1p-60) return sqrt(v[2]) * 0x1p-80;
+  return sqrt(v[0]);
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const float* part, int parts, float* norm) {
+  __shared__ double red[3 * kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  const double r = norm_of(part, parts, red);
+  if (threadIdx.x == 0) norm[0] = static_cast<float>(r);
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    lds16(p, x);
+  } else {
+    float a[4], b[4];
+    lds16(p, a);
+    lds16(p + 4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = a[i], x[i + 4] = b[i];
+  }
+}
+__device__ __forceinline__ void store8(bf16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                            pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Each thread reads and writes its own elements only: dst may be src.
+template <typename TI, typename TO>
+__device__ __forceinline__ void scale_segment(const TI* src, TO* dst, int64_t n, float c) {
+  int64_t head = head_of(src, n);
+  if (reinterpret_cast<uintptr_t>(dst + head) & 15) head = n;  // no common boundary: element by element
+  const int64_t nv = (n - head) / 8;
+  for (int64_t k = threadIdx.x; k < head; k += kThreads) dst[k] = from_f32<TO>(c * to_f32(src[k]));
+  constexpr int kU = 4;
+  int64_t i = threadIdx.x;
+  for (; i + (kU - 1) * kThreads < nv; i += kU * kThreads) {
+    float x[kU][8];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) load8(src + head + (i + u * kThreads) * 8, x[u]);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[u][e] *= c;
+      store8(dst + head + (i + u * kThreads) * 8, x[u]);
+    }
+  }
+  for (; i < nv; i += kThreads) {
+    float x[8];
+    load8(src + head + i * 8, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= c;
+    store8(dst + head + i * 8, x);
+  }
+  for (int64_t k = head + nv * 8 + threadIdx.x; k < n; k += kThreads) dst[k] = from_f32<TO>(c * to_f32(src[k]));
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+    grad_scale_kernel(const __grid_constant__ Table<N> t, const float* part, int parts, float max_norm, float* norm) {
+  __shared__ double red[3 * kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  const float r = static_cast<float>(norm_of(part, parts, red));
+  if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = r;
+  const float c = (r > max_norm && r < INFINITY) ? max_norm / r : 1.0f;
+  for_segments(t, [&](int i, int64_t a, int64_t n) {
+    if (c == 1.0f && t.src[i] == t.dst[i]) return;
+    switch (t.kind[i]) {
+      case 0: return scale_segment(static_cast<const float*>(t.src[i]) + a, static_cast<float*>(t.dst[i]) + a, n, c);
+      case 1: return scale_segment(static_cast<const bf16*>(t.src[i]) + a, static_cast<float*>(t.dst[i]) + a, n, c);
+      case 2: return scale_segment(static_cast<const float*>(t.src[i]) + a, static_cast<bf16*>(t.dst[i]) + a, n, c);
+      default: return scale_segment(static_cast<const bf16*>(t.src[i]) + a, static_cast<bf16*>(t.dst[i]) + a, n, c);
+    }
+  });
+}
+
+// Tensors [*next, ...) into the table, empty ones left out, until it is full;
+// returns the units taken.
+template <int N>
+uint32_t fill(Table<N>& t, const GradArgs& a, int* next) {
+  t.n = 0;
+  uint32_t units = 0;
+  for (; *next < a.n && t.n < N; ++*next) {
+    const int i = *next;
+    if (a.counts[i] == 0) continue;
+    t.src[t.n] = a.grads[i];
+    t.dst[t.n] = a.outs ? a.outs[i] : nullptr;
+    t.count[t.n] = a.counts[i];
+    t.kind[t.n] = (a.dtypes[i] == ATTNRES_BF16 ? 1 : 0) | (a.outs && a.out_dtypes[i] == ATTNRES_BF16 ? 2 : 0);
+    t.first[t.n] = units;
+    units += static_cast<uint32_t>((a.counts[i] - 1) / kUnit + 1);
+    ++t.n;
+  }
+  t.first[t.n] = units;
+  return units;
+}
+
+unsigned ctas_for(uint32_t units) {
+  const unsigned cap = std::min<unsigned>(kMaxCtas, 2u * static_cast<unsigned>(sm_count()));
+  return std::min<unsigned>(units, cap);
+}
+
+template <int N>
+int run_table(const GradArgs& a, cudaStream_t s) {
+  Table<N> t;
+  int parts = 0;
+  for (int next = 0; next < a.n;) {
+    const uint32_t units = fill(t, a, &next);
+    if (!units) break;
+    const unsigned grid = ctas_for(units);
+    const int e = launch_step(
+        [&] { return launch_pdl(grad_sums_kernel<N>, grid, kThreads, 0, s, t, a.scratch + 3 * parts); });
+    if (e) return e;
+    parts += static_cast<int>(grid);
+  }
+  if (!a.outs || parts == 0)
+    return launch_step([&] { return launch_pdl(grad_norm_kernel, 1, kThreads, 0, s, a.scratch, parts, a.norm); });
+  for (int next = 0; next < a.n;) {
+    const uint32_t units = fill(t, a, &next);
+    if (!units) break;
+    const unsigned grid = ctas_for(units);
+    const int e = launch_step([&] {
+      return launch_pdl(grad_scale_kernel<N>, grid, kThreads, 0, s, t, a.scratch, parts, a.max_norm, a.norm);
+    });
+    if (e) return e;
+  }
+  return ATTNRES_OK;
+}
+
+}  // namespace
+
+int64_t grads_scratch(int n) {
+  const int64_t launches = n < 1 ? 1 : (static_cast<int64_t>(n) - 1) / kMaxTensors + 1;
+  return 3 * kMaxCtas * launches;
+}
+
+int run_grads(const GradArgs& a, cudaStream_t s) {
+  if (a.n <= 32) return run_table<32>(a, s);
+  if (a.n <= 256) return run_table<256>(a, s);
+  return run_table<kMaxTensors>(a, s);
+}
+
+}  // namespace attnres

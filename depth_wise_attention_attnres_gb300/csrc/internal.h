@@ -227,6 +227,69 @@ cudaError_t launch_gupdate(float* G, float* ds, float* dfp, int64_t E, cudaStrea
 cudaError_t launch_spread(float* dst, int64_t dst_stride, int R, const float* g, int64_t E, cudaStream_t s);
 cudaError_t take_timeout_bwd(unsigned int* flag);
 
+// The gated residual and its backward (residual.cu). f == nullptr in the
+// backward leaves the pre-norm's part alone (the backward of RMSNorm).
+struct ResidualArgs {
+  const void* f;        // [T, d]
+  const void* x;        // [T, d] or nullptr
+  const void* gate;     // [ceil(T / gate_rows), d] or nullptr
+  int64_t gate_rows;
+  const float* gpost;   // [d] or nullptr: no post-norm
+  const float* gpre;    // [d] or nullptr: no normed
+  float eps_post, eps_pre, scale;
+  int64_t T;
+  int d;
+  int f_bf16, x_bf16, g_bf16, sigmoid;
+  void* x_out;
+  void* normed;
+};
+struct ResidualBwdArgs {
+  const void* f;
+  const void* gate;
+  int64_t gate_rows;
+  const float* gpost;
+  const void* xo;       // x_out as stored; read with dn only
+  const float* gpre;
+  const void* dxo;      // dL/dx_out or nullptr
+  const void* dn;       // dL/dnormed or nullptr
+  float eps_post, eps_pre, scale;
+  int64_t T;
+  int d;
+  int f_bf16, x_bf16, g_bf16, sigmoid, dx_bf16;  // f_bf16: the type of f, dn and df
+  void* df;             // each output may be nullptr
+  void* dx;
+  void* dgate;
+  float* dgpost;
+  float* dgpre;
+  int accumulate;
+  float* scratch;
+};
+// A launch of the library: its CUDA error, or an injected failure (api.cu).
+int launched_status(cudaError_t (*fn)(void*), void* arg);
+template <typename F>
+int launch_step(F&& f) {
+  return launched_status([](void* p) { return (*static_cast<F*>(p))(); }, &f);
+}
+// Each makes one or more launches and returns an attnres_status.
+int run_residual(const ResidualArgs& a, cudaStream_t s);
+int run_residual_bwd(const ResidualBwdArgs& a, cudaStream_t s);
+int64_t residual_bwd_scratch(int64_t T, int d, int64_t gate_rows);
+
+// The gradient list (grads.cu).
+struct GradArgs {
+  const void* const* grads;
+  const int64_t* counts;
+  const int32_t* dtypes;
+  void* const* outs;          // nullptr: the norm alone
+  const int32_t* out_dtypes;
+  int n;
+  float max_norm;
+  float* norm;
+  float* scratch;
+};
+int run_grads(const GradArgs& a, cudaStream_t s);
+int64_t grads_scratch(int n);
+
 // Failure-path test hooks (api.cu), off by default. Which producer, if any,
 // withholds a copy: the tile index to leave unissued, or -1.
 enum WithholdKernel { kWithholdNone = 0, kWithholdFull = 1, kWithholdStage1Tc = 2, kWithholdMerge = 3 };
@@ -247,10 +310,10 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 // Launch with programmatic stream serialization (see pdl_wait in common.cuh).
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, int smem,
-                       cudaStream_t s, Args&&... args) {
+cudaError_t launch_pdl_grid(void (*kernel)(KArgs...), dim3 grid, unsigned block, int smem,
+                            cudaStream_t s, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
@@ -260,6 +323,11 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, int smem,
+                       cudaStream_t s, Args&&... args) {
+  return launch_pdl_grid(kernel, dim3(grid), block, smem, s, std::forward<Args>(args)...);
 }
 
 }  // namespace attnres

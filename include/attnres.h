@@ -173,6 +173,149 @@ int attnres_rmsnorm(const void* x, int64_t T, int32_t d, int32_t dtype, const fl
                     float eps, void* out, void* stream);
 
 /*
+ * attnres_gated_residual - what lies between a sublayer's output f and the
+ * next sublayer's input: the norm after the sublayer, its gate, the residual
+ * scale, the addition to the stream and the next sublayer's pre-norm, in one
+ * pass over the rows:
+ *
+ *   y[t, k]      = gamma_post[k] f[t, k] / sqrt(mean_k f[t, k]^2 + eps_post)
+ *   x_out[t, k]  = x[t, k] + scale * act(gate[t / gate_rows, k]) * y[t, k]
+ *   normed[t, k] = gamma_pre[k] x_out[t, k] / sqrt(mean_k x_out[t, k]^2 + eps_pre)
+ *
+ * all in fp32, x_out and normed each rounded once (normed from the fp32 row,
+ * before x_out is rounded, as in the pre-norm epilogues). With x NULL the
+ * result is the sublayer's AttnRes source itself; with x an fp32 running sum
+ * of a block it is the sum advanced by the sublayer.
+ *
+ *   f           device, [T, d] of dtype: the sublayer's output.
+ *   x           device, [T, d] of x_dtype: the stream, or NULL (x = 0).
+ *   gamma_post  device, fp32 [d], or NULL: no post-norm (y = f).
+ *   gate        device, [ceil(T / gate_rows), d] of gate_dtype, or NULL (1).
+ *               Token t takes row t / gate_rows: gate_rows 1 is a gate per
+ *               token, gate_rows >= T one row for all of them (a learned gain
+ *               per feature), anything between one row per run of tokens (the
+ *               last run may be short).
+ *   gate_rows   >= 1 (not looked at without a gate).
+ *   gate_act    ATTNRES_GATE_IDENTITY, or ATTNRES_GATE_SIGMOID: 1/(1+exp(-g)).
+ *   scale       host, finite.
+ *   x_out       device, [T, d] of x_dtype; may be x (in place).
+ *   gamma_pre   device, fp32 [d], and normed, device, [T, d] of dtype: both
+ *               given, or both NULL (no pre-norm).
+ *   dtype BF16 takes x_dtype BF16 or F32; dtype F32 takes x_dtype F32. The
+ *   gate may be of either type.
+ * Outputs overlap nothing but, for x_out, x itself. Rows whose squares
+ * overflow fp32 (elements of about 1e19) are outside what RMSNorm computes
+ * here, as in attnres_rmsnorm. Any d >= 1; d a multiple of 8 up to 8192 with
+ * 16-byte aligned pointers takes the fast kernel.
+ */
+typedef enum { ATTNRES_GATE_IDENTITY = 0, ATTNRES_GATE_SIGMOID = 1 } attnres_gate_act;
+
+int attnres_gated_residual(const void* f, const void* x, const float* gamma_post, float eps_post,
+                           const void* gate, int64_t gate_rows, int32_t gate_dtype,
+                           int32_t gate_act, float scale, int64_t T, int32_t d, int32_t dtype,
+                           int32_t x_dtype, void* x_out, const float* gamma_pre, float eps_pre,
+                           void* normed, void* stream);
+
+/*
+ * attnres_gated_residual_bwd - its gradients, given dL/dx_out and dL/dnormed.
+ * With r = 1/sqrt(mean(x_out^2) + eps_pre), u = r x_out, q = r_f f (r_f the
+ * same of f; q = f without a post-norm), h = gamma_pre dnormed and, per token,
+ * <a> the mean over features:
+ *   D          = dx_out + r (h - u <h u>)                   dL/dx = D
+ *   dy         = scale act(gate) D
+ *   df         = r_f (gamma_post dy - q <gamma_post dy q>)  (dy without a post-norm)
+ *   dgate      = sum over the row's tokens of scale act'(gate) gamma_post q D
+ *   dgamma_post = sum_t dy q,   dgamma_pre = sum_t dnormed u.
+ * Everything is recomputed from f, the gate and the stored x_out: the forward
+ * keeps nothing else.
+ *
+ *   f, gamma_post, eps_post, gate, gate_rows, gate_dtype, gate_act, scale, T,
+ *   d, dtype, x_dtype, gamma_pre, eps_pre   as the forward's.
+ *   x_out      device, [T, d] of x_dtype, as the forward left it. Read only
+ *              with dnormed; may be NULL without.
+ *   dx_out     device, [T, d] of dx_dtype, or NULL (0): dL/dx_out by every way
+ *              other than normed.
+ *   dnormed    device, [T, d] of dtype, or NULL (0; gamma_pre is then not
+ *              looked at). dx_out or dnormed must be given.
+ *   dx_dtype   F32, or with dtype BF16 also BF16.
+ *   df         device, [T, d] of dtype, or NULL (not wanted).
+ *   dx         device, [T, d] of dx_dtype, or NULL; may be dx_out (in place).
+ *   dgate      device, like gate, or NULL: written (not added to), summed over
+ *              its tokens in fp32 and rounded once.
+ *   dgamma_post, dgamma_pre   device, fp32 [d], or NULL: added to, or with
+ *              accumulate 0 written. Without a post-norm (dnormed) the
+ *              dgamma_post (dgamma_pre) gradient is zero.
+ *   scratch    device, fp32, at least attnres_gated_residual_bwd_scratch_floats
+ *              floats; need not be initialised, contents on return unspecified.
+ *              Calls that may overlap on the GPU need scratches of their own.
+ * Sums run in a fixed order: the same call gives the same bits. Outputs
+ * overlap nothing but, for dx, dx_out itself. T == 0 launches nothing unless
+ * accumulate is 0, which writes zeros to the gains' gradients.
+ */
+int attnres_gated_residual_bwd(const void* f, const float* gamma_post, float eps_post,
+                               const void* gate, int64_t gate_rows, int32_t gate_dtype,
+                               int32_t gate_act, float scale, int64_t T, int32_t d, int32_t dtype,
+                               int32_t x_dtype, const void* x_out, const float* gamma_pre,
+                               float eps_pre, const void* dx_out, int32_t dx_dtype,
+                               const void* dnormed, void* df, void* dx, void* dgate,
+                               float* dgamma_post, float* dgamma_pre, int32_t accumulate,
+                               float* scratch, int64_t scratch_floats, void* stream);
+/* Scratch the call above needs, in floats; -1 for bad sizes (gate_rows 1 without a gate). */
+int64_t attnres_gated_residual_bwd_scratch_floats(int64_t T, int32_t d, int64_t gate_rows);
+
+/*
+ * attnres_rmsnorm_bwd - gradients of attnres_rmsnorm, and of the pre-norm of
+ * any *_prenorm call with respect to the row it normalised (x: the stored z):
+ *   dx = dres + r (h - u <h u>),  h = gamma dy, u = r x;   dgamma = sum_t dy u.
+ *
+ *   x, dy      device, [T, d] of dtype.
+ *   dres       device, [T, d] of dx_dtype, or NULL (0): the gradient of x by
+ *              its other uses (attnres_full_bwd's dV slice, for one).
+ *   dx         device, [T, d] of dx_dtype; may be dres (in place).
+ *   dgamma     device, fp32 [d], or NULL: added to, or with accumulate 0
+ *              written.
+ *   dx_dtype, scratch, overlaps and T == 0   as attnres_gated_residual_bwd.
+ */
+int attnres_rmsnorm_bwd(const void* x, int64_t T, int32_t d, int32_t dtype, const float* gamma,
+                        float eps, const void* dy, const void* dres, int32_t dx_dtype, void* dx,
+                        float* dgamma, int32_t accumulate, float* scratch, int64_t scratch_floats,
+                        void* stream);
+int64_t attnres_rmsnorm_bwd_scratch_floats(int64_t T, int32_t d);
+
+/*
+ * attnres_grad_norm / attnres_grad_clip - the global norm of a list of
+ * gradients, norm = sqrt(sum over all elements of all tensors of g^2), and the
+ * list scaled so that its norm is at most max_norm:
+ *   out_i = c g_i,  c = max_norm / norm if max_norm < norm < inf, else 1.
+ * A norm that is not finite thus changes no gradient and is there to be read.
+ *
+ *   grads      host array of n device pointers: tensor i holds counts[i]
+ *              consecutive elements of dtypes[i] (each F32 or BF16).
+ *   counts, dtypes   host arrays; counts[i] >= 0 (0: grads[i] not looked at).
+ *   n          >= 0. The host arrays are read before the call returns.
+ *   outs, out_dtypes   host arrays like grads and dtypes: where the scaled
+ *              tensors go (all elements are written; outs[i] may be grads[i]
+ *              with the same type). outs NULL: in place; with c = 1 nothing is
+ *              then written. Outputs overlap no gradient but their own and no
+ *              other output, so a tensor is listed once.
+ *   max_norm   host, >= 0 (may be infinite: the norm alone, or a conversion).
+ *   norm       device, fp32 [1]: the norm before clipping.
+ *   scratch    device, fp32, at least attnres_grad_norm_scratch_floats(n)
+ *              floats; as for attnres_gated_residual_bwd.
+ * The squares are summed in fp32, per thread and in three scales, and the
+ * parts in fp64, in a fixed order: the norm is right for gradients anywhere in
+ * fp32's normal range, also where g^2 would overflow or vanish, and the same
+ * call gives the same bits. attnres_grad_norm may list a tensor twice; it then
+ * counts twice. Tensors of 16-byte aligned storage stream fastest.
+ */
+int attnres_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes,
+                      int32_t n, float* norm, float* scratch, int64_t scratch_floats, void* stream);
+int attnres_grad_clip(const void* const* grads, const int64_t* counts, const int32_t* dtypes,
+                      void* const* outs, const int32_t* out_dtypes, int32_t n, float max_norm,
+                      float* norm, float* scratch, int64_t scratch_floats, void* stream);
+int64_t attnres_grad_norm_scratch_floats(int32_t n);
+
+/*
  * attnres_full_bwd - backward of one read over V[0 .. n_src): given
  * dz = dL/dz of its result, ADD the gradients with respect to the sources,
  * the query and the key-norm gain into dV, dw and dgamma. The read is
