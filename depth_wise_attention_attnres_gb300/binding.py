@@ -680,7 +680,7 @@ def attnres_test_fail_launch(after: int) -> int:
 
 
 # Kernels whose copy producer attnres_test_withhold_stage can starve.
-WITHHOLD_NONE, WITHHOLD_FULL, WITHHOLD_STAGE1_TC, WITHHOLD_MERGE = 0, 1, 2, 3
+WITHHOLD_NONE, WITHHOLD_FULL, WITHHOLD_STAGE1_TC, WITHHOLD_MERGE, WITHHOLD_RESIDUAL = 0, 1, 2, 3, 4
 
 
 def attnres_test_withhold_stage(kernel: int, index: int = 0) -> None:

@@ -1170,15 +1170,16 @@ int attnres_device_status(void* stream) {
     cudaGetLastError();
     return ATTNRES_ERR_CUDA;
   }
-  unsigned int f1 = 0, f2 = 0, f3 = 0, f4 = 0, f5 = 0, f6 = 0, f7 = 0, f8 = 0;
+  unsigned int f1 = 0, f2 = 0, f3 = 0, f4 = 0, f5 = 0, f6 = 0, f7 = 0, f8 = 0, f9 = 0;
   if (take_timeout_full(&f1) != cudaSuccess || take_timeout_stage1(&f2) != cudaSuccess ||
       take_timeout_merge(&f3) != cudaSuccess || take_timeout_stage1tc(&f4) != cudaSuccess ||
       take_timeout_bwd(&f5) != cudaSuccess || take_timeout_proj(&f6) != cudaSuccess ||
-      take_timeout_dsplit(&f7) != cudaSuccess || take_timeout_blockbwd(&f8) != cudaSuccess) {
+      take_timeout_dsplit(&f7) != cudaSuccess || take_timeout_blockbwd(&f8) != cudaSuccess ||
+      take_timeout_residual(&f9) != cudaSuccess) {
     cudaGetLastError();
     return ATTNRES_ERR_CUDA;
   }
-  if (f1 || f2 || f3 || f4 || f5 || f6 || f7 || f8) return ATTNRES_ERR_TIMEOUT;
+  if (f1 || f2 || f3 || f4 || f5 || f6 || f7 || f8 || f9) return ATTNRES_ERR_TIMEOUT;
   e = cudaGetLastError();
   return e == cudaSuccess ? ATTNRES_OK : ATTNRES_ERR_CUDA;
 }
@@ -1188,7 +1189,7 @@ int64_t attnres_test_fail_launch(int64_t after) {
 }
 
 int attnres_test_withhold_stage(int32_t kernel, int64_t index) {
-  if (kernel < kWithholdNone || kernel > kWithholdMerge || (kernel != kWithholdNone && index < 0))
+  if (kernel < kWithholdNone || kernel > kWithholdResidual || (kernel != kWithholdNone && index < 0))
     return ATTNRES_ERR_INVALID_ARG;
   g_withhold_index.store(kernel == kWithholdNone ? -1 : index);
   g_withhold_kernel.store(kernel);

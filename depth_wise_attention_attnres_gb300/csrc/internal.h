@@ -292,7 +292,7 @@ int64_t grads_scratch(int n);
 
 // Failure-path test hooks (api.cu), off by default. Which producer, if any,
 // withholds a copy: the tile index to leave unissued, or -1.
-enum WithholdKernel { kWithholdNone = 0, kWithholdFull = 1, kWithholdStage1Tc = 2, kWithholdMerge = 3 };
+enum WithholdKernel { kWithholdNone = 0, kWithholdFull = 1, kWithholdStage1Tc = 2, kWithholdMerge = 3, kWithholdResidual = 4 };
 int64_t withhold_for(WithholdKernel k);
 
 // Device-side timeout records of each kernel file: read and clear (blocking).
@@ -300,6 +300,7 @@ cudaError_t take_timeout_full(unsigned int* flag);
 cudaError_t take_timeout_stage1(unsigned int* flag);
 cudaError_t take_timeout_merge(unsigned int* flag);
 cudaError_t take_timeout_stage1tc(unsigned int* flag);
+cudaError_t take_timeout_residual(unsigned int* flag);
 
 // Shared launch helpers (api.cu).
 int sm_count();

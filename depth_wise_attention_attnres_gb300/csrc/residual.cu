@@ -16,6 +16,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "residual.cuh"
 
 namespace attnres {
 namespace {
@@ -34,14 +35,6 @@ __device__ __forceinline__ void st(void* p, int64_t i, int is_bf16, float v) {
   else
     static_cast<float*>(p)[i] = v;
 }
-// sigmoid(g) and its slope from e = exp(-|g|), which neither overflows nor
-// loses the small factor of the slope e / (1 + e)^2 to cancellation.
-__device__ __forceinline__ float sigmoid(float g, float* slope) {
-  const float e = expf(-fabsf(g)), r = 1.0f / (1.0f + e);
-  *slope = e * r * r;
-  return g < 0.f ? e * r : r;
-}
-
 // Sums of a CTA of kThreads threads; every thread gets them.
 template <int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* red) {
@@ -267,26 +260,30 @@ __global__ void __launch_bounds__(kThreads) residual_bwd_rows_kernel(ResidualBwd
       if (!a.f) continue;
       const float gp = post_gain(a, k);
       if (a.df) st(a.df, row + k, a.f_bf16, a.gpost ? r.rf * (gp * g.dy - g.q * r.mf) : g.dy);
-      if (a.dgate && a.gate_rows == 1 && a.T > 1) st(a.dgate, row + k, a.g_bf16, a.scale * slope * gp * g.q * g.D);
+      if (a.dgate && a.gate_rows == 1) st(a.dgate, row + k, a.g_bf16, a.scale * slope * gp * g.q * g.D);
     }
   }
 }
 
-// The last step of the sums over tokens: the partial rows added in order, one
-// thread per feature and kind.
-__global__ void __launch_bounds__(kThreads)
+// The last step of the sums over tokens: the partial rows of each kind added in
+// a fixed order, kLanes runs of them at once per feature.
+__global__ void __launch_bounds__(kColumns* kLanes)
     residual_bwd_reduce_kernel(ResidualBwdArgs a, const float* part, int parts, int gate_too) {
+  __shared__ float red[kLanes][kColumns];
   pdl_trigger();
   pdl_wait();
-  const int which = blockIdx.y;
+  const int which = blockIdx.y, col = threadIdx.x % kColumns, lane = threadIdx.x / kColumns;
   float* const gain = which == 0 ? a.dgpost : a.dgpre;
   if (which < 2 ? gain == nullptr : !gate_too) return;
-  const int64_t k = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (k >= a.d) return;
+  const int64_t k = static_cast<int64_t>(blockIdx.x) * kColumns + col;
   float s = 0.f;
-  // Without a post-norm gamma_post has no part in anything.
-  if (which != 0 || a.gpost)
-    for (int p = 0; p < parts; ++p) s += part[(static_cast<int64_t>(which) * parts + p) * a.d + k];
+  // Without the norm its gain has no part in anything.
+  if (k < a.d && (which != 0 || a.gpost) && (which != 1 || a.dn))
+    for (int p = lane; p < parts; p += kLanes) s += part[(static_cast<int64_t>(which) * parts + p) * a.d + k];
+  red[lane][col] = s;
+  __syncthreads();
+  if (lane != 0 || k >= a.d) return;
+  for (int j = 1; j < kLanes; ++j) s += red[j][col];
   if (which == 2)
     st(a.dgate, k, a.g_bf16, s);
   else
@@ -298,14 +295,19 @@ unsigned row_grid(int64_t T) {
   return static_cast<unsigned>(T < cap ? T : cap);
 }
 
-// Whether all tokens share one gate row (its gradient is then summed with the
-// gains' gradients).
-bool one_gate_row(const ResidualBwdArgs& a) { return a.gate && a.gate_rows >= a.T; }
+int run_reduce(const ResidualBwdArgs& a, const float* part, int parts, cudaStream_t s) {
+  const bool gate_sum = residual_bwd_sums_gate(a) && parts > 0;
+  if (!a.dgpost && !a.dgpre && !gate_sum) return ATTNRES_OK;
+  return launch_step([&] {
+    return launch_pdl_grid(residual_bwd_reduce_kernel, dim3((a.d - 1) / kColumns + 1, gate_sum ? 3 : 2),
+                           kColumns * kLanes, 0, s, a, part, parts, static_cast<int>(gate_sum));
+  });
+}
 
 int run_bwd_generic(const ResidualBwdArgs& a, cudaStream_t s) {
   RowStats* stats = reinterpret_cast<RowStats*>(a.scratch);
   float* part = a.scratch + 4 * a.T;
-  const bool gate_sum = a.dgate && one_gate_row(a);
+  const bool gate_sum = residual_bwd_sums_gate(a);
   const int chunks = static_cast<int>(a.T < kChunks ? a.T : kChunks);
   const int column_blocks = (a.d - 1) / kColumns + 1;
   int e = 0;
@@ -327,24 +329,32 @@ int run_bwd_generic(const ResidualBwdArgs& a, cudaStream_t s) {
     if (!e && (a.dx || a.df || (a.dgate && a.gate_rows == 1)))
       e = launch_step([&] { return launch_pdl(residual_bwd_rows_kernel, row_grid(a.T), kThreads, 0, s, a, stats); });
   }
-  if (!e && (a.dgpost || a.dgpre || gate_sum) && (a.T > 0 || !a.accumulate))
-    e = launch_step([&] {
-      return launch_pdl_grid(residual_bwd_reduce_kernel, dim3((a.d - 1) / kThreads + 1, 3), kThreads, 0, s, a, part,
-                             a.T > 0 ? chunks : 0, static_cast<int>(gate_sum));
-    });
+  if (!e && (a.T > 0 || !a.accumulate)) e = run_reduce(a, part, chunks, s);
+  return e;
+}
+
+int run_bwd_fast(const ResidualBwdArgs& a, cudaStream_t s) {
+  int e = launch_step([&] { return launch_residual_bwd_fast(a, s); });
+  if (!e && residual_bwd_shares_gates(a)) e = launch_step([&] { return launch_residual_bwd_join_gate(a, s); });
+  if (!e) e = run_reduce(a, a.scratch, residual_bwd_parts(a), s);
   return e;
 }
 
 }  // namespace
 
 int run_residual(const ResidualArgs& a, cudaStream_t s) {
+  if (residual_fast_ok(a)) return launch_step([&] { return launch_residual_fast(a, s); });
   return launch_step([&] { return launch_pdl(residual_generic_kernel, row_grid(a.T), kThreads, 0, s, a); });
 }
 
-int run_residual_bwd(const ResidualBwdArgs& a, cudaStream_t s) { return run_bwd_generic(a, s); }
+int run_residual_bwd(const ResidualBwdArgs& a, cudaStream_t s) {
+  return residual_bwd_fast_ok(a) ? run_bwd_fast(a, s) : run_bwd_generic(a, s);
+}
 
-int64_t residual_bwd_scratch(int64_t T, int d, int64_t /*gate_rows*/) {
-  return 4 * T + 3 * (T < kChunks ? T : int64_t{kChunks}) * d;
+int64_t residual_bwd_scratch(int64_t T, int d, int64_t gate_rows) {
+  const int64_t generic = 4 * T + 3 * (T < kChunks ? T : int64_t{kChunks}) * d;
+  const int64_t fast = residual_bwd_fast_scratch(T, d, gate_rows);
+  return generic > fast ? generic : fast;
 }
 
 }  // namespace attnres

@@ -670,7 +670,8 @@ int64_t attnres_test_fail_launch(int64_t after);
  * Full-read bulk kernel (index counts the (tile, source) copies of each CTA),
  * 2 = the tensor-core stage 1 (index counts each CTA's tiles), 3 = the tiled
  * merge (index counts each CTA's tiles; tiles fetched before the previous
- * kernel finishes, in a Block pass, are never withheld). Every CTA with more
+ * kernel finishes, in a Block pass, are never withheld), 4 = the gated residual
+ * and its backward (index counts each team's rows). Every CTA (4: team) with more
  * than `index` copies withholds its copy number `index`; its other copies are
  * issued and waited for before the CTA exits. Stays set until changed.
  * Returns ATTNRES_ERR_INVALID_ARG for an unknown kernel or a negative index.

@@ -370,3 +370,26 @@ def test_rows_past_32_bit_offsets():
     ref.check(dx[-tail:], vals["dx"], bounds["dx"], "dx")
     ref.check(dgamma, vals["dgamma_pre"], bounds["dgamma_pre"], "dgamma_pre")
     assert (dx[:-tail] == 0).all()
+
+
+def test_withheld_row_times_out_and_recovers():
+    # 900 rows of 640 over at most 760 teams: every team has one row or two, each withholds its first.
+    c = Case(900, 640, gate_rows=100, gate_type="f32")
+    good = c.outputs()
+    c.forward()
+    c.backward(good)
+    want = c.xo.clone()
+    assert ar.attnres_device_status() == 0
+    for run in (c.forward, lambda: c.backward(c.outputs())):
+        ar.attnres_test_withhold_stage(ar.WITHHOLD_RESIDUAL, 0)
+        try:
+            run()
+        finally:
+            ar.attnres_test_withhold_stage(ar.WITHHOLD_NONE)
+        assert ar.attnres_device_status() == 4          # ATTNRES_ERR_TIMEOUT
+        assert ar.attnres_device_status() == 0
+        c.xo.copy_(want)
+    again = c.outputs()
+    c.forward()
+    c.backward(again)
+    assert torch.equal(c.xo, want) and all(torch.equal(again[k], good[k]) for k in good)
