@@ -22,9 +22,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libattnres.so")
 
 SOURCES = ["api.cu", "full_fwd.cu", "stage1.cu", "merge.cu", "generic.cu", "noalloc.cu",
-           "stage1_tc.cu", "full_bwd.cu", "proj.cu", "dsplit.cu", "block_bwd.cu", "residual.cu", "residual_fast.cu",
-           "grads.cu"]
-HEADERS = ["common.cuh", "internal.h", "residual.cuh"]
+           "stage1_tc.cu", "full_bwd.cu", "proj.cu", "dsplit.cu", "block_bwd.cu", "residual.cu", "residual_fwd.cu",
+           "residual_bwd.cu", "grads.cu"]
+HEADERS = ["common.cuh", "internal.h", "residual.cuh", "residual_team.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

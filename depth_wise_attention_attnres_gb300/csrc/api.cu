@@ -1170,16 +1170,16 @@ int attnres_device_status(void* stream) {
     cudaGetLastError();
     return ATTNRES_ERR_CUDA;
   }
-  unsigned int f1 = 0, f2 = 0, f3 = 0, f4 = 0, f5 = 0, f6 = 0, f7 = 0, f8 = 0, f9 = 0;
+  unsigned int f1 = 0, f2 = 0, f3 = 0, f4 = 0, f5 = 0, f6 = 0, f7 = 0, f8 = 0, f9 = 0, f10 = 0;
   if (take_timeout_full(&f1) != cudaSuccess || take_timeout_stage1(&f2) != cudaSuccess ||
       take_timeout_merge(&f3) != cudaSuccess || take_timeout_stage1tc(&f4) != cudaSuccess ||
       take_timeout_bwd(&f5) != cudaSuccess || take_timeout_proj(&f6) != cudaSuccess ||
       take_timeout_dsplit(&f7) != cudaSuccess || take_timeout_blockbwd(&f8) != cudaSuccess ||
-      take_timeout_residual(&f9) != cudaSuccess) {
+      take_timeout_residual_fwd(&f9) != cudaSuccess || take_timeout_residual_bwd(&f10) != cudaSuccess) {
     cudaGetLastError();
     return ATTNRES_ERR_CUDA;
   }
-  if (f1 || f2 || f3 || f4 || f5 || f6 || f7 || f8 || f9) return ATTNRES_ERR_TIMEOUT;
+  if (f1 || f2 || f3 || f4 || f5 || f6 || f7 || f8 || f9 || f10) return ATTNRES_ERR_TIMEOUT;
   e = cudaGetLastError();
   return e == cudaSuccess ? ATTNRES_OK : ATTNRES_ERR_CUDA;
 }

@@ -300,7 +300,8 @@ cudaError_t take_timeout_full(unsigned int* flag);
 cudaError_t take_timeout_stage1(unsigned int* flag);
 cudaError_t take_timeout_merge(unsigned int* flag);
 cudaError_t take_timeout_stage1tc(unsigned int* flag);
-cudaError_t take_timeout_residual(unsigned int* flag);
+cudaError_t take_timeout_residual_fwd(unsigned int* flag);
+cudaError_t take_timeout_residual_bwd(unsigned int* flag);
 
 // Shared launch helpers (api.cu).
 int sm_count();

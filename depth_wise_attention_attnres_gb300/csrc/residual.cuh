@@ -7,11 +7,23 @@
 namespace attnres {
 
 // sigmoid(g) and its slope from e = exp(-|g|), which neither overflows nor
-// loses the small factor of the slope e / (1 + e)^2 to cancellation.
+// loses the small factor of the slope e / (1 + e)^2 to cancellation. e is the
+// square of 2^(t/2), t = -|g| log2(e) in two parts (the second one's power to
+// first order), so that the result may be subnormal where 2^(t/2) is not;
+// e^-110 is 0 in fp32. Within 10 x 2^-24 of the exact value, relative.
 __device__ __forceinline__ float sigmoid(float g, float* slope) {
-  const float e = expf(-fabsf(g)), r = 1.0f / (1.0f + e);
-  *slope = e * r * r;
-  return g < 0.f ? e * r : r;
+  float m = fabsf(g);
+  m = m > 110.f ? 110.f : m;  // a NaN stays
+  const float t = m * -0.72134752f;                      // -log2(e) / 2
+  const float rest = fmaf(m, -0.72134752f, -t) - m * 9.62981e-9f;  // and what fp32 leaves of it
+  float y, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
+  y = fmaf(y, rest * 0.69314718f, y);
+  const float e = y * y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  const float er = e * r;
+  *slope = er * r;
+  return g < 0.f ? er : r;
 }
 
 // Whether runs of tokens, but not all of them, share gate rows whose gradient
@@ -23,7 +35,7 @@ inline bool residual_bwd_sums_gate(const ResidualBwdArgs& a) {
   return a.dgate && a.gate_rows > 1 && a.gate_rows >= a.T;
 }
 
-// residual_fast.cu
+// residual_fwd.cu, residual_bwd.cu
 bool residual_fast_ok(const ResidualArgs& a);
 bool residual_bwd_fast_ok(const ResidualBwdArgs& a);
 int64_t residual_bwd_fast_scratch(int64_t T, int d, int64_t gate_rows);
