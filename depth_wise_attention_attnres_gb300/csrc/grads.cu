@@ -2,8 +2,8 @@
 //
 // norm = sqrt(sum g^2) over every element of every tensor; clipping multiplies
 // by max_norm / norm where norm exceeds max_norm. Two launches either way: the
-// first leaves one partial sum per CTA, the second adds them (in fp64, in a
-// fixed order, every CTA for itself) and writes the norm, or the norm and the
+// first leaves one partial sum per CTA, the second adds them (in a fixed
+// order, every CTA for itself) and writes the norm, or the norm and the
 // scaled tensors. Bound by memory: the norm reads every gradient once, the
 // scaling reads them again and writes them.
 //
@@ -41,8 +41,26 @@ struct Table {
   int n;
 };
 
+// Sums of squares of g, g 2^-80 and g 2^80. A batch of loads is summed from
+// zero and then added to the thread's total, whose rounding is kept and added at
+// the end (total >= batch but for the first ones): small gradients are not lost
+// behind large ones, and a total that overflowed stays infinite.
 struct Sums {
   float2 mid, big, small;
+};
+struct Total {
+  float s[3] = {0.f, 0.f, 0.f}, rest[3] = {0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(const Sums& b) {
+    const float v[3] = {b.mid.x + b.mid.y, b.big.x + b.big.y, b.small.x + b.small.y};
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const float t = s[i] + v[i];
+      rest[i] += (s[i] - t) + v[i];
+      s[i] = t;
+    }
+  }
+  // After an overflow the rest is not a number.
+  __device__ __forceinline__ float value(int i) const { return isfinite(s[i]) ? s[i] + rest[i] : s[i]; }
 };
 
 __device__ __forceinline__ void add2(Sums& s, float2 x) {
@@ -71,10 +89,9 @@ __device__ __forceinline__ int64_t head_of(const T* p, int64_t n) {
 }
 
 template <typename T>
-__device__ __forceinline__ void sum_segment(Sums& s, const T* p, int64_t n) {
+__device__ __forceinline__ void sum_segment(Total& total, const T* p, int64_t n) {
   constexpr int kV = 16 / sizeof(T), kU = 8;
   const int64_t head = head_of(p, n);
-  if (threadIdx.x < head) add2(s, make_float2(to_f32(p[threadIdx.x]), 0.f));
   const uint4* v = reinterpret_cast<const uint4*>(p + head);
   const int64_t nv = (n - head) / kV;
   int64_t i = threadIdx.x;
@@ -82,11 +99,16 @@ __device__ __forceinline__ void sum_segment(Sums& s, const T* p, int64_t n) {
     uint4 x[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) x[u] = v[i + u * kThreads];
+    Sums s{};
 #pragma unroll
     for (int u = 0; u < kU; ++u) add_vec(s, p, x[u]);
+    total.add(s);
   }
+  Sums s{};
+  if (threadIdx.x < head) add2(s, make_float2(to_f32(p[threadIdx.x]), 0.f));
   for (; i < nv; i += kThreads) add_vec(s, p, v[i]);
   for (int64_t k = head + nv * kV + threadIdx.x; k < n; k += kThreads) add2(s, make_float2(to_f32(p[k]), 0.f));
+  total.add(s);
 }
 
 // Runs fn(tensor, first element, elements) over the CTA's share of the units.
@@ -110,64 +132,55 @@ __device__ __forceinline__ void for_segments(const Table<N>& t, F&& fn) {
   }
 }
 
-__device__ __forceinline__ double warp_sum_f64(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// Sums over the CTA; every thread gets them.
-__device__ __forceinline__ void block_sum3(double (&v)[3], double* red) {
+// Sums over the CTA; every thread gets them. (All in fp32: a tree of positive
+// terms is within its depth x 2^-24, and the fp64 units of this GPU are few.)
+__device__ __forceinline__ void block_sum3(float (&v)[3], float (*red)[3]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    v[i] = warp_sum_f64(v[i]);
-    if (lane == 0) red[warp * 3 + i] = v[i];
+    v[i] = warp_sum(v[i]);
+    if (lane == 0) red[warp][i] = v[i];
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    v[i] = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w) v[i] += red[w * 3 + i];
-  }
+  for (int i = 0; i < 3; ++i) v[i] = warp_sum(lane < kThreads / 32 ? red[lane][i] : 0.f);
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) grad_sums_kernel(const __grid_constant__ Table<N> t, float* part) {
-  __shared__ double red[3 * kThreads / 32];
+  __shared__ float red[kThreads / 32][3];
   pdl_trigger();
   pdl_wait();
-  Sums s{};
+  Total s;
   for_segments(t, [&](int i, int64_t a, int64_t n) {
     if (t.kind[i] & 1)
       sum_segment(s, static_cast<const bf16*>(t.src[i]) + a, n);
     else
       sum_segment(s, static_cast<const float*>(t.src[i]) + a, n);
   });
-  double v[3] = {static_cast<double>(s.mid.x) + s.mid.y, static_cast<double>(s.big.x) + s.big.y,
-                 static_cast<double>(s.small.x) + s.small.y};
+  float v[3] = {s.value(0), s.value(1), s.value(2)};
   block_sum3(v, red);
-  if (threadIdx.x < 3) part[3 * blockIdx.x + threadIdx.x] = static_cast<float>(v[threadIdx.x]);
+  if (threadIdx.x < 3) part[3 * blockIdx.x + threadIdx.x] = threadIdx.x == 0 ? v[0] : (threadIdx.x == 1 ? v[1] : v[2]);
 }
 
 // The norm from the partial sums (the same bits in every CTA).
-__device__ __forceinline__ double norm_of(const float* part, int parts, double* red) {
-  double v[3] = {0.0, 0.0, 0.0};
+__device__ __forceinline__ float norm_of(const float* part, int parts, float (*red)[3]) {
+  float v[3] = {0.f, 0.f, 0.f};
   for (int p = threadIdx.x; p < parts; p += kThreads)
 #pragma unroll
     for (int i = 0; i < 3; ++i) v[i] += part[3 * p + i];
   block_sum3(v, red);
-  if (isinf(v[0])) return sqrt(v[1]) * 0x1p80;
-  if (v[0] < 0x1p-60) return sqrt(v[2]) * 0x1p-80;
-  return sqrt(v[0]);
+  if (isinf(v[0])) return sqrtf(v[1]) * 0x1p80f;
+  if (v[0] < 0x1p-60f) return sqrtf(v[2]) * 0x1p-80f;
+  return sqrtf(v[0]);
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const float* part, int parts, float* norm) {
-  __shared__ double red[3 * kThreads / 32];
+  __shared__ float red[kThreads / 32][3];
   pdl_trigger();
   pdl_wait();
-  const double r = norm_of(part, parts, red);
-  if (threadIdx.x == 0) norm[0] = static_cast<float>(r);
+  const float r = norm_of(part, parts, red);
+  if (threadIdx.x == 0) norm[0] = r;
 }
 
 template <typename T>
@@ -224,10 +237,10 @@ __device__ __forceinline__ void scale_segment(const TI* src, TO* dst, int64_t n,
 template <int N>
 __global__ void __launch_bounds__(kThreads)
     grad_scale_kernel(const __grid_constant__ Table<N> t, const float* part, int parts, float max_norm, float* norm) {
-  __shared__ double red[3 * kThreads / 32];
+  __shared__ float red[kThreads / 32][3];
   pdl_trigger();
   pdl_wait();
-  const float r = static_cast<float>(norm_of(part, parts, red));
+  const float r = norm_of(part, parts, red);
   if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = r;
   const float c = (r > max_norm && r < INFINITY) ? max_norm / r : 1.0f;
   for_segments(t, [&](int i, int64_t a, int64_t n) {

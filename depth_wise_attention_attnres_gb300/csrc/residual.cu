@@ -266,24 +266,28 @@ __global__ void __launch_bounds__(kThreads) residual_bwd_rows_kernel(ResidualBwd
 }
 
 // The last step of the sums over tokens: the partial rows of each kind added in
-// a fixed order, kLanes runs of them at once per feature.
-__global__ void __launch_bounds__(kColumns* kLanes)
+// a fixed order, 32 runs of them at once (every 32nd) per feature.
+__global__ void __launch_bounds__(1024)
     residual_bwd_reduce_kernel(ResidualBwdArgs a, const float* part, int parts, int gate_too) {
-  __shared__ float red[kLanes][kColumns];
+  __shared__ float red[32][33];
   pdl_trigger();
   pdl_wait();
-  const int which = blockIdx.y, col = threadIdx.x % kColumns, lane = threadIdx.x / kColumns;
+  const int which = blockIdx.y, x = threadIdx.x & 31, y = threadIdx.x >> 5;
   float* const gain = which == 0 ? a.dgpost : a.dgpre;
   if (which < 2 ? gain == nullptr : !gate_too) return;
-  const int64_t k = static_cast<int64_t>(blockIdx.x) * kColumns + col;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 32;
   float s = 0.f;
   // Without the norm its gain has no part in anything.
-  if (k < a.d && (which != 0 || a.gpost) && (which != 1 || a.dn))
-    for (int p = lane; p < parts; p += kLanes) s += part[(static_cast<int64_t>(which) * parts + p) * a.d + k];
-  red[lane][col] = s;
+  if (first + x < a.d && (which != 0 || a.gpost) && (which != 1 || a.dn)) {
+    const float* p = part + static_cast<int64_t>(which) * parts * a.d + first + x;
+#pragma unroll 5
+    for (int i = y; i < parts; i += 32) s += p[static_cast<int64_t>(i) * a.d];
+  }
+  red[y][x] = s;
   __syncthreads();
-  if (lane != 0 || k >= a.d) return;
-  for (int j = 1; j < kLanes; ++j) s += red[j][col];
+  s = warp_sum(red[x][y]);  // warp y: feature first + y
+  const int64_t k = first + y;
+  if (x != 0 || k >= a.d) return;
   if (which == 2)
     st(a.dgate, k, a.g_bf16, s);
   else
@@ -299,8 +303,8 @@ int run_reduce(const ResidualBwdArgs& a, const float* part, int parts, cudaStrea
   const bool gate_sum = residual_bwd_sums_gate(a) && parts > 0;
   if (!a.dgpost && !a.dgpre && !gate_sum) return ATTNRES_OK;
   return launch_step([&] {
-    return launch_pdl_grid(residual_bwd_reduce_kernel, dim3((a.d - 1) / kColumns + 1, gate_sum ? 3 : 2),
-                           kColumns * kLanes, 0, s, a, part, parts, static_cast<int>(gate_sum));
+    return launch_pdl_grid(residual_bwd_reduce_kernel, dim3((a.d - 1) / 32 + 1, gate_sum ? 3 : 2), 1024, 0,
+                           s, a, part, parts, static_cast<int>(gate_sum));
   });
 }
 

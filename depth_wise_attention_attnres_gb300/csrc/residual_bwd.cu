@@ -9,8 +9,6 @@
 // them, or left in two parts per team for one more kernel. The sums of row r's
 // second mean and of row r + 1's first ones go through the team together, so a
 // row costs one barrier.
-#include <type_traits>
-
 #include "residual_team.cuh"
 
 namespace attnres {
@@ -18,37 +16,43 @@ namespace {
 
 __device__ unsigned int g_timeout = 0;
 
-constexpr int kNormWarps = 32, kGatedWarps = 16;
+// 20 warps of 96 registers, 32 of 64; past d = 5120 the gated kernel's threads
+// take 16 features and 128 registers (a row is then 11 to 16 warps).
+constexpr int kNormWarps = 32, kGatedWarps = 20, kWideWarps = 16;
 int max_warps(const ResidualBwdArgs& a) { return a.f ? kGatedWarps : kNormWarps; }
 
-// act'(gate) of a gate row that tokens share: the one factor of its gradient
-// that is left out of their sum.
-__device__ __forceinline__ V8 shared_slope(const ResidualBwdArgs& a, int64_t group, int k) {
-  V8 gate = ld8(a.gate, group * a.d + k, a.g_bf16), slope;
+// 8 features of a gate row that tokens share: act(gate), and its slope.
+__device__ __forceinline__ V8 shared_act(const ResidualBwdArgs& a, int64_t group, int k, V8& slope) {
+  V8 gate = ld8(a.gate, group * a.d + k, a.g_bf16);
   activate8<true>(gate, slope, a.sigmoid);
-  return slope;
+  return gate;
 }
-// scale * act(gate) of one.
-__device__ __forceinline__ V8 shared_factor(const ResidualBwdArgs& a, int64_t group, int k) {
-  V8 gate = ld8(a.gate, group * a.d + k, a.g_bf16), unused;
-  activate8<false>(gate, unused, a.sigmoid);
-  return mul8(gate, a.scale);
+// scale * gamma_post (1 without a post-norm).
+__device__ __forceinline__ V8 scaled_gain(const ResidualBwdArgs& a, int k) {
+  return a.gpost ? mul8(ld8(a.gpost + k), a.scale) : fill8(a.scale);
 }
 
-// Writes (or keeps, for the kernel that joins them) the sum over the team's
-// tokens of a gate row, at 8 features.
-__device__ __forceinline__ void flush_gate(const ResidualBwdArgs& a, const Team& m, float* shared_part, int teams,
-                                           int64_t group, int k, V8& acc) {
+// The end of a run of tokens that share a gate row, at 8 features, with acc the
+// sum of q D over the team's tokens of it: their part of sum act q D, and the
+// gate row's gradient, slope scale gamma_post acc, written where the team has all
+// of the row's tokens, or kept for the kernel that joins the teams' parts.
+// part nullptr: the gradient is not wanted; all: one row for all tokens (its
+// gradient goes with the other sums over tokens, in acc).
+__device__ __forceinline__ void flush_gate(const ResidualBwdArgs& a, const Team& m, float* part, int teams, bool all,
+                                           int64_t group, int k, V8& acc, V8& post) {
+  V8 slope;
+  post = fma8(shared_act(a, group, k, slope), acc, post);
+  const V8 sum = mul8(mul8(slope, scaled_gain(a, k)), acc);
+  acc = all ? sum : fill8(0.f);
+  if (!part) return;
   const int64_t start = group * a.gate_rows;
   const int64_t end = a.gate_rows < a.T - start ? start + a.gate_rows : a.T;
-  const V8 sum = mul8(acc, shared_slope(a, group, k));
-  acc = fill8(0.f);
   if (start >= m.r0 && end <= m.r0 + m.rows) {
     st8(a.dgate, group * a.d + k, a.g_bf16, sum);
     return;
   }
   const int64_t id = static_cast<int64_t>(blockIdx.x) * teams + m.team;
-  float* part = shared_part + (id * 2 + (start < m.r0 ? 0 : 1)) * a.d + k;
+  part += (id * 2 + (start < m.r0 ? 0 : 1)) * a.d + k;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     part[2 * i] = sum.p[i].x;
@@ -58,11 +62,11 @@ __device__ __forceinline__ void flush_gate(const ResidualBwdArgs& a, const Team&
 
 // A thread's part of a sum over tokens, for its team.
 template <int VPT>
-__device__ __forceinline__ void park(float* buf, const Team& m, int d, const V8 (&t)[VPT]) {
+__device__ __forceinline__ void park(float* buf, const Team& m, int d, const V8 (&t)[VPT], float scale) {
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int k = (v * m.warps * 32 + m.tid) * 8;
-    if (k < d) st8(buf + m.team * d + k, t[v]);
+    if (k < d) st8(buf + m.team * d + k, mul8(t[v], scale));
   }
 }
 
@@ -72,22 +76,14 @@ __device__ __forceinline__ void park(float* buf, const Team& m, int d, const V8 
 template <int VPT>
 __device__ __forceinline__ void write_sums(const ResidualBwdArgs& a, const Team& m, const TeamGeom& g, float* buf,
                                            float* sums, bool with_post, bool with_gate, const V8 (&post)[VPT],
-                                           const V8 (&pre)[VPT], V8 (&gate)[VPT]) {
+                                           const V8 (&pre)[VPT], const V8 (&gate)[VPT]) {
   for (int which = 0; which < 3; ++which) {
     if (which == 0 ? !with_post : (which == 1 ? !(a.dn && a.dgpre) : !with_gate)) continue;
     __syncthreads();
-    if (which == 0) {
-      park(buf, m, a.d, post);
-    } else if (which == 1) {
-      park(buf, m, a.d, pre);
-    } else {
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int k = (v * m.warps * 32 + m.tid) * 8;
-        if (k < a.d) gate[v] = mul8(gate[v], shared_slope(a, 0, k));
-      }
-      park(buf, m, a.d, gate);
-    }
+    if (which == 0)
+      park(buf, m, a.d, post, a.scale);
+    else
+      park(buf, m, a.d, which == 1 ? pre : gate, 1.f);
     __syncthreads();
     float* part = sums + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.d;
     for (int k = threadIdx.x; k < a.d; k += blockDim.x) {
@@ -112,17 +108,18 @@ __global__ void __launch_bounds__((HAS_F ? kGatedWarps : kNormWarps) * 32, 1)
   const int d = a.d, k = m.tid * 8;
   const bool mine = k < d, post_norm = HAS_F && a.gpost != nullptr;
   const float inv_d = 1.0f / static_cast<float>(d);
-  V8 gpost = fill8(1.f), gpre = fill8(0.f);
-  if (mine && post_norm) gpost = ld8(a.gpost + k);
+  // scale * gamma_post, with a shared gate times its value too.
+  V8 gain = mine && HAS_F ? scaled_gain(a, k) : fill8(0.f), gpre = fill8(0.f), slope;
   if (mine && a.dn) gpre = ld8(a.gpre + k);
   // The shared gate row of the current token, and the first token of the next one.
   int64_t group = 0, group_end = a.T;
-  V8 w = fill8(a.scale);  // scale * act(gate)
   if (GATE == kSharedGate) {
     group = m.r0 / a.gate_rows;
     if (a.gate_rows < a.T) group_end = (group + 1) * a.gate_rows;
-    if (mine && m.rows > 0) w = shared_factor(a, group, k);
+    if (mine && m.rows > 0) gain = mul8(gain, shared_act(a, group, k, slope));
   }
+  // Sums over tokens: act q D (dgamma_post / scale), dn u, and of the current
+  // shared gate row q D.
   V8 post[1] = {fill8(0.f)}, pre[1] = {fill8(0.f)}, gsum[1] = {fill8(0.f)};
 
   // Waits for a row and takes its part of sum x^2, sum h x and sum f^2.
@@ -154,7 +151,7 @@ __global__ void __launch_bounds__((HAS_F ? kGatedWarps : kNormWarps) * 32, 1)
     if (GATE == kSharedGate && row == group_end) {
       ++group;
       group_end += a.gate_rows;
-      if (mine) w = shared_factor(a, group, k);
+      if (mine) gain = mul8(scaled_gain(a, k), shared_act(a, group, k, slope));
     }
     const unsigned char* st = m.ring + stage * g.stage_bytes;
     const float rx = a.dn ? rsqrtf(s[0] * inv_d + a.eps_pre) : 0.f, mx = rx * (s[1] * inv_d);
@@ -164,9 +161,9 @@ __global__ void __launch_bounds__((HAS_F ? kGatedWarps : kNormWarps) * 32, 1)
     }
 #pragma unroll
     for (int i = 0; i < kSums; ++i) s[i] = 0.f;
-    V8 D, q, dy, slope;
+    V8 q, t;  // t = gamma_post dy = scale gamma_post act D
     if (mine) {
-      D = a.dxo ? ld8(reinterpret_cast<const G*>(st + g.dxo) + k) : fill8(0.f);
+      V8 D = a.dxo ? ld8(reinterpret_cast<const G*>(st + g.dxo) + k) : fill8(0.f);
       if (a.dn) {
         const V8 x = mul8(ld8(reinterpret_cast<const X*>(st + g.x) + k), rx);
         const V8 h = ld8(reinterpret_cast<const F*>(st + g.dn) + k);
@@ -175,15 +172,20 @@ __global__ void __launch_bounds__((HAS_F ? kGatedWarps : kNormWarps) * 32, 1)
       }
       if (a.dx) st8(static_cast<G*>(a.dx) + row * d + k, D);
       if constexpr (HAS_F) {
-        if (GATE == kTokenGate) {
-          w = ld8(st + g.gate, k, a.g_bf16);
-          activate8<true>(w, slope, a.sigmoid);
-          w = mul8(w, a.scale);
-        }
         q = mul8(ld8(reinterpret_cast<const F*>(st + g.f) + k), rf);
-        dy = mul8(w, D);
-        post[0] = fma8(dy, q, post[0]);
-        s[3] = dot8(mul8(gpost, dy), q);
+        if (GATE == kTokenGate) {
+          V8 act = ld8(st + g.gate, k, a.g_bf16);
+          activate8<true>(act, slope, a.sigmoid);
+          const V8 qD = mul8(q, D);
+          post[0] = fma8(act, qD, post[0]);
+          if (a.dgate) st8(a.dgate, row * d + k, a.g_bf16, mul8(slope, mul8(gain, qD)));
+          t = mul8(mul8(gain, act), D);
+        } else {
+          V8& sum = GATE == kSharedGate ? gsum[0] : post[0];
+          sum = fma8(q, D, sum);
+          t = mul8(gain, D);
+        }
+        s[3] = dot8(t, q);
       }
     }
     if (++stage == m.nst) stage = 0, parity ^= 1u;
@@ -196,34 +198,22 @@ __global__ void __launch_bounds__((HAS_F ? kGatedWarps : kNormWarps) * 32, 1)
     // Every thread has what it needs of row r: its stage is free.
     if (m.tid == 0 && m.issued < m.rows) issue_row(m, g);
     if constexpr (HAS_F) {
-      if (mine) {
-        if (GATE != kNoGate) {
-          const V8 y = mul8(mul8(gpost, a.scale), q);
-          if (GATE == kTokenGate) {
-            if (a.dgate) st8(a.dgate, row * d + k, a.g_bf16, mul8(slope, mul8(y, D)));
-          } else {
-            gsum[0] = fma8(y, D, gsum[0]);
-          }
-        }
-        if (a.df) {
-          const V8 t = mul8(gpost, dy);
-          st8(static_cast<F*>(a.df) + row * d + k, post_norm ? mul8(fma8(q, -(s[3] * inv_d), t), rf) : t);
-        }
-        if (GATE == kSharedGate && shared_part && (r + 1 == m.rows || row + 1 == group_end))
-          flush_gate(a, m, shared_part, g.teams, group, k, gsum[0]);
-      }
+      if (mine && a.df)
+        st8(static_cast<F*>(a.df) + row * d + k, post_norm ? mul8(fma8(q, -(s[3] * inv_d), t), rf) : t);
+      if (GATE == kSharedGate && mine && (r + 1 == m.rows || row + 1 == group_end))
+        flush_gate(a, m, shared_part, g.teams, a.gate_rows >= a.T, group, k, gsum[0], post[0]);
     }
   }
   write_sums<1>(a, m, g, reinterpret_cast<float*>(smem + g.stages), sums, post_norm && a.dgpost,
-                GATE == kSharedGate && a.dgate && !shared_part, post, pre, gsum);
+                GATE == kSharedGate && a.dgate && a.gate_rows >= a.T, post, pre, gsum);
 }
 
-// The gated backward past d = 4096: 16 features a thread, so only D and the
+// The gated backward past d = 5120: 16 features a thread, so only D and the
 // sums over tokens stay in registers; the row is read from its stage again in
 // each step, and the gains from shared memory. A stage is refilled after the
 // next row's first sum, when every thread is past its last read of it.
 template <int GATE>
-__global__ void __launch_bounds__(kGatedWarps * 32, 1)
+__global__ void __launch_bounds__(kWideWarps * 32, 1)
     residual_bwd_wide_kernel(ResidualBwdArgs a, const __grid_constant__ TeamGeom g, float* sums, float* shared_part) {
   constexpr int kV = 2;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -235,9 +225,9 @@ __global__ void __launch_bounds__(kGatedWarps * 32, 1)
   const int d = a.d, step = m.warps * 256;
   const bool post_norm = a.gpost != nullptr;
   const float inv_d = 1.0f / static_cast<float>(d);
-  float* gains = reinterpret_cast<float*>(smem + g.gain);  // gamma_post, gamma_pre
+  float* gains = reinterpret_cast<float*>(smem + g.gain);  // scale * gamma_post, gamma_pre
   for (int k = threadIdx.x; k < d; k += blockDim.x) {
-    gains[k] = post_norm ? a.gpost[k] : 1.f;
+    gains[k] = post_norm ? a.gpost[k] * a.scale : a.scale;
     gains[d + k] = a.dn ? a.gpre[k] : 0.f;
   }
   __syncthreads();
@@ -287,13 +277,13 @@ __global__ void __launch_bounds__(kGatedWarps * 32, 1)
     if (m.tid == 0 && r > 0 && m.nst > 1 && m.issued < m.rows) issue_row(m, g);
     const float rx = a.dn ? rsqrtf(s[0] * inv_d + a.eps_pre) : 0.f, mx = rx * (s[1] * inv_d);
     const float rf = post_norm ? rsqrtf(s[2] * inv_d + a.eps_post) : 1.f;
-    // scale * act(gate) at 8 features, and with_slope act'(gate) of a token's own gate.
-    auto factor = [&](auto with_slope, V8& slope, int k) {
-      if (GATE == kSharedGate) return shared_factor(a, group, k);
-      if (GATE == kNoGate) return fill8(a.scale);
-      V8 w = ld8(st + g.gate, k, a.g_bf16);
-      activate8<decltype(with_slope)::value>(w, slope, a.sigmoid);
-      return mul8(w, a.scale);
+    // act(gate) at 8 features, and a token's own gate's slope.
+    auto act_at = [&](V8& slope, int k) {
+      if (GATE == kSharedGate) return shared_act(a, group, k, slope);
+      if (GATE == kNoGate) return fill8(1.f);
+      V8 act = ld8(st + g.gate, k, a.g_bf16);
+      activate8<true>(act, slope, a.sigmoid);
+      return act;
     };
 
     V8 D[kV], slope;
@@ -310,34 +300,29 @@ __global__ void __launch_bounds__(kGatedWarps * 32, 1)
         }
         if (a.dx) st8(a.dx, row * d + k, a.dx_bf16, D[v]);
         if (post_norm)
-          q[0] += dot8(mul8(ld8(gains + k), mul8(factor(std::false_type{}, slope, k), D[v])),
-                       mul8(ld8(st + g.f, k, a.f_bf16), rf));
+          q[0] += dot8(mul8(ld8(gains + k), mul8(act_at(slope, k), D[v])), mul8(ld8(st + g.f, k, a.f_bf16), rf));
       }
     }
     (void)team_sum(m, q, 1, true);
-    const float mf = q[0] * inv_d;
+    const float mf = post_norm ? q[0] * inv_d : 0.f;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
       const int k = v * step + m.tid * 8;
       if (k < d) {
-        const V8 f = mul8(ld8(st + g.f, k, a.f_bf16), rf), c = ld8(gains + k);
-        const V8 dy = mul8(factor(std::true_type{}, slope, k), D[v]);
-        post[v] = fma8(dy, f, post[v]);
-        if (GATE != kNoGate) {
-          const V8 y = mul8(mul8(c, a.scale), f);
-          if (GATE == kTokenGate) {
-            if (a.dgate) st8(a.dgate, row * d + k, a.g_bf16, mul8(slope, mul8(y, D[v])));
-          } else {
-            gsum[v] = fma8(y, D[v], gsum[v]);
-          }
+        const V8 f = mul8(ld8(st + g.f, k, a.f_bf16), rf), c = ld8(gains + k), qD = mul8(f, D[v]);
+        const V8 act = act_at(slope, k);
+        if (GATE == kSharedGate) {
+          gsum[v] = fma8(f, D[v], gsum[v]);
+        } else {
+          post[v] = fma8(act, qD, post[v]);
+          if (GATE == kTokenGate && a.dgate) st8(a.dgate, row * d + k, a.g_bf16, mul8(slope, mul8(c, qD)));
         }
         if (a.df) {
-          V8 t = mul8(c, dy);
-          if (post_norm) t = mul8(fma8(f, -mf, t), rf);
-          st8(a.df, row * d + k, a.f_bf16, t);
+          const V8 t = mul8(mul8(c, act), D[v]);
+          st8(a.df, row * d + k, a.f_bf16, post_norm ? mul8(fma8(f, -mf, t), rf) : t);
         }
-        if (GATE == kSharedGate && shared_part && (r + 1 == m.rows || row + 1 == group_end))
-          flush_gate(a, m, shared_part, g.teams, group, k, gsum[v]);
+        if (GATE == kSharedGate && (r + 1 == m.rows || row + 1 == group_end))
+          flush_gate(a, m, shared_part, g.teams, a.gate_rows >= a.T, group, k, gsum[v], post[v]);
       }
     }
     // A ring of one stage: the next row's copies start when all are done with this one.
@@ -347,7 +332,7 @@ __global__ void __launch_bounds__(kGatedWarps * 32, 1)
     }
   }
   write_sums<kV>(a, m, g, reinterpret_cast<float*>(smem + g.stages), sums, post_norm && a.dgpost,
-                 GATE == kSharedGate && a.dgate && !shared_part, post, pre, gsum);
+                 GATE == kSharedGate && a.dgate && a.gate_rows >= a.T, post, pre, gsum);
 }
 
 // Gate rows whose tokens lie in several teams' runs: the sums of those teams,
@@ -366,11 +351,15 @@ __global__ void __launch_bounds__(256)
   const int64_t first = ((start + 1) * teams - 1) / a.T;  // the team with the row's first token
   if (a.T * (first + 1) / teams != row) return;
   const int64_t end = a.gate_rows < a.T - start ? start + a.gate_rows : a.T;
-  float s = shared_part[(first * 2 + 1) * a.d + k];
-  for (int64_t u = t; u < teams; ++u) {
-    const int64_t u0 = a.T * u / teams, u1 = a.T * (u + 1) / teams;
-    if (u0 >= end) break;
-    if (u0 < u1) s += shared_part[u * 2 * a.d + k];
+  const int64_t last = (end * teams - 1) / a.T;           // and the one with its last
+  const float* part = shared_part + k;
+  float s = part[(first * 2 + 1) * a.d];
+  if (a.T >= teams) {
+#pragma unroll 8
+    for (int64_t u = t; u <= last; ++u) s += part[u * 2 * a.d];
+  } else {  // some teams have no rows, and have written nothing
+    for (int64_t u = t; u <= last; ++u)
+      if (a.T * u / teams < a.T * (u + 1) / teams) s += part[u * 2 * a.d];
   }
   if (a.g_bf16)
     static_cast<bf16*>(a.dgate)[group * a.d + k] = from_f32<bf16>(s);

@@ -31,10 +31,8 @@ struct TeamGeom {
   int64_t withhold;
 };
 
-// Features of a thread and warps of a CTA: 8 features and up to 32 warps where
-// a thread's state fits in 64 registers (the forward, the RMSNorm backward);
-// the gated backward takes 16 warps of up to 128 registers, and past d = 4096
-// 16 features a thread.
+// Teams of a CTA of up to max_warps warps: 8 features a thread where a row then
+// fits in them, else 16.
 struct TeamShape {
   int vectors, warps, teams;
 };

@@ -302,8 +302,8 @@ int64_t attnres_rmsnorm_bwd_scratch_floats(int64_t T, int32_t d);
  *   norm       device, fp32 [1]: the norm before clipping.
  *   scratch    device, fp32, at least attnres_grad_norm_scratch_floats(n)
  *              floats; as for attnres_gated_residual_bwd.
- * The squares are summed in fp32, per thread and in three scales, and the
- * parts in fp64, in a fixed order: the norm is right for gradients anywhere in
+ * The squares are summed in fp32, in three scales and in a fixed order, with
+ * the rounding of long sums carried along: the norm is right for gradients anywhere in
  * fp32's normal range, also where g^2 would overflow or vanish, and the same
  * call gives the same bits. attnres_grad_norm may list a tensor twice; it then
  * counts twice. Tensors of 16-byte aligned storage stream fastest.
