@@ -152,8 +152,15 @@ def _slices(t: torch.Tensor) -> tuple[int, int, int, int]:
     return t.shape[0], t.shape[1], t.shape[2], t.stride(0)
 
 
+# The current stream's handle without a Stream object around it, which costs
+# more than a small kernel (2.9 us against 0.1).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -348,23 +355,33 @@ def attnres_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float, out: torch
 
 def _like(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: int) -> int:
     """The pointer of a contiguous tensor of a shape and type on a device."""
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on the current CUDA device")
     return t.data_ptr()
 
 
-def _scratch(scratch, need: int, device: int, stream) -> torch.Tensor:
-    """A call's scratch: the caller's, checked, or a new one that lives until `stream` is done with it."""
+def _opt(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, device: int) -> int | None:
+    return None if t is None else _like(name, t, shape, dtype, device)
+
+
+def _two_dims(name: str, t: torch.Tensor) -> torch.Size:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [T, d]")
+    return t.shape
+
+
+def _scratch(scratch, need, device: int, stream) -> torch.Tensor:
+    """A call's scratch: the caller's (whose size the library checks), or a new one of need() elements that lives
+    until `stream` is done with it."""
     if scratch is None:
-        scratch = torch.empty(need, device=torch.device("cuda", device), dtype=torch.float32)
+        scratch = torch.empty(need(), device=torch.device("cuda", device), dtype=torch.float32)
         if stream is not None:
             scratch.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
                                   torch.cuda.ExternalStream(int(stream)))
-    elif (scratch.dtype != torch.float32 or scratch.numel() < need or not scratch.is_contiguous() or
-          scratch.get_device() != device):
-        raise ValueError(f"scratch must be contiguous fp32 of at least {need} elements on the current CUDA device")
+    elif scratch.dtype is not torch.float32 or not scratch.is_contiguous() or scratch.get_device() != device:
+        raise ValueError("scratch must be contiguous fp32 on the current CUDA device")
     return scratch
 
 
@@ -386,16 +403,15 @@ def attnres_gated_residual(f: torch.Tensor, x: torch.Tensor | None, gamma_post: 
     f, normed [T, d] of one type; x, x_out [T, d] of one type (fp32 if f is; x
     may be None for 0, and x_out may be x); gate [ceil(T / gate_rows), d], token
     t taking row t // gate_rows, or None; gamma_post None for no post-norm."""
-    T, d = _rows(f)
-    device, shape = torch.cuda.current_device(), f.shape
+    shape = T, d = _two_dims("f", f)
+    dt, xt, device, f32 = f.dtype, x_out.dtype, torch.cuda.current_device(), torch.float32
     gptr, gcode = _gate(gate, gate_rows, T, d, device)
-    _check("attnres_gated_residual", lib().attnres_gated_residual(
-        _like("f", f, shape, f.dtype, device), None if x is None else _like("x", x, shape, x_out.dtype, device),
-        None if gamma_post is None else _like("gamma_post", gamma_post, (d,), torch.float32, device), eps_post,
-        gptr, gate_rows, gcode, gate_act, scale, T, d, _dtype(f), _dtype(x_out),
-        _like("x_out", x_out, shape, x_out.dtype, device),
-        None if gamma_pre is None else _like("gamma_pre", gamma_pre, (d,), torch.float32, device), eps_pre,
-        None if normed is None else _like("normed", normed, shape, f.dtype, device), _stream(stream)))
+    _check("attnres_gated_residual", (_lib or lib()).attnres_gated_residual(
+        _like("f", f, shape, dt, device), _opt("x", x, shape, xt, device),
+        _opt("gamma_post", gamma_post, (d,), f32, device), eps_post, gptr, gate_rows, gcode, gate_act, scale, T, d,
+        _dtype(f), _dtype(x_out), _like("x_out", x_out, shape, xt, device),
+        _opt("gamma_pre", gamma_pre, (d,), f32, device), eps_pre, _opt("normed", normed, shape, dt, device),
+        _stream(stream)))
     return x_out
 
 
@@ -420,32 +436,26 @@ def attnres_gated_residual_bwd(f: torch.Tensor, gamma_post: torch.Tensor | None,
     to, or with accumulate False written. scratch: fp32, at least
     attnres_gated_residual_bwd_scratch_floats(T, d, gate_rows) elements
     (allocated here if None)."""
-    T, d = _rows(f)
-    device, shape = torch.cuda.current_device(), f.shape
+    shape = T, d = _two_dims("f", f)
+    dt, device, f32 = f.dtype, torch.cuda.current_device(), torch.float32
     grad = dx_out if dx_out is not None else dx
-    gdt = torch.float32 if grad is None else grad.dtype
-    code = F32 if grad is None else _dtype(grad)
-    rows = 1 if gate is None else gate_rows
+    gt, code = (f32, F32) if grad is None else (grad.dtype, _dtype(grad))
+    xt, xcode = (dt, _dtype(f)) if x_out is None else (x_out.dtype, _dtype(x_out))
     gptr, gcode = _gate(gate, gate_rows, T, d, device)
-    if dgate is not None and gate is None:
-        raise ValueError("dgate needs a gate")
-
-    def rowwise(name, t, dtype):
-        return None if t is None else _like(name, t, shape, dtype, device)
-
-    def gain(name, t):
-        return None if t is None else _like(name, t, (d,), torch.float32, device)
-
-    need = attnres_gated_residual_bwd_scratch_floats(T, d, rows)
-    scratch = _scratch(scratch, need, device, stream)
-    _check("attnres_gated_residual_bwd", lib().attnres_gated_residual_bwd(
-        _like("f", f, shape, f.dtype, device), gain("gamma_post", gamma_post), eps_post, gptr, rows, gcode, gate_act,
-        scale, T, d, _dtype(f), _dtype(f if x_out is None else x_out),
-        None if x_out is None else rowwise("x_out", x_out, x_out.dtype), gain("gamma_pre", gamma_pre),
-        eps_pre, rowwise("dx_out", dx_out, gdt), code, rowwise("dnormed", dnormed, f.dtype), rowwise("df", df, f.dtype),
-        rowwise("dx", dx, gdt), None if dgate is None else _like("dgate", dgate, gate.shape, gate.dtype, device),
-        gain("dgamma_post", dgamma_post), gain("dgamma_pre", dgamma_pre), int(bool(accumulate)), scratch.data_ptr(),
-        scratch.numel(), _stream(stream)))
+    if gate is None:
+        gate_rows = 1
+        if dgate is not None:
+            raise ValueError("dgate needs a gate")
+    scratch = _scratch(scratch, lambda: attnres_gated_residual_bwd_scratch_floats(T, d, gate_rows), device, stream)
+    _check("attnres_gated_residual_bwd", (_lib or lib()).attnres_gated_residual_bwd(
+        _like("f", f, shape, dt, device), _opt("gamma_post", gamma_post, (d,), f32, device), eps_post, gptr, gate_rows,
+        gcode, gate_act, scale, T, d, _dtype(f), xcode, _opt("x_out", x_out, shape, xt, device),
+        _opt("gamma_pre", gamma_pre, (d,), f32, device), eps_pre, _opt("dx_out", dx_out, shape, gt, device), code,
+        _opt("dnormed", dnormed, shape, dt, device), _opt("df", df, shape, dt, device),
+        _opt("dx", dx, shape, gt, device),
+        None if dgate is None else _like("dgate", dgate, gate.shape, gate.dtype, device),
+        _opt("dgamma_post", dgamma_post, (d,), f32, device), _opt("dgamma_pre", dgamma_pre, (d,), f32, device),
+        1 if accumulate else 0, scratch.data_ptr(), scratch.numel(), _stream(stream)))
 
 
 def attnres_rmsnorm_bwd_scratch_floats(T: int, d: int) -> int:
@@ -460,14 +470,13 @@ def attnres_rmsnorm_bwd(x: torch.Tensor, gamma: torch.Tensor, eps: float, dy: to
     (fp32 [d] or None) added to, or with accumulate False written. x and dy [T, d] of one type; dres (or
     None) and dx of one type, dx may be dres. scratch: fp32, at least
     attnres_rmsnorm_bwd_scratch_floats(T, d) elements (allocated here if None)."""
-    T, d = _rows(x)
-    device, shape = torch.cuda.current_device(), x.shape
-    scratch = _scratch(scratch, attnres_rmsnorm_bwd_scratch_floats(T, d), device, stream)
-    _check("attnres_rmsnorm_bwd", lib().attnres_rmsnorm_bwd(
-        _like("x", x, shape, x.dtype, device), T, d, _dtype(x), _like("gamma", gamma, (d,), torch.float32, device), eps,
-        _like("dy", dy, shape, x.dtype, device), None if dres is None else _like("dres", dres, shape, dx.dtype, device),
-        _dtype(dx), _like("dx", dx, shape, dx.dtype, device),
-        None if dgamma is None else _like("dgamma", dgamma, (d,), torch.float32, device), int(bool(accumulate)),
+    shape = T, d = _two_dims("x", x)
+    dt, gt, device, f32 = x.dtype, dx.dtype, torch.cuda.current_device(), torch.float32
+    scratch = _scratch(scratch, lambda: attnres_rmsnorm_bwd_scratch_floats(T, d), device, stream)
+    _check("attnres_rmsnorm_bwd", (_lib or lib()).attnres_rmsnorm_bwd(
+        _like("x", x, shape, dt, device), T, d, _dtype(x), _like("gamma", gamma, (d,), f32, device), eps,
+        _like("dy", dy, shape, dt, device), _opt("dres", dres, shape, gt, device), _dtype(dx),
+        _like("dx", dx, shape, gt, device), _opt("dgamma", dgamma, (d,), f32, device), 1 if accumulate else 0,
         scratch.data_ptr(), scratch.numel(), _stream(stream)))
     return dx
 
@@ -519,7 +528,9 @@ def _grad_call(grads, outs, norm, scratch, stream) -> tuple[GradList, torch.Tens
         raise ValueError("gradients must be on the current CUDA device")
     if norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != device:
         raise ValueError("norm must be one fp32 element on the current CUDA device")
-    return grads, _scratch(scratch, grads.scratch_floats, device, stream)
+    if scratch is not None and scratch.numel() < grads.scratch_floats:
+        raise ValueError(f"scratch must hold at least {grads.scratch_floats} elements")
+    return grads, _scratch(scratch, lambda: grads.scratch_floats, device, stream)
 
 
 def attnres_grad_norm_scratch_floats(n: int) -> int:
@@ -530,7 +541,7 @@ def attnres_grad_norm_scratch_floats(n: int) -> int:
 def attnres_grad_norm(grads, norm: torch.Tensor, scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """norm (fp32, one element) = sqrt of the sum of squares of every element of a list of tensors or a GradList."""
     grads, scratch = _grad_call(grads, None, norm, scratch, stream)
-    _check("attnres_grad_norm", lib().attnres_grad_norm(
+    _check("attnres_grad_norm", (_lib or lib()).attnres_grad_norm(
         grads.pointers, grads.counts, grads.codes, grads.n, norm.data_ptr(), scratch.data_ptr(), scratch.numel(),
         _stream(stream)))
     return norm
@@ -542,7 +553,7 @@ def attnres_grad_clip(grads, max_norm: float, norm: torch.Tensor, outs=None, scr
     above max_norm, else times 1: in place, or into `outs` (fp32 or bf16, all elements written; a GradList holds
     its own)."""
     grads, scratch = _grad_call(grads, outs, norm, scratch, stream)
-    _check("attnres_grad_clip", lib().attnres_grad_clip(
+    _check("attnres_grad_clip", (_lib or lib()).attnres_grad_clip(
         grads.pointers, grads.counts, grads.codes, grads.out_pointers, grads.out_codes, grads.n, max_norm,
         norm.data_ptr(), scratch.data_ptr(), scratch.numel(), _stream(stream)))
     return norm

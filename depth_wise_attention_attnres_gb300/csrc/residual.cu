@@ -268,13 +268,14 @@ __global__ void __launch_bounds__(kThreads) residual_bwd_rows_kernel(ResidualBwd
 // The last step of the sums over tokens: the partial rows of each kind added in
 // a fixed order, 32 runs of them at once (every 32nd) per feature.
 __global__ void __launch_bounds__(1024)
-    residual_bwd_reduce_kernel(ResidualBwdArgs a, const float* part, int parts, int gate_too) {
+    residual_bwd_reduce_kernel(ResidualBwdArgs a, const float* part, int parts, int kinds) {
   __shared__ float red[32][33];
   pdl_trigger();
   pdl_wait();
-  const int which = blockIdx.y, x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  // The blockIdx.y-th of the kinds wanted: 0 dgamma_post, 1 dgamma_pre, 2 the gate.
+  const int which = blockIdx.y == 0 ? __ffs(kinds) - 1 : (blockIdx.y == 1 && kinds == 7 ? 1 : 31 - __clz(kinds));
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   float* const gain = which == 0 ? a.dgpost : a.dgpre;
-  if (which < 2 ? gain == nullptr : !gate_too) return;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * 32;
   float s = 0.f;
   // Without the norm its gain has no part in anything.
@@ -300,11 +301,11 @@ unsigned row_grid(int64_t T) {
 }
 
 int run_reduce(const ResidualBwdArgs& a, const float* part, int parts, cudaStream_t s) {
-  const bool gate_sum = residual_bwd_sums_gate(a) && parts > 0;
-  if (!a.dgpost && !a.dgpre && !gate_sum) return ATTNRES_OK;
+  const int kinds = (a.dgpost ? 1 : 0) | (a.dgpre ? 2 : 0) | (residual_bwd_sums_gate(a) && parts > 0 ? 4 : 0);
+  if (!kinds) return ATTNRES_OK;
+  const unsigned n = (kinds & 1) + (kinds >> 1 & 1) + (kinds >> 2);
   return launch_step([&] {
-    return launch_pdl_grid(residual_bwd_reduce_kernel, dim3((a.d - 1) / 32 + 1, gate_sum ? 3 : 2), 1024, 0,
-                           s, a, part, parts, static_cast<int>(gate_sum));
+    return launch_pdl_grid(residual_bwd_reduce_kernel, dim3((a.d - 1) / 32 + 1, n), 1024, 0, s, a, part, parts, kinds);
   });
 }
 

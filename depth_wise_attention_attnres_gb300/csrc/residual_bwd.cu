@@ -16,10 +16,34 @@ namespace {
 
 __device__ unsigned int g_timeout = 0;
 
-// 20 warps of 96 registers, 32 of 64; past d = 5120 the gated kernel's threads
-// take 16 features and 128 registers (a row is then 11 to 16 warps).
-constexpr int kNormWarps = 32, kGatedWarps = 20, kWideWarps = 16;
-int max_warps(const ResidualBwdArgs& a) { return a.f ? kGatedWarps : kNormWarps; }
+// Warps of a CTA. The backward of RMSNorm: 28 of 72 registers, or 16 of 128 for
+// 16 features a thread. The gated one: 20 of 96, or 16 of 128 where runs of
+// tokens share gate rows; past the width that 8 features a thread cover its
+// threads take 16 and 128 registers.
+constexpr int norm_warps(int vectors) { return vectors == 1 ? 28 : 16; }
+constexpr int gated_warps(int gate) { return gate == kSharedGate ? 16 : 20; }
+constexpr int kWideWarps = 16;
+// Rows in flight per SM (as the forward's: the rings of the RMSNorm backward
+// are held to what left the writes room; the gated one, with more arithmetic to
+// cover, lost by it).
+constexpr int kNormRing = 146 * 1024, kGatedRing = kTeamSmem;
+
+// The gate of a call: none or one row for all tokens, one per token, or rows
+// that runs of tokens share.
+int gate_kind(int64_t T, int64_t gate_rows, bool gate) {
+  if (!gate || (gate_rows > 1 && gate_rows >= T)) return kNoGate;
+  return gate_rows == 1 ? kTokenGate : kSharedGate;
+}
+TeamShape norm_shape(int d) {
+  const int v = d > 256 * norm_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1;
+  return team_shape(d, v, norm_warps(v));
+}
+TeamShape gated_shape(int d, int gate) {
+  return d <= 256 * gated_warps(gate) ? team_shape(d, 1, gated_warps(gate)) : team_shape(d, 2, kWideWarps);
+}
+TeamShape shape_of(const ResidualBwdArgs& a) {
+  return a.f ? gated_shape(a.d, gate_kind(a.T, a.gate_rows, a.gate != nullptr)) : norm_shape(a.d);
+}
 
 // 8 features of a gate row that tokens share: act(gate), and its slope.
 __device__ __forceinline__ V8 shared_act(const ResidualBwdArgs& a, int64_t group, int k, V8& slope) {
@@ -33,31 +57,30 @@ __device__ __forceinline__ V8 scaled_gain(const ResidualBwdArgs& a, int k) {
 }
 
 // The end of a run of tokens that share a gate row, at 8 features, with acc the
-// sum of q D over the team's tokens of it: their part of sum act q D, and the
-// gate row's gradient, slope scale gamma_post acc, written where the team has all
-// of the row's tokens, or kept for the kernel that joins the teams' parts.
-// part nullptr: the gradient is not wanted; all: one row for all tokens (its
-// gradient goes with the other sums over tokens, in acc).
-__device__ __forceinline__ void flush_gate(const ResidualBwdArgs& a, const Team& m, float* part, int teams, bool all,
-                                           int64_t group, int k, V8& acc, V8& post) {
+// sum of q D over the team's tokens of it: returns their part of sum act q D,
+// and makes acc the gate row's gradient, slope scale gamma_post acc, which is
+// written where the team has all of the row's tokens, or kept for the kernel
+// that joins the teams' parts (part nullptr: neither).
+__device__ __forceinline__ V8 flush_gate(const ResidualBwdArgs& a, const Team& m, float* part, int teams, int64_t group,
+                                         int k, V8& acc) {
   V8 slope;
-  post = fma8(shared_act(a, group, k, slope), acc, post);
-  const V8 sum = mul8(mul8(slope, scaled_gain(a, k)), acc);
-  acc = all ? sum : fill8(0.f);
-  if (!part) return;
+  const V8 post = mul8(shared_act(a, group, k, slope), acc);
+  acc = mul8(mul8(slope, scaled_gain(a, k)), acc);
+  if (!part) return post;
   const int64_t start = group * a.gate_rows;
   const int64_t end = a.gate_rows < a.T - start ? start + a.gate_rows : a.T;
   if (start >= m.r0 && end <= m.r0 + m.rows) {
-    st8(a.dgate, group * a.d + k, a.g_bf16, sum);
-    return;
+    st8(a.dgate, group * a.d + k, a.g_bf16, acc);
+    return post;
   }
   const int64_t id = static_cast<int64_t>(blockIdx.x) * teams + m.team;
   part += (id * 2 + (start < m.r0 ? 0 : 1)) * a.d + k;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    part[2 * i] = sum.p[i].x;
-    part[2 * i + 1] = sum.p[i].y;
+    part[2 * i] = acc.p[i].x;
+    part[2 * i + 1] = acc.p[i].y;
   }
+  return post;
 }
 
 // A thread's part of a sum over tokens, for its team.
@@ -94,39 +117,95 @@ __device__ __forceinline__ void write_sums(const ResidualBwdArgs& a, const Team&
   }
 }
 
-// F: the type of f, dnormed and df; X: of x_out; G: of dx_out and dx. HAS_F:
-// with the sublayer's side; without, the backward of RMSNorm.
-template <typename F, typename X, typename G, int GATE, bool HAS_F>
-__global__ void __launch_bounds__((HAS_F ? kGatedWarps : kNormWarps) * 32, 1)
+// The backward of RMSNorm. F: the type of x and dy; G: of dres and dx.
+template <typename F, typename G, int VPT>
+__global__ void __launch_bounds__(norm_warps(VPT) * 32, 1)
+    rmsnorm_bwd_kernel(ResidualBwdArgs a, const __grid_constant__ TeamGeom g, float* sums) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  init_bars(g, smem);
+  Team m = make_team<false>(g, a.T, smem);
+  pdl_trigger();
+  pdl_wait();
+  fill_ring(m, g);
+  const int d = a.d, k0 = m.tid * 8, step = m.warps * 256;
+  const float inv_d = 1.0f / static_cast<float>(d);
+  V8 gain[VPT], sum[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    gain[v] = sum[v] = fill8(0.f);
+    if (k0 + v * step < d) gain[v] = ld8(a.gpre + k0 + v * step);
+  }
+  int stage = 0;
+  uint32_t parity = 0;
+  for (int r = 0; r < m.rows; ++r) {
+    const unsigned char* st = m.ring + stage * g.stage_bytes;
+    bool ok = mbar_wait(m.bars + stage * 8, parity);
+    if (++stage == m.nst) stage = 0, parity ^= 1u;
+    V8 x[VPT], h[VPT], D[VPT];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int k = k0 + v * step;
+      if (ok && k < d) {
+        x[v] = ld8(reinterpret_cast<const F*>(st + g.x) + k);
+        h[v] = ld8(reinterpret_cast<const F*>(st + g.dn) + k);
+        s[0] += dot8(x[v], x[v]);
+        s[1] += dot8(mul8(gain[v], h[v]), x[v]);
+        D[v] = a.dxo ? ld8(reinterpret_cast<const G*>(st + g.dxo) + k) : fill8(0.f);
+      }
+    }
+    ok = team_sum(m, s, r & 1, ok);
+    if (!ok) {
+      give_up(m, g, r, &g_timeout);
+      break;
+    }
+    // Every thread has its part of the row in registers: the stage is free.
+    if (m.tid == 0 && m.issued < m.rows) issue_row(m, g);
+    const float rx = rsqrtf(s[0] * inv_d + a.eps_pre), mx = rx * (s[1] * inv_d);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int k = k0 + v * step;
+      if (k < d) {
+        const V8 u = mul8(x[v], rx);
+        sum[v] = fma8(h[v], u, sum[v]);
+        st8(static_cast<G*>(a.dx) + (m.r0 + r) * d + k, fma8(fma8(u, -mx, mul8(gain[v], h[v])), rx, D[v]));
+      }
+    }
+  }
+  write_sums<VPT>(a, m, g, reinterpret_cast<float*>(smem + g.stages), sums, false, false, sum, sum, sum);
+}
+
+// F: the type of f, dnormed and df; X: of x_out; G: of dx_out and dx. GATE
+// kNoGate also takes the one gate row of all tokens, which rides on the gain.
+template <typename F, typename X, typename G, int GATE>
+__global__ void __launch_bounds__(gated_warps(GATE) * 32, 1)
     residual_bwd_kernel(ResidualBwdArgs a, const __grid_constant__ TeamGeom g, float* sums, float* shared_part) {
   extern __shared__ __align__(128) unsigned char smem[];
   init_bars(g, smem);
-  Team m = make_team(g, a.T, smem);
+  Team m = make_team<false>(g, a.T, smem);
   pdl_trigger();
   pdl_wait();
   fill_ring(m, g);
   const int d = a.d, k = m.tid * 8;
-  const bool mine = k < d, post_norm = HAS_F && a.gpost != nullptr;
+  const bool mine = k < d, post_norm = a.gpost != nullptr;
   const float inv_d = 1.0f / static_cast<float>(d);
   // scale * gamma_post, with a shared gate times its value too.
-  V8 gain = mine && HAS_F ? scaled_gain(a, k) : fill8(0.f), gpre = fill8(0.f), slope;
-  if (mine && a.dn) gpre = ld8(a.gpre + k);
-  // The shared gate row of the current token, and the first token of the next one.
-  int64_t group = 0, group_end = a.T;
-  if (GATE == kSharedGate) {
-    group = m.r0 / a.gate_rows;
-    if (a.gate_rows < a.T) group_end = (group + 1) * a.gate_rows;
-    if (mine && m.rows > 0) gain = mul8(gain, shared_act(a, group, k, slope));
+  V8 gain = fill8(0.f), gpre = fill8(0.f), slope;
+  if (mine) {
+    if (GATE != kSharedGate) gain = scaled_gain(a, k);
+    if (GATE == kNoGate && a.gate) gain = mul8(gain, shared_act(a, 0, k, slope));
+    if (a.dn) gpre = ld8(a.gpre + k);
   }
-  // Sums over tokens: act q D (dgamma_post / scale), dn u, and of the current
-  // shared gate row q D.
-  V8 post[1] = {fill8(0.f)}, pre[1] = {fill8(0.f)}, gsum[1] = {fill8(0.f)};
+  // Sums over tokens: q D (with a gate per token act q D), of the current run of
+  // a shared gate row; dn u. Those of the runs before wait in shared memory.
+  V8 acc = fill8(0.f), pre[1] = {fill8(0.f)};
+  float* const earlier = reinterpret_cast<float*>(smem + g.gain) + m.team * d + k;
+  if (GATE == kSharedGate && mine) st8(earlier, acc);
 
   // Waits for a row and takes its part of sum x^2, sum h x and sum f^2.
   int stage = 0;
   uint32_t parity = 0;
-  constexpr int kSums = HAS_F ? 4 : 2;
-  float s[kSums] = {};  // those of a row, and last sum gamma_post dy q of the row before
+  float s[4] = {};  // those of a row, and last sum gamma_post dy q of the row before
   auto begin_row = [&]() {
     const bool ok = mbar_wait(m.bars + stage * 8, parity);
     if (ok && mine) {
@@ -136,79 +215,82 @@ __global__ void __launch_bounds__((HAS_F ? kGatedWarps : kNormWarps) * 32, 1)
         s[0] = dot8(x, x);
         s[1] = dot8(mul8(gpre, ld8(reinterpret_cast<const F*>(st + g.dn) + k)), x);
       }
-      if constexpr (HAS_F) {
-        const V8 f = ld8(reinterpret_cast<const F*>(st + g.f) + k);
-        s[2] = dot8(f, f);
-      }
+      const V8 f = ld8(reinterpret_cast<const F*>(st + g.f) + k);
+      s[2] = dot8(f, f);
     }
     return ok;
   };
   bool ok = m.rows == 0 || begin_row();
   ok = team_sum(m, s, 1, ok);
   if (!ok) give_up(m, g, 0, &g_timeout);
-  for (int r = 0; ok && r < m.rows; ++r) {
-    const int64_t row = m.r0 + r;
-    if (GATE == kSharedGate && row == group_end) {
-      ++group;
-      group_end += a.gate_rows;
+  // Runs of tokens with one gate row (without such rows: the one run).
+  for (int r = 0; ok && r < m.rows;) {
+    int run_end = m.rows;
+    if (GATE == kSharedGate) {
+      const int64_t group = (m.r0 + r) / a.gate_rows;
+      const int64_t end = (group + 1) * a.gate_rows - m.r0;
+      if (end < run_end) run_end = static_cast<int>(end);
       if (mine) gain = mul8(scaled_gain(a, k), shared_act(a, group, k, slope));
     }
-    const unsigned char* st = m.ring + stage * g.stage_bytes;
-    const float rx = a.dn ? rsqrtf(s[0] * inv_d + a.eps_pre) : 0.f, mx = rx * (s[1] * inv_d);
-    float rf = 1.f;
-    if constexpr (HAS_F) {
-      if (post_norm) rf = rsqrtf(s[2] * inv_d + a.eps_post);
-    }
+    for (; r < run_end; ++r) {
+      const int64_t at = (m.r0 + r) * d + k;
+      const unsigned char* st = m.ring + stage * g.stage_bytes;
+      const float rx = a.dn ? rsqrtf(s[0] * inv_d + a.eps_pre) : 0.f, mx = rx * (s[1] * inv_d);
+      const float rf = post_norm ? rsqrtf(s[2] * inv_d + a.eps_post) : 1.f;
 #pragma unroll
-    for (int i = 0; i < kSums; ++i) s[i] = 0.f;
-    V8 q, t;  // t = gamma_post dy = scale gamma_post act D
-    if (mine) {
-      V8 D = a.dxo ? ld8(reinterpret_cast<const G*>(st + g.dxo) + k) : fill8(0.f);
-      if (a.dn) {
-        const V8 x = mul8(ld8(reinterpret_cast<const X*>(st + g.x) + k), rx);
-        const V8 h = ld8(reinterpret_cast<const F*>(st + g.dn) + k);
-        pre[0] = fma8(h, x, pre[0]);
-        D = fma8(fma8(x, -mx, mul8(gpre, h)), rx, D);
-      }
-      if (a.dx) st8(static_cast<G*>(a.dx) + row * d + k, D);
-      if constexpr (HAS_F) {
+      for (int i = 0; i < 4; ++i) s[i] = 0.f;
+      V8 q, t;  // t = gamma_post dy = scale gamma_post act D
+      if (mine) {
+        V8 D = a.dxo ? ld8(reinterpret_cast<const G*>(st + g.dxo) + k) : fill8(0.f);
+        if (a.dn) {
+          const V8 u = mul8(ld8(reinterpret_cast<const X*>(st + g.x) + k), rx);
+          const V8 h = ld8(reinterpret_cast<const F*>(st + g.dn) + k);
+          pre[0] = fma8(h, u, pre[0]);
+          D = fma8(fma8(u, -mx, mul8(gpre, h)), rx, D);
+        }
+        if (a.dx) st8(static_cast<G*>(a.dx) + at, D);
         q = mul8(ld8(reinterpret_cast<const F*>(st + g.f) + k), rf);
         if (GATE == kTokenGate) {
           V8 act = ld8(st + g.gate, k, a.g_bf16);
           activate8<true>(act, slope, a.sigmoid);
           const V8 qD = mul8(q, D);
-          post[0] = fma8(act, qD, post[0]);
-          if (a.dgate) st8(a.dgate, row * d + k, a.g_bf16, mul8(slope, mul8(gain, qD)));
+          acc = fma8(act, qD, acc);
+          if (a.dgate) st8(a.dgate, at, a.g_bf16, mul8(slope, mul8(gain, qD)));
           t = mul8(mul8(gain, act), D);
         } else {
-          V8& sum = GATE == kSharedGate ? gsum[0] : post[0];
-          sum = fma8(q, D, sum);
+          acc = fma8(q, D, acc);
           t = mul8(gain, D);
         }
         s[3] = dot8(t, q);
       }
-    }
-    if (++stage == m.nst) stage = 0, parity ^= 1u;
-    if (r + 1 < m.rows) ok = begin_row();
-    ok = team_sum(m, s, r & 1, ok);
-    if (!ok) {
-      give_up(m, g, r + 1, &g_timeout);
-      break;
-    }
-    // Every thread has what it needs of row r: its stage is free.
-    if (m.tid == 0 && m.issued < m.rows) issue_row(m, g);
-    if constexpr (HAS_F) {
+      if (++stage == m.nst) stage = 0, parity ^= 1u;
+      if (r + 1 < m.rows) ok = begin_row();
+      ok = team_sum(m, s, r & 1, ok);
+      if (!ok) {
+        give_up(m, g, r + 1, &g_timeout);
+        break;
+      }
+      // Every thread has what it needs of row r: its stage is free.
+      if (m.tid == 0 && m.issued < m.rows) issue_row(m, g);
       if (mine && a.df)
-        st8(static_cast<F*>(a.df) + row * d + k, post_norm ? mul8(fma8(q, -(s[3] * inv_d), t), rf) : t);
-      if (GATE == kSharedGate && mine && (r + 1 == m.rows || row + 1 == group_end))
-        flush_gate(a, m, shared_part, g.teams, a.gate_rows >= a.T, group, k, gsum[0], post[0]);
+        st8(static_cast<F*>(a.df) + at, post_norm ? mul8(fma8(q, -(s[3] * inv_d), t), rf) : t);
+    }
+    if (GATE == kSharedGate && mine) {
+      const V8 post = flush_gate(a, m, shared_part, g.teams, (m.r0 + run_end - 1) / a.gate_rows, k, acc);
+      st8(earlier, add8(ld8(earlier), post));
+      acc = fill8(0.f);
     }
   }
+  V8 post[1] = {acc}, gate[1] = {acc};
+  if (mine) {
+    if (GATE == kSharedGate) post[0] = ld8(earlier);
+    if (GATE == kNoGate && a.gate) post[0] = flush_gate(a, m, nullptr, g.teams, 0, k, gate[0]);
+  }
   write_sums<1>(a, m, g, reinterpret_cast<float*>(smem + g.stages), sums, post_norm && a.dgpost,
-                GATE == kSharedGate && a.dgate && a.gate_rows >= a.T, post, pre, gsum);
+                GATE == kNoGate && a.gate && a.dgate, post, pre, gate);
 }
 
-// The gated backward past d = 5120: 16 features a thread, so only D and the
+// The gated backward of wider rows: 16 features a thread, so only D and the
 // sums over tokens stay in registers; the row is read from its stage again in
 // each step, and the gains from shared memory. A stage is refilled after the
 // next row's first sum, when every thread is past its last read of it.
@@ -218,7 +300,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, 1)
   constexpr int kV = 2;
   extern __shared__ __align__(128) unsigned char smem[];
   init_bars(g, smem);
-  Team m = make_team(g, a.T, smem);
+  Team m = make_team<false>(g, a.T, smem);
   pdl_trigger();
   pdl_wait();
   fill_ring(m, g);
@@ -231,6 +313,13 @@ __global__ void __launch_bounds__(kWideWarps * 32, 1)
     gains[d + k] = a.dn ? a.gpre[k] : 0.f;
   }
   __syncthreads();
+  if (GATE == kNoGate && a.gate) {  // one row for all tokens
+    for (int k = threadIdx.x * 8; k < d; k += blockDim.x * 8) {
+      V8 slope;
+      st8(gains + k, mul8(ld8(gains + k), shared_act(a, 0, k, slope)));
+    }
+    __syncthreads();
+  }
   int64_t group = 0, group_end = a.T;
   if (GATE == kSharedGate) {
     group = m.r0 / a.gate_rows;
@@ -321,8 +410,10 @@ __global__ void __launch_bounds__(kWideWarps * 32, 1)
           const V8 t = mul8(mul8(c, act), D[v]);
           st8(a.df, row * d + k, a.f_bf16, post_norm ? mul8(fma8(f, -mf, t), rf) : t);
         }
-        if (GATE == kSharedGate && (r + 1 == m.rows || row + 1 == group_end))
-          flush_gate(a, m, shared_part, g.teams, a.gate_rows >= a.T, group, k, gsum[v], post[v]);
+        if (GATE == kSharedGate && (r + 1 == m.rows || row + 1 == group_end)) {
+          post[v] = add8(post[v], flush_gate(a, m, shared_part, g.teams, group, k, gsum[v]));
+          gsum[v] = fill8(0.f);
+        }
       }
     }
     // A ring of one stage: the next row's copies start when all are done with this one.
@@ -331,8 +422,16 @@ __global__ void __launch_bounds__(kWideWarps * 32, 1)
       if (m.tid == 0) issue_row(m, g);
     }
   }
+  if (GATE == kNoGate && a.gate) {
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      const int k = v * step + m.tid * 8;
+      gsum[v] = post[v];
+      if (k < d) post[v] = flush_gate(a, m, nullptr, g.teams, 0, k, gsum[v]);
+    }
+  }
   write_sums<kV>(a, m, g, reinterpret_cast<float*>(smem + g.stages), sums, post_norm && a.dgpost,
-                 GATE == kSharedGate && a.dgate && a.gate_rows >= a.T, post, pre, gsum);
+                 GATE == kNoGate && a.gate && a.dgate, post, pre, gsum);
 }
 
 // Gate rows whose tokens lie in several teams' runs: the sums of those teams,
@@ -375,9 +474,16 @@ bool geom_of(const ResidualBwdArgs& a, TeamGeom* g) {
   add_input(*g, a.dxo, a.d * (a.dx_bf16 ? 2 : 4), &g->dxo);
   add_input(*g, a.dn, a.d * es, &g->dn);
   add_input(*g, a.gate && a.gate_rows == 1 ? a.gate : nullptr, a.d * (a.g_bf16 ? 2 : 4), &g->gate);
-  const TeamShape s = team_shape(a.d, max_warps(a));
+  const TeamShape s = shape_of(a);
+  // Past 8 features a thread the gated kernel's gains, and where runs of tokens
+  // share gate rows the sums of earlier runs.
+  int gain_bytes = 0;
+  if (a.f && s.vectors > 1)
+    gain_bytes = 8 * a.d;
+  else if (a.f && gate_kind(a.T, a.gate_rows, a.gate != nullptr) == kSharedGate)
+    gain_bytes = 4 * s.teams * a.d;
   // The teams' sums go through the rings' space: 4 bytes a feature and team.
-  return finish_geom(*g, s, s.vectors > 1 ? 8 * a.d : 0, s.vectors > 1 ? 1 : 2) && g->nst * g->stage_bytes >= 4 * a.d;
+  return finish_geom(*g, s, gain_bytes, a.f && s.vectors > 1 ? 1 : 2, a.f ? kGatedRing : kNormRing) && g->nst * g->stage_bytes >= 4 * a.d;
 }
 
 struct Plan {
@@ -386,18 +492,20 @@ struct Plan {
   float* sums;
   float* shared;
   cudaStream_t s;
+  int gate;
 };
 
 template <typename F, typename X, typename G>
 cudaError_t launch_typed(const ResidualBwdArgs& a, const Plan& p) {
-  if (!a.gate) return launch_teams(residual_bwd_kernel<F, X, G, kNoGate, true>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
-  if (a.gate_rows == 1)
-    return launch_teams(residual_bwd_kernel<F, X, G, kTokenGate, true>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
-  return launch_teams(residual_bwd_kernel<F, X, G, kSharedGate, true>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  if (p.gate == kNoGate) return launch_teams(residual_bwd_kernel<F, X, G, kNoGate>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  if (p.gate == kTokenGate)
+    return launch_teams(residual_bwd_kernel<F, X, G, kTokenGate>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  return launch_teams(residual_bwd_kernel<F, X, G, kSharedGate>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
 }
 template <typename F, typename G>
 cudaError_t launch_norm(const ResidualBwdArgs& a, const Plan& p) {
-  return launch_teams(residual_bwd_kernel<F, F, G, kNoGate, false>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  if (norm_shape(a.d).vectors > 1) return launch_teams(rmsnorm_bwd_kernel<F, G, 2>, p.g, p.ctas, p.s, a, p.g, p.sums);
+  return launch_teams(rmsnorm_bwd_kernel<F, G, 1>, p.g, p.ctas, p.s, a, p.g, p.sums);
 }
 
 }  // namespace
@@ -409,30 +517,33 @@ bool residual_bwd_fast_ok(const ResidualBwdArgs& a) {
          aligned16(a.dx) && aligned16(a.dgate) && geom_of(a, &g);
 }
 
-// Enough for either shape of a CTA (the gated one has more teams to a CTA's
-// partial rows of shared gates, the other more CTAs to none).
+// Enough for any gate of these rows, and with gate_rows 1 for the backward of
+// RMSNorm: that of the shape with the fewest teams, so the most CTAs.
 int64_t residual_bwd_fast_scratch(int64_t T, int d, int64_t gate_rows) {
   if (T == 0 || d % 8 != 0 || d > kMaxTeamD) return 0;
-  const TeamShape s = team_shape(d, kGatedWarps);
+  const int gate = gate_kind(T, gate_rows, true);
+  TeamShape s = gated_shape(d, gate);
+  const TeamShape n = norm_shape(d);
+  if (gate == kTokenGate && n.teams < s.teams) s = n;
   const int64_t ctas = team_ctas(T, s, kMaxCtas);
-  return 3 * ctas * d + (gate_rows > 1 && gate_rows < T ? ctas * s.teams * 2 * d : 0);
+  return 3 * ctas * d + (gate == kSharedGate ? ctas * s.teams * 2 * d : 0);
 }
 
 int residual_bwd_parts(const ResidualBwdArgs& a) {
-  return static_cast<int>(team_ctas(a.T, team_shape(a.d, max_warps(a)), cta_cap()));
+  return static_cast<int>(team_ctas(a.T, shape_of(a), cta_cap()));
 }
 
 cudaError_t launch_residual_bwd_fast(const ResidualBwdArgs& a, cudaStream_t s) {
-  Plan p{{}, residual_bwd_parts(a), a.scratch, nullptr, s};
+  Plan p{{}, residual_bwd_parts(a), a.scratch, nullptr, s, gate_kind(a.T, a.gate_rows, a.gate != nullptr)};
   if (!geom_of(a, &p.g)) return cudaErrorInvalidValue;
   if (residual_bwd_shares_gates(a)) p.shared = p.sums + 3 * p.ctas * a.d;
   if (!a.f) {
     if (!a.f_bf16) return launch_norm<float, float>(a, p);
     return a.dx_bf16 ? launch_norm<bf16, bf16>(a, p) : launch_norm<bf16, float>(a, p);
   }
-  if (team_shape(a.d, kGatedWarps).vectors > 1) {
-    if (!a.gate) return launch_teams(residual_bwd_wide_kernel<kNoGate>, p.g, p.ctas, s, a, p.g, p.sums, p.shared);
-    if (a.gate_rows == 1)
+  if (shape_of(a).vectors > 1) {
+    if (p.gate == kNoGate) return launch_teams(residual_bwd_wide_kernel<kNoGate>, p.g, p.ctas, s, a, p.g, p.sums, p.shared);
+    if (p.gate == kTokenGate)
       return launch_teams(residual_bwd_wide_kernel<kTokenGate>, p.g, p.ctas, s, a, p.g, p.sums, p.shared);
     return launch_teams(residual_bwd_wide_kernel<kSharedGate>, p.g, p.ctas, s, a, p.g, p.sums, p.shared);
   }
@@ -442,7 +553,7 @@ cudaError_t launch_residual_bwd_fast(const ResidualBwdArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_residual_bwd_join_gate(const ResidualBwdArgs& a, cudaStream_t s) {
-  const int64_t ctas = residual_bwd_parts(a), teams = ctas * team_shape(a.d, kGatedWarps).teams;
+  const int64_t ctas = residual_bwd_parts(a), teams = ctas * shape_of(a).teams;
   const float* shared = a.scratch + 3 * ctas * a.d;
   if (teams < 2) return cudaSuccess;
   return launch_pdl_grid(residual_bwd_join_gate_kernel, dim3(static_cast<unsigned>(teams - 1), (a.d - 1) / 256 + 1), 256, 0,

@@ -1,9 +1,12 @@
 // The gated residual for d a multiple of 8 up to 8192 with aligned rows (the
 // formulas stand at the top of residual.cu, the teams in residual_team.cuh).
 //
-// Bound by memory: each row is read and written once. A thread holds 8 features
-// of the row and of the gains. The sum of squares of row r's result and that of
-// row r + 1's f go through the team together, so a row costs one barrier.
+// Bound by memory: each row is read and written once. A thread holds its 8 or
+// 16 features of the row and of the gains. The sum of squares of row r's result
+// and that of row r + 1's f go through the team together, so a row costs one
+// barrier. With 16 features a thread the teams take rows in turn (131072 x 2048
+// in 322 us, with a run of rows each 354); with 8 a run each was better (104857 x
+// 640: 92 % of the copy bandwidth against 86).
 #include "residual_team.cuh"
 
 namespace attnres {
@@ -11,91 +14,126 @@ namespace {
 
 __device__ unsigned int g_timeout = 0;
 
-constexpr int kMaxWarps = 32;
+// 28 warps of 72 registers, or 16 of 128 for 16 features a thread: with 32 of 64
+// and 20 of 96 the spills cost more than the warps brought (131072 x 2048 in 364
+// us against 319).
+constexpr int max_warps(int vectors) { return vectors == 1 ? 28 : 16; }
+// Rows in flight per SM: with all of the 227 KB the reads crowd out the writes
+// (65536 x 1024 with an fp32 stream at 84 % of the copy bandwidth, with this 97).
+constexpr int kRingBytes = 146 * 1024;
 
-// F: the type of f and normed; X: of x and x_out.
-template <typename F, typename X, int GATE>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+// F: the type of f and normed; X: of x and x_out. GATE kNoGate also takes the
+// one gate row of all tokens, which then rides on the gain.
+template <typename F, typename X, int GATE, int VPT>
+__global__ void __launch_bounds__(max_warps(VPT) * 32, 1)
     residual_fast_kernel(ResidualArgs a, const __grid_constant__ TeamGeom g) {
   extern __shared__ __align__(128) unsigned char smem[];
   init_bars(g, smem);
-  Team m = make_team(g, a.T, smem);
+  Team m = make_team<VPT == 2 && GATE != kSharedGate>(g, a.T, smem);
   pdl_trigger();
   pdl_wait();
   fill_ring(m, g);
-  const int d = a.d, k = m.tid * 8;
-  const bool mine = k < d;
+  const int d = a.d, k0 = m.tid * 8, step = m.warps * 256;
   const float inv_d = 1.0f / static_cast<float>(d);
-  // Without a post-norm its gain is 1; scale rides on it.
-  V8 gpost = fill8(a.scale), gpre = fill8(0.f);
-  if (mine && a.gpost) gpost = mul8(ld8(a.gpost + k), a.scale);
-  if (mine && a.gpre) gpre = ld8(a.gpre + k);
-  // The shared gate row of the current token, and the first token of the next one.
-  int64_t group = 0, group_end = a.T;
-  V8 gate = fill8(1.f), unused;
-  if (GATE == kSharedGate) {
-    group = m.r0 / a.gate_rows;
-    if (a.gate_rows < a.T) group_end = (group + 1) * a.gate_rows;
-    if (mine && m.rows > 0) {
-      gate = ld8(a.gate, group * d + k, a.g_bf16);
-      activate8<false>(gate, unused, a.sigmoid);
+  V8 gain[VPT], gpre[VPT], f[VPT], x[VPT];
+  // scale * gamma_post (1 without a post-norm), with a shared gate times its value too.
+  auto load_gain = [&](int64_t group) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int k = k0 + v * step;
+      gain[v] = fill8(0.f);
+      if (k < d) {
+        gain[v] = a.gpost ? mul8(ld8(a.gpost + k), a.scale) : fill8(a.scale);
+        if (GATE != kTokenGate && a.gate) {
+          V8 gate = ld8(a.gate, group * d + k, a.g_bf16), unused;
+          activate8<false>(gate, unused, a.sigmoid);
+          gain[v] = mul8(gain[v], gate);
+        }
+      }
     }
+  };
+  if (GATE != kSharedGate) load_gain(0);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    gpre[v] = f[v] = fill8(0.f);
+    if (k0 + v * step < d && a.gpre) gpre[v] = ld8(a.gpre + k0 + v * step);
   }
 
-  // Waits for row r and takes its part of sum f^2.
+  // Waits for a row and takes its part of f and of sum f^2.
   int stage = 0;
   uint32_t parity = 0;
-  auto begin_row = [&](float* sum) {
+  auto begin_row = [&]() {
     const bool ok = mbar_wait(m.bars + stage * 8, parity);
-    if (ok && mine && a.gpost) {
-      const V8 f = ld8(reinterpret_cast<const F*>(m.ring + stage * g.stage_bytes + g.f) + k);
-      *sum = dot8(f, f);
+    float s = 0.f;
+    if (ok) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+        if (k0 + v * step < d) {
+          f[v] = ld8(reinterpret_cast<const F*>(m.ring + stage * g.stage_bytes + g.f) + k0 + v * step);
+          s += dot8(f[v], f[v]);
+        }
     }
-    return ok;
+    return ok ? s : -1.f;
   };
-  float s[2] = {0.f, 0.f};  // sum x_out^2 of a row, sum f^2 of the next
-  bool ok = m.rows == 0 || begin_row(&s[1]);
+  float s[2] = {0.f, m.rows == 0 ? 0.f : begin_row()};  // sum x_out^2 of a row, sum f^2 of the next
+  bool ok = !(s[1] < 0.f);
   ok = team_sum(m, s, 1, ok);
   if (!ok) give_up(m, g, 0, &g_timeout);
-  for (int r = 0; ok && r < m.rows; ++r) {
-    const int64_t row = m.r0 + r;
-    if (GATE == kSharedGate && row == group_end) {
-      ++group;
-      group_end += a.gate_rows;
-      if (mine) {
-        gate = ld8(a.gate, group * d + k, a.g_bf16);
-        activate8<false>(gate, unused, a.sigmoid);
+  // Runs of tokens with one gate row (without such rows: the one run).
+  for (int r = 0; ok && r < m.rows;) {
+    int run_end = m.rows;
+    if (GATE == kSharedGate) {
+      const int64_t group = (m.r0 + r) / a.gate_rows;
+      const int64_t end = (group + 1) * a.gate_rows - m.r0;
+      if (end < run_end) run_end = static_cast<int>(end);
+      load_gain(group);
+    }
+    for (; r < run_end; ++r) {
+      const int64_t row = (m.r0 + static_cast<int64_t>(r) * m.stride) * d;
+      const unsigned char* st = m.ring + stage * g.stage_bytes;
+      const float rf = a.gpost ? rsqrtf(s[1] * inv_d + a.eps_post) : 1.f;
+      s[0] = s[1] = 0.f;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int k = k0 + v * step;
+        if (k < d) {
+          x[v] = a.x ? ld8(reinterpret_cast<const X*>(st + g.x) + k) : fill8(0.f);
+          V8 w = mul8(gain[v], rf);
+          if (GATE == kTokenGate) {
+            V8 gate = ld8(st + g.gate, k, a.g_bf16), unused;
+            activate8<false>(gate, unused, a.sigmoid);
+            w = mul8(w, gate);
+          }
+          x[v] = fma8(w, f[v], x[v]);
+          st8(static_cast<X*>(a.x_out) + row + k, x[v]);
+          s[0] += dot8(x[v], x[v]);
+        }
+      }
+      if (++stage == m.nst) stage = 0, parity ^= 1u;
+      if (r + 1 < m.rows) s[1] = begin_row();
+      ok = !(s[1] < 0.f);
+      ok = team_sum(m, s, r & 1, ok);
+      if (!ok) {
+        give_up(m, g, r + 1, &g_timeout);
+        break;
+      }
+      // Every thread has what it needs of row r: its stage is free.
+      if (m.tid == 0 && m.issued < m.rows) issue_row(m, g);
+      if (a.normed) {
+        const float rx = rsqrtf(s[0] * inv_d + a.eps_pre);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          const int k = k0 + v * step;
+          if (k < d) st8(static_cast<F*>(a.normed) + row + k, mul8(mul8(gpre[v], rx), x[v]));
+        }
       }
     }
-    const unsigned char* st = m.ring + stage * g.stage_bytes;
-    V8 x = fill8(0.f);
-    const float rf = a.gpost ? rsqrtf(s[1] * inv_d + a.eps_post) : 1.f;
-    s[0] = s[1] = 0.f;
-    if (mine) {
-      const V8 f = ld8(reinterpret_cast<const F*>(st + g.f) + k);
-      if (a.x) x = ld8(reinterpret_cast<const X*>(st + g.x) + k);
-      V8 w = mul8(gpost, rf);
-      if (GATE == kTokenGate) {
-        gate = ld8(st + g.gate, k, a.g_bf16);
-        activate8<false>(gate, unused, a.sigmoid);
-      }
-      if (GATE != kNoGate) w = mul8(w, gate);
-      x = fma8(w, f, x);
-      st8(static_cast<X*>(a.x_out) + row * d + k, x);
-      s[0] = dot8(x, x);
-    }
-    if (++stage == m.nst) stage = 0, parity ^= 1u;
-    if (r + 1 < m.rows) ok = begin_row(&s[1]);
-    ok = team_sum(m, s, r & 1, ok);
-    if (!ok) {
-      give_up(m, g, r + 1, &g_timeout);
-      break;
-    }
-    // Every thread has what it needs of row r: its stage is free.
-    if (m.tid == 0 && m.issued < m.rows) issue_row(m, g);
-    if (a.normed && mine)
-      st8(static_cast<F*>(a.normed) + row * d + k, mul8(mul8(gpre, rsqrtf(s[0] * inv_d + a.eps_pre)), x));
   }
+}
+
+TeamShape shape_of(int d) {
+  const int v = d > 256 * max_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1;
+  return team_shape(d, v, max_warps(v));
 }
 
 bool geom_of(const ResidualArgs& a, TeamGeom* g) {
@@ -104,14 +142,15 @@ bool geom_of(const ResidualArgs& a, TeamGeom* g) {
   add_input(*g, a.f, a.d * es, &g->f);
   add_input(*g, a.x, a.d * xs, &g->x);
   add_input(*g, a.gate && a.gate_rows == 1 ? a.gate : nullptr, a.d * (a.g_bf16 ? 2 : 4), &g->gate);
-  return finish_geom(*g, team_shape(a.d, kMaxWarps), 0, 2);
+  return finish_geom(*g, shape_of(a.d), 0, 2, kRingBytes);
 }
 
-template <typename F, typename X>
+template <typename F, typename X, int VPT>
 cudaError_t launch_typed(const ResidualArgs& a, const TeamGeom& g, int64_t ctas, cudaStream_t s) {
-  if (!a.gate) return launch_teams(residual_fast_kernel<F, X, kNoGate>, g, ctas, s, a, g);
-  if (a.gate_rows == 1) return launch_teams(residual_fast_kernel<F, X, kTokenGate>, g, ctas, s, a, g);
-  return launch_teams(residual_fast_kernel<F, X, kSharedGate>, g, ctas, s, a, g);
+  if (!a.gate || (a.gate_rows >= a.T && a.gate_rows > 1))
+    return launch_teams(residual_fast_kernel<F, X, kNoGate, VPT>, g, ctas, s, a, g);
+  if (a.gate_rows == 1) return launch_teams(residual_fast_kernel<F, X, kTokenGate, VPT>, g, ctas, s, a, g);
+  return launch_teams(residual_fast_kernel<F, X, kSharedGate, VPT>, g, ctas, s, a, g);
 }
 
 }  // namespace
@@ -125,9 +164,14 @@ bool residual_fast_ok(const ResidualArgs& a) {
 cudaError_t launch_residual_fast(const ResidualArgs& a, cudaStream_t s) {
   TeamGeom g;
   if (!geom_of(a, &g)) return cudaErrorInvalidValue;
-  const int64_t ctas = team_ctas(a.T, team_shape(a.d, kMaxWarps), cta_cap());
-  if (!a.f_bf16) return launch_typed<float, float>(a, g, ctas, s);
-  return a.x_bf16 ? launch_typed<bf16, bf16>(a, g, ctas, s) : launch_typed<bf16, float>(a, g, ctas, s);
+  const TeamShape t = shape_of(a.d);
+  const int64_t ctas = team_ctas(a.T, t, cta_cap());
+  if (t.vectors == 1) {
+    if (!a.f_bf16) return launch_typed<float, float, 1>(a, g, ctas, s);
+    return a.x_bf16 ? launch_typed<bf16, bf16, 1>(a, g, ctas, s) : launch_typed<bf16, float, 1>(a, g, ctas, s);
+  }
+  if (!a.f_bf16) return launch_typed<float, float, 2>(a, g, ctas, s);
+  return a.x_bf16 ? launch_typed<bf16, bf16, 2>(a, g, ctas, s) : launch_typed<bf16, float, 2>(a, g, ctas, s);
 }
 
 cudaError_t take_timeout_residual_fwd(unsigned int* flag) {

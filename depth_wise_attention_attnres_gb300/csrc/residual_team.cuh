@@ -31,19 +31,26 @@ struct TeamGeom {
   int64_t withhold;
 };
 
-// Teams of a CTA of up to max_warps warps: 8 features a thread where a row then
-// fits in them, else 16.
+// How a CTA of up to max_warps warps is cut into teams whose threads take
+// 8 * vectors features of a row.
 struct TeamShape {
   int vectors, warps, teams;
 };
-inline TeamShape team_shape(int d, int max_warps) {
+inline TeamShape team_shape(int d, int vectors, int max_warps) {
   TeamShape s;
-  s.vectors = d <= max_warps * 256 ? 1 : 2;
-  s.warps = (d - 1) / (256 * s.vectors) + 1;
+  s.vectors = vectors;
+  s.warps = (d - 1) / (256 * vectors) + 1;
   s.teams = max_warps / s.warps;
   // Teams of several warps meet at named barriers, of which there are 15.
   if (s.warps > 1 && s.teams > 15) s.teams = 15;
   return s;
+}
+// 16 features a thread halve the cost of the sums over the team, where not too
+// many lanes idle: at a width that 8 features fill and 16 leave a third of the
+// lanes without work (d = 640) the gain is gone.
+inline bool sixteen_pay(int d) {
+  const int w1 = (d - 1) / 256 + 1, w2 = (d - 1) / 512 + 1;
+  return 10 * w1 > 15 * w2;  // fill(16) * 1.33 > fill(8), fills being d / (256 w1) and d / (512 w2)
 }
 inline int64_t team_ctas(int64_t T, const TeamShape& s, int64_t cap) {
   const int64_t want = (T - 1) / s.teams + 1;
@@ -59,13 +66,17 @@ inline void add_input(TeamGeom& g, const void* p, int bytes, int* at) {
   g.off[g.n++] = g.stage_bytes;
   g.stage_bytes += bytes;
 }
-// Splits the shared memory into the teams' rings; false if they cannot hold `least` rows.
-inline bool finish_geom(TeamGeom& g, const TeamShape& s, int gain_bytes, int least) {
+// Cuts the teams' rings out of `budget` bytes of shared memory, or of all of it
+// where the budget does not hold `least` rows; false if that does not either.
+inline bool finish_geom(TeamGeom& g, const TeamShape& s, int gain_bytes, int least, int budget) {
   g.warps = s.warps;
   g.teams = s.teams;
   g.gain = kGainOff;
   g.stages = kGainOff + gain_bytes;
-  g.nst = (kTeamSmem - g.stages) / (g.teams * g.stage_bytes);
+  const int most = (kTeamSmem - g.stages) / (g.teams * g.stage_bytes);
+  g.nst = budget / (g.teams * g.stage_bytes);
+  if (g.nst < least) g.nst = least;
+  if (g.nst > most) g.nst = most;
   if (g.nst > kMaxStages) g.nst = kMaxStages;
   g.total = g.stages + g.nst * g.teams * g.stage_bytes;
   g.withhold = withhold_for(kWithholdResidual);
@@ -126,6 +137,12 @@ __device__ __forceinline__ V8 mul8(const V8& a, const V8& b) {
   for (int i = 0; i < 4; ++i) r.p[i] = fmul2(a.p[i], b.p[i]);
   return r;
 }
+__device__ __forceinline__ V8 add8(const V8& a, const V8& b) {
+  V8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = make_float2(a.p[i].x + b.p[i].x, a.p[i].y + b.p[i].y);
+  return r;
+}
 __device__ __forceinline__ V8 mul8(const V8& a, float b) { return mul8(a, fill8(b)); }
 __device__ __forceinline__ V8 fma8(const V8& a, const V8& b, const V8& c) {
   V8 r;
@@ -180,10 +197,13 @@ struct Team {
   uint32_t bars;
   unsigned char* ring;
   int64_t r0;                  // first row
-  int rows;
+  int rows, stride;            // how many, and how far apart
   int issued, next;            // rows whose copies were started; the next one's stage (first thread only)
 };
 
+// The team's rows: a run of consecutive ones, or every so manyth one, with all
+// teams of the grid walking through the same stretch of memory.
+template <bool INTERLEAVED>
 __device__ __forceinline__ Team make_team(const TeamGeom& g, int64_t T, unsigned char* smem) {
   Team m;
   m.warps = g.warps;
@@ -195,8 +215,15 @@ __device__ __forceinline__ Team make_team(const TeamGeom& g, int64_t T, unsigned
   m.ring = smem + g.stages + static_cast<size_t>(m.team) * g.nst * g.stage_bytes;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * g.teams + m.team;
   const int64_t all = static_cast<int64_t>(gridDim.x) * g.teams;
-  m.r0 = T * id / all;
-  m.rows = static_cast<int>(T * (id + 1) / all - m.r0);
+  if (INTERLEAVED) {
+    m.r0 = id;
+    m.rows = T > id ? static_cast<int>((T - id - 1) / all + 1) : 0;
+    m.stride = static_cast<int>(all);
+  } else {
+    m.r0 = T * id / all;
+    m.rows = static_cast<int>(T * (id + 1) / all - m.r0);
+    m.stride = 1;
+  }
   m.issued = m.next = 0;
   return m;
 }
@@ -218,7 +245,7 @@ __device__ __forceinline__ void issue_row(Team& m, const TeamGeom& g) {
     const uint32_t bar = m.bars + s * 8, dst = smem_u32(m.ring) + s * g.stage_bytes;
     mbar_arrive_expect_tx(bar, g.stage_bytes);
     for (int i = 0; i < g.n; ++i)
-      bulk_g2s(dst + g.off[i], g.src[i] + (m.r0 + m.issued) * g.bytes[i], g.bytes[i], bar);
+      bulk_g2s(dst + g.off[i], g.src[i] + (m.r0 + static_cast<int64_t>(m.issued) * m.stride) * g.bytes[i], g.bytes[i], bar);
   }
   ++m.issued;
 }
