@@ -28,7 +28,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kUnit = 2048;        // elements
-constexpr int kMaxCtas = 304;      // partial sums of one launch
+constexpr int kMaxCtas = 456;      // partial sums of one launch
+// Resident CTAs of an SM that the two kernels are launched for.
+constexpr int kSumsPerSm = 3, kScalePerSm = 2;
 constexpr int kMaxTensors = 1024;  // of one launch: 29 KB of the 32,764 bytes of arguments
 
 template <int N>
@@ -104,9 +106,18 @@ __device__ __forceinline__ void sum_segment(Total& total, const T* p, int64_t n)
     for (int u = 0; u < kU; ++u) add_vec(s, p, x[u]);
     total.add(s);
   }
+  // The last batch is cut by predicates: its loads too are all in flight at once.
+  if (i < nv) {
+    uint4 x[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) x[u] = i + u * kThreads < nv ? v[i + u * kThreads] : make_uint4(0, 0, 0, 0);
+    Sums s{};
+#pragma unroll
+    for (int u = 0; u < kU; ++u) add_vec(s, p, x[u]);
+    total.add(s);
+  }
   Sums s{};
   if (threadIdx.x < head) add2(s, make_float2(to_f32(p[threadIdx.x]), 0.f));
-  for (; i < nv; i += kThreads) add_vec(s, p, v[i]);
   for (int64_t k = head + nv * kV + threadIdx.x; k < n; k += kThreads) add2(s, make_float2(to_f32(p[k]), 0.f));
   total.add(s);
 }
@@ -183,55 +194,52 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const float* part, 
   if (threadIdx.x == 0) norm[0] = r;
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    lds16(p, x);
-  } else {
-    float a[4], b[4];
-    lds16(p, a);
-    lds16(p + 4, b);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = a[i], x[i + 4] = b[i];
-  }
+// c times the elements of 16 bytes of source, stored in the destination's type.
+__device__ __forceinline__ void scale_vec(const float*, float* dst, uint4 v, float c) {
+  *reinterpret_cast<float4*>(dst) = make_float4(c * __uint_as_float(v.x), c * __uint_as_float(v.y),
+                                                c * __uint_as_float(v.z), c * __uint_as_float(v.w));
 }
-__device__ __forceinline__ void store8(bf16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                            pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ void scale_vec(const float*, bf16* dst, uint4 v, float c) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(c * __uint_as_float(v.x), c * __uint_as_float(v.y)),
+                                              pack_bf16x2(c * __uint_as_float(v.z), c * __uint_as_float(v.w)));
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void scale_vec(const bf16*, bf16* dst, uint4 v, float c) {
+  *reinterpret_cast<uint4*>(dst) =
+      make_uint4(pack_bf16x2(c * bf16_lo(v.x), c * bf16_hi(v.x)), pack_bf16x2(c * bf16_lo(v.y), c * bf16_hi(v.y)),
+                 pack_bf16x2(c * bf16_lo(v.z), c * bf16_hi(v.z)), pack_bf16x2(c * bf16_lo(v.w), c * bf16_hi(v.w)));
+}
+__device__ __forceinline__ void scale_vec(const bf16*, float* dst, uint4 v, float c) {
+  reinterpret_cast<float4*>(dst)[0] = make_float4(c * bf16_lo(v.x), c * bf16_hi(v.x), c * bf16_lo(v.y), c * bf16_hi(v.y));
+  reinterpret_cast<float4*>(dst)[1] = make_float4(c * bf16_lo(v.z), c * bf16_hi(v.z), c * bf16_lo(v.w), c * bf16_hi(v.w));
 }
 
 // Each thread reads and writes its own elements only: dst may be src.
 template <typename TI, typename TO>
 __device__ __forceinline__ void scale_segment(const TI* src, TO* dst, int64_t n, float c) {
+  constexpr int kV = 16 / sizeof(TI), kU = 8, kStep = kU * kThreads;
+  constexpr int kAlign = kV * sizeof(TO) < 16 ? kV * sizeof(TO) : 16;
   int64_t head = head_of(src, n);
-  if (reinterpret_cast<uintptr_t>(dst + head) & 15) head = n;  // no common boundary: element by element
-  const int64_t nv = (n - head) / 8;
+  if (reinterpret_cast<uintptr_t>(dst + head) % kAlign) head = n;  // no common boundary: element by element
+  const uint4* v = reinterpret_cast<const uint4*>(src + head);
+  TO* const out = dst + head;
+  const int64_t nv = (n - head) / kV;
   for (int64_t k = threadIdx.x; k < head; k += kThreads) dst[k] = from_f32<TO>(c * to_f32(src[k]));
-  constexpr int kU = 4;
+  for (int64_t k = head + nv * kV + threadIdx.x; k < n; k += kThreads) dst[k] = from_f32<TO>(c * to_f32(src[k]));
   int64_t i = threadIdx.x;
-  for (; i + (kU - 1) * kThreads < nv; i += kU * kThreads) {
-    float x[kU][8];
+  uint4 x[kU];
+  for (; i + (kU - 1) * kThreads < nv; i += kStep) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) load8(src + head + (i + u * kThreads) * 8, x[u]);
+    for (int u = 0; u < kU; ++u) x[u] = v[i + u * kThreads];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] *= c;
-      store8(dst + head + (i + u * kThreads) * 8, x[u]);
-    }
+    for (int u = 0; u < kU; ++u) scale_vec(src, out + (i + u * kThreads) * kV, x[u], c);
   }
-  for (; i < nv; i += kThreads) {
-    float x[8];
-    load8(src + head + i * 8, x);
+  if (i < nv) {  // the last batch
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= c;
-    store8(dst + head + i * 8, x);
+    for (int u = 0; u < kU; ++u) x[u] = i + u * kThreads < nv ? v[i + u * kThreads] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (i + u * kThreads < nv) scale_vec(src, out + (i + u * kThreads) * kV, x[u], c);
   }
-  for (int64_t k = head + nv * 8 + threadIdx.x; k < n; k += kThreads) dst[k] = from_f32<TO>(c * to_f32(src[k]));
 }
 
 template <int N>
@@ -275,8 +283,8 @@ uint32_t fill(Table<N>& t, const GradArgs& a, int* next) {
   return units;
 }
 
-unsigned ctas_for(uint32_t units) {
-  const unsigned cap = std::min<unsigned>(kMaxCtas, 2u * static_cast<unsigned>(sm_count()));
+unsigned ctas_for(uint32_t units, int per_sm) {
+  const unsigned cap = std::min<unsigned>(kMaxCtas, static_cast<unsigned>(per_sm * sm_count()));
   return std::min<unsigned>(units, cap);
 }
 
@@ -287,7 +295,7 @@ int run_table(const GradArgs& a, cudaStream_t s) {
   for (int next = 0; next < a.n;) {
     const uint32_t units = fill(t, a, &next);
     if (!units) break;
-    const unsigned grid = ctas_for(units);
+    const unsigned grid = ctas_for(units, kSumsPerSm);
     const int e = launch_step(
         [&] { return launch_pdl(grad_sums_kernel<N>, grid, kThreads, 0, s, t, a.scratch + 3 * parts); });
     if (e) return e;
@@ -298,7 +306,7 @@ int run_table(const GradArgs& a, cudaStream_t s) {
   for (int next = 0; next < a.n;) {
     const uint32_t units = fill(t, a, &next);
     if (!units) break;
-    const unsigned grid = ctas_for(units);
+    const unsigned grid = ctas_for(units, kScalePerSm);
     const int e = launch_step([&] {
       return launch_pdl(grad_scale_kernel<N>, grid, kThreads, 0, s, t, a.scratch, parts, a.max_norm, a.norm);
     });

@@ -265,34 +265,77 @@ __global__ void __launch_bounds__(kThreads) residual_bwd_rows_kernel(ResidualBwd
   }
 }
 
-// The last step of the sums over tokens: the partial rows of each kind added in
-// a fixed order, 32 runs of them at once (every 32nd) per feature.
+// The last step of the sums over tokens. The first blocks: the partial rows of
+// each kind wanted added in a fixed order, 32 runs of them at once (every 32nd)
+// for 32 features. Then, where runs of tokens share gate rows, the rows that
+// several teams had tokens of: the last part of the first such team and the
+// first parts of the others, in order (residual_bwd_join in residual.cuh says
+// which way the blocks are cut).
 __global__ void __launch_bounds__(1024)
-    residual_bwd_reduce_kernel(ResidualBwdArgs a, const float* part, int parts, int kinds) {
+    residual_bwd_reduce_kernel(ResidualBwdArgs a, const float* part, int parts, int kinds, int blocks, ResidualJoin j) {
   __shared__ float red[32][33];
   pdl_trigger();
   pdl_wait();
-  // The blockIdx.y-th of the kinds wanted: 0 dgamma_post, 1 dgamma_pre, 2 the gate.
-  const int which = blockIdx.y == 0 ? __ffs(kinds) - 1 : (blockIdx.y == 1 && kinds == 7 ? 1 : 31 - __clz(kinds));
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  float* const gain = which == 0 ? a.dgpost : a.dgpre;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * 32;
-  float s = 0.f;
-  // Without the norm its gain has no part in anything.
-  if (first + x < a.d && (which != 0 || a.gpost) && (which != 1 || a.dn)) {
-    const float* p = part + static_cast<int64_t>(which) * parts * a.d + first + x;
+  const int column_blocks = (a.d - 1) / 32 + 1;
+  if (static_cast<int>(blockIdx.x) < blocks) {
+    // The nth of the kinds: 0 dgamma_post, 1 dgamma_pre, 2 the gate.
+    const int nth = blockIdx.x / column_blocks;
+    const int which = nth == 0 ? __ffs(kinds) - 1 : (nth == 1 && kinds == 7 ? 1 : 31 - __clz(kinds));
+    float* const gain = which == 0 ? a.dgpost : a.dgpre;
+    const int64_t first = static_cast<int64_t>(blockIdx.x % column_blocks) * 32;
+    float s = 0.f;
+    // Without the norm its gain has no part in anything.
+    if (first + x < a.d && (which != 0 || a.gpost) && (which != 1 || a.dn)) {
+      const float* p = part + static_cast<int64_t>(which) * parts * a.d + first + x;
 #pragma unroll 5
-    for (int i = y; i < parts; i += 32) s += p[static_cast<int64_t>(i) * a.d];
+      for (int i = y; i < parts; i += 32) s += p[static_cast<int64_t>(i) * a.d];
+    }
+    red[y][x] = s;
+    __syncthreads();
+    s = warp_sum(red[x][y]);  // warp y: feature first + y
+    const int64_t k = first + y;
+    if (x != 0 || k >= a.d) return;
+    if (which == 2)
+      st(a.dgate, k, a.g_bf16, s);
+    else
+      gain[k] = a.accumulate ? gain[k] + s : s;
+    return;
   }
-  red[y][x] = s;
-  __syncthreads();
-  s = warp_sum(red[x][y]);  // warp y: feature first + y
-  const int64_t k = first + y;
-  if (x != 0 || k >= a.d) return;
-  if (which == 2)
-    st(a.dgate, k, a.g_bf16, s);
-  else
-    gain[k] = a.accumulate ? gain[k] + s : s;
+  const int64_t item = blockIdx.x - blocks;
+  const int64_t T = a.T, n = j.teams;
+  if (j.by_group) {
+    // A gate row and 32 features of it, 32 teams' parts at once.
+    const int64_t group = item / column_blocks, k = item % column_blocks * 32 + x;
+    const int64_t start = group * a.gate_rows, end = a.gate_rows < T - start ? start + a.gate_rows : T;
+    const int64_t first = ((start + 1) * n - 1) / T, last = (end * n - 1) / T;  // teams of its first and last token
+    if (first == last) return;
+    float s = 0.f;
+    if (k < a.d)
+      for (int64_t u = first + y; u <= last; u += 32)
+        if (T >= n || T * u / n < T * (u + 1) / n)  // a team without rows has written nothing
+          s += j.part[(u * 2 + (u == first ? 1 : 0)) * a.d + k];
+    red[y][x] = s;
+    __syncthreads();
+    s = warp_sum(red[x][y]);
+    const int64_t kk = item % column_blocks * 32 + y;
+    if (x == 0 && kk < a.d) st(a.dgate, group * a.d + kk, a.g_bf16, s);
+    return;
+  }
+  // A team and 1024 features, where that team's first row is the first token of
+  // its gate row outside the run of the team before.
+  const int wide_blocks = (a.d - 1) / 1024 + 1;
+  const int64_t t = item / wide_blocks + 1, k = item % wide_blocks * 1024 + threadIdx.x;
+  const int64_t row = T * t / n, group = row / a.gate_rows, start = group * a.gate_rows;
+  if (row == T * (t + 1) / n || start == row || k >= a.d) return;
+  const int64_t first = ((start + 1) * n - 1) / T;
+  if (T * (first + 1) / n != row) return;
+  const int64_t end = a.gate_rows < T - start ? start + a.gate_rows : T;
+  const int64_t last = (end * n - 1) / T;
+  float s = j.part[(first * 2 + 1) * a.d + k];
+  for (int64_t u = t; u <= last; ++u)
+    if (T >= n || T * u / n < T * (u + 1) / n) s += j.part[u * 2 * a.d + k];
+  st(a.dgate, group * a.d + k, a.g_bf16, s);
 }
 
 unsigned row_grid(int64_t T) {
@@ -300,12 +343,14 @@ unsigned row_grid(int64_t T) {
   return static_cast<unsigned>(T < cap ? T : cap);
 }
 
-int run_reduce(const ResidualBwdArgs& a, const float* part, int parts, cudaStream_t s) {
+int run_reduce(const ResidualBwdArgs& a, const float* part, int parts, const ResidualJoin& join, cudaStream_t s) {
   const int kinds = (a.dgpost ? 1 : 0) | (a.dgpre ? 2 : 0) | (residual_bwd_sums_gate(a) && parts > 0 ? 4 : 0);
-  if (!kinds) return ATTNRES_OK;
-  const unsigned n = (kinds & 1) + (kinds >> 1 & 1) + (kinds >> 2);
+  const int blocks = ((kinds & 1) + (kinds >> 1 & 1) + (kinds >> 2)) * ((a.d - 1) / 32 + 1);
+  const int64_t all = blocks + join.blocks;
+  if (!all) return ATTNRES_OK;
   return launch_step([&] {
-    return launch_pdl_grid(residual_bwd_reduce_kernel, dim3((a.d - 1) / 32 + 1, n), 1024, 0, s, a, part, parts, kinds);
+    return launch_pdl(residual_bwd_reduce_kernel, static_cast<unsigned>(all), 1024, 0, s, a, part, parts, kinds, blocks,
+                      join);
   });
 }
 
@@ -334,15 +379,13 @@ int run_bwd_generic(const ResidualBwdArgs& a, cudaStream_t s) {
     if (!e && (a.dx || a.df || (a.dgate && a.gate_rows == 1)))
       e = launch_step([&] { return launch_pdl(residual_bwd_rows_kernel, row_grid(a.T), kThreads, 0, s, a, stats); });
   }
-  if (!e && (a.T > 0 || !a.accumulate)) e = run_reduce(a, part, chunks, s);
+  if (!e && (a.T > 0 || !a.accumulate)) e = run_reduce(a, part, chunks, ResidualJoin{}, s);
   return e;
 }
 
 int run_bwd_fast(const ResidualBwdArgs& a, cudaStream_t s) {
-  int e = launch_step([&] { return launch_residual_bwd_fast(a, s); });
-  if (!e && residual_bwd_shares_gates(a)) e = launch_step([&] { return launch_residual_bwd_join_gate(a, s); });
-  if (!e) e = run_reduce(a, a.scratch, residual_bwd_parts(a), s);
-  return e;
+  const int e = launch_step([&] { return launch_residual_bwd_fast(a, s); });
+  return e ? e : run_reduce(a, a.scratch, residual_bwd_parts(a), residual_bwd_join(a), s);
 }
 
 }  // namespace

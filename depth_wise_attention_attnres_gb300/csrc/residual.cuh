@@ -35,6 +35,16 @@ inline bool residual_bwd_sums_gate(const ResidualBwdArgs& a) {
   return a.dgate && a.gate_rows > 1 && a.gate_rows >= a.T;
 }
 
+// How the gate rows whose tokens several teams had are summed from the teams'
+// parts ([teams][2][d]: of a row that began before the team's tokens, and of one
+// that goes on after them): a block for each gate row and 32 features, or where
+// there are more rows than teams for each team's first row and 1024 features.
+struct ResidualJoin {
+  const float* part = nullptr;
+  int64_t teams = 0, blocks = 0;
+  int by_group = 0;
+};
+
 // residual_fwd.cu, residual_bwd.cu
 bool residual_fast_ok(const ResidualArgs& a);
 bool residual_bwd_fast_ok(const ResidualBwdArgs& a);
@@ -42,6 +52,6 @@ int64_t residual_bwd_fast_scratch(int64_t T, int d, int64_t gate_rows);
 int residual_bwd_parts(const ResidualBwdArgs& a);
 cudaError_t launch_residual_fast(const ResidualArgs& a, cudaStream_t s);
 cudaError_t launch_residual_bwd_fast(const ResidualBwdArgs& a, cudaStream_t s);
-cudaError_t launch_residual_bwd_join_gate(const ResidualBwdArgs& a, cudaStream_t s);
+ResidualJoin residual_bwd_join(const ResidualBwdArgs& a);
 
 }  // namespace attnres

@@ -34,15 +34,15 @@ int gate_kind(int64_t T, int64_t gate_rows, bool gate) {
   if (!gate || (gate_rows > 1 && gate_rows >= T)) return kNoGate;
   return gate_rows == 1 ? kTokenGate : kSharedGate;
 }
-TeamShape norm_shape(int d) {
+TeamShape norm_shape(int64_t T, int d) {
   const int v = d > 256 * norm_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1;
-  return team_shape(d, v, norm_warps(v));
+  return team_shape(T, d, v, norm_warps(v));
 }
-TeamShape gated_shape(int d, int gate) {
-  return d <= 256 * gated_warps(gate) ? team_shape(d, 1, gated_warps(gate)) : team_shape(d, 2, kWideWarps);
+TeamShape gated_shape(int64_t T, int d, int gate) {
+  return d <= 256 * gated_warps(gate) ? team_shape(T, d, 1, gated_warps(gate)) : team_shape(T, d, 2, kWideWarps);
 }
 TeamShape shape_of(const ResidualBwdArgs& a) {
-  return a.f ? gated_shape(a.d, gate_kind(a.T, a.gate_rows, a.gate != nullptr)) : norm_shape(a.d);
+  return a.f ? gated_shape(a.T, a.d, gate_kind(a.T, a.gate_rows, a.gate != nullptr)) : norm_shape(a.T, a.d);
 }
 
 // 8 features of a gate row that tokens share: act(gate), and its slope.
@@ -434,38 +434,6 @@ __global__ void __launch_bounds__(kWideWarps * 32, 1)
                  GATE == kNoGate && a.gate && a.dgate, post, pre, gsum);
 }
 
-// Gate rows whose tokens lie in several teams' runs: the sums of those teams,
-// in order. A thread block takes a team and a block of features and acts if
-// the team's first row is the first of its gate row's tokens outside the run
-// of the team that has the row's first token.
-__global__ void __launch_bounds__(256)
-    residual_bwd_join_gate_kernel(ResidualBwdArgs a, const float* shared_part, int64_t teams) {
-  pdl_trigger();
-  pdl_wait();
-  const int64_t t = blockIdx.x + 1;
-  const int64_t k = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;
-  const int64_t row = a.T * t / teams;
-  const int64_t group = row / a.gate_rows, start = group * a.gate_rows;
-  if (row == a.T * (t + 1) / teams || start == row || k >= a.d) return;
-  const int64_t first = ((start + 1) * teams - 1) / a.T;  // the team with the row's first token
-  if (a.T * (first + 1) / teams != row) return;
-  const int64_t end = a.gate_rows < a.T - start ? start + a.gate_rows : a.T;
-  const int64_t last = (end * teams - 1) / a.T;           // and the one with its last
-  const float* part = shared_part + k;
-  float s = part[(first * 2 + 1) * a.d];
-  if (a.T >= teams) {
-#pragma unroll 8
-    for (int64_t u = t; u <= last; ++u) s += part[u * 2 * a.d];
-  } else {  // some teams have no rows, and have written nothing
-    for (int64_t u = t; u <= last; ++u)
-      if (a.T * u / teams < a.T * (u + 1) / teams) s += part[u * 2 * a.d];
-  }
-  if (a.g_bf16)
-    static_cast<bf16*>(a.dgate)[group * a.d + k] = from_f32<bf16>(s);
-  else
-    static_cast<float*>(a.dgate)[group * a.d + k] = s;
-}
-
 bool geom_of(const ResidualBwdArgs& a, TeamGeom* g) {
   *g = TeamGeom{};
   const int es = a.f_bf16 ? 2 : 4, xs = a.x_bf16 ? 2 : 4;
@@ -504,7 +472,7 @@ cudaError_t launch_typed(const ResidualBwdArgs& a, const Plan& p) {
 }
 template <typename F, typename G>
 cudaError_t launch_norm(const ResidualBwdArgs& a, const Plan& p) {
-  if (norm_shape(a.d).vectors > 1) return launch_teams(rmsnorm_bwd_kernel<F, G, 2>, p.g, p.ctas, p.s, a, p.g, p.sums);
+  if (norm_shape(a.T, a.d).vectors > 1) return launch_teams(rmsnorm_bwd_kernel<F, G, 2>, p.g, p.ctas, p.s, a, p.g, p.sums);
   return launch_teams(rmsnorm_bwd_kernel<F, G, 1>, p.g, p.ctas, p.s, a, p.g, p.sums);
 }
 
@@ -522,8 +490,8 @@ bool residual_bwd_fast_ok(const ResidualBwdArgs& a) {
 int64_t residual_bwd_fast_scratch(int64_t T, int d, int64_t gate_rows) {
   if (T == 0 || d % 8 != 0 || d > kMaxTeamD) return 0;
   const int gate = gate_kind(T, gate_rows, true);
-  TeamShape s = gated_shape(d, gate);
-  const TeamShape n = norm_shape(d);
+  TeamShape s = gated_shape(T, d, gate);
+  const TeamShape n = norm_shape(T, d);
   if (gate == kTokenGate && n.teams < s.teams) s = n;
   const int64_t ctas = team_ctas(T, s, kMaxCtas);
   return 3 * ctas * d + (gate == kSharedGate ? ctas * s.teams * 2 * d : 0);
@@ -552,12 +520,15 @@ cudaError_t launch_residual_bwd_fast(const ResidualBwdArgs& a, cudaStream_t s) {
   return a.dx_bf16 ? launch_typed<bf16, float, bf16>(a, p) : launch_typed<bf16, float, float>(a, p);
 }
 
-cudaError_t launch_residual_bwd_join_gate(const ResidualBwdArgs& a, cudaStream_t s) {
-  const int64_t ctas = residual_bwd_parts(a), teams = ctas * shape_of(a).teams;
-  const float* shared = a.scratch + 3 * ctas * a.d;
-  if (teams < 2) return cudaSuccess;
-  return launch_pdl_grid(residual_bwd_join_gate_kernel, dim3(static_cast<unsigned>(teams - 1), (a.d - 1) / 256 + 1), 256, 0,
-                         s, a, shared, teams);
+ResidualJoin residual_bwd_join(const ResidualBwdArgs& a) {
+  ResidualJoin j;
+  if (!residual_bwd_shares_gates(a)) return j;
+  const int64_t ctas = residual_bwd_parts(a), groups = (a.T - 1) / a.gate_rows + 1;
+  j.part = a.scratch + 3 * ctas * a.d;
+  j.teams = ctas * shape_of(a).teams;
+  j.by_group = groups < j.teams;
+  j.blocks = j.by_group ? groups * ((a.d - 1) / 32 + 1) : (j.teams - 1) * ((a.d - 1) / 1024 + 1);
+  return j;
 }
 
 cudaError_t take_timeout_residual_bwd(unsigned int* flag) {

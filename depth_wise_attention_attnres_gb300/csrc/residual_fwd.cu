@@ -131,9 +131,9 @@ __global__ void __launch_bounds__(max_warps(VPT) * 32, 1)
   }
 }
 
-TeamShape shape_of(int d) {
+TeamShape shape_of(int64_t T, int d) {
   const int v = d > 256 * max_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1;
-  return team_shape(d, v, max_warps(v));
+  return team_shape(T, d, v, max_warps(v));
 }
 
 bool geom_of(const ResidualArgs& a, TeamGeom* g) {
@@ -142,7 +142,7 @@ bool geom_of(const ResidualArgs& a, TeamGeom* g) {
   add_input(*g, a.f, a.d * es, &g->f);
   add_input(*g, a.x, a.d * xs, &g->x);
   add_input(*g, a.gate && a.gate_rows == 1 ? a.gate : nullptr, a.d * (a.g_bf16 ? 2 : 4), &g->gate);
-  return finish_geom(*g, shape_of(a.d), 0, 2, kRingBytes);
+  return finish_geom(*g, shape_of(a.T, a.d), 0, 2, kRingBytes);
 }
 
 template <typename F, typename X, int VPT>
@@ -164,7 +164,7 @@ bool residual_fast_ok(const ResidualArgs& a) {
 cudaError_t launch_residual_fast(const ResidualArgs& a, cudaStream_t s) {
   TeamGeom g;
   if (!geom_of(a, &g)) return cudaErrorInvalidValue;
-  const TeamShape t = shape_of(a.d);
+  const TeamShape t = shape_of(a.T, a.d);
   const int64_t ctas = team_ctas(a.T, t, cta_cap());
   if (t.vectors == 1) {
     if (!a.f_bf16) return launch_typed<float, float, 1>(a, g, ctas, s);

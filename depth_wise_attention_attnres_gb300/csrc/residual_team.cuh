@@ -36,13 +36,16 @@ struct TeamGeom {
 struct TeamShape {
   int vectors, warps, teams;
 };
-inline TeamShape team_shape(int d, int vectors, int max_warps) {
+inline TeamShape team_shape(int64_t T, int d, int vectors, int max_warps) {
   TeamShape s;
   s.vectors = vectors;
   s.warps = (d - 1) / (256 * vectors) + 1;
   s.teams = max_warps / s.warps;
   // Teams of several warps meet at named barriers, of which there are 15.
   if (s.warps > 1 && s.teams > 15) s.teams = 15;
+  // With few rows every SM gets a CTA before any gets a second team.
+  const int64_t each = T > 0 ? (T - 1) / kMaxCtas + 1 : 1;
+  if (s.teams > each) s.teams = static_cast<int>(each);
   return s;
 }
 // 16 features a thread halve the cost of the sums over the team, where not too
