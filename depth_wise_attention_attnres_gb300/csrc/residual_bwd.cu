@@ -19,7 +19,7 @@ __device__ unsigned int g_timeout = 0;
 // Warps of a CTA. The backward of RMSNorm: 28 of 72 registers, or 16 of 128 for
 // 16 features a thread. The gated one: 20 of 96, or 16 of 128 where runs of
 // tokens share gate rows; past the width that 8 features a thread cover its
-// threads take 16 and 128 registers.
+// threads take 16, and 128 registers.
 constexpr int norm_warps(int vectors) { return vectors == 1 ? 28 : 16; }
 constexpr int gated_warps(int gate) { return gate == kSharedGate ? 16 : 20; }
 constexpr int kWideWarps = 16;
@@ -175,10 +175,13 @@ __global__ void __launch_bounds__(norm_warps(VPT) * 32, 1)
   write_sums<VPT>(a, m, g, reinterpret_cast<float*>(smem + g.stages), sums, false, false, sum, sum, sum);
 }
 
-// F: the type of f, dnormed and df; X: of x_out; G: of dx_out and dx. GATE
-// kNoGate also takes the one gate row of all tokens, which rides on the gain.
-template <typename F, typename X, typename G, int GATE>
-__global__ void __launch_bounds__(gated_warps(GATE) * 32, 1)
+// The gated backward. F: the type of f, dnormed and df; X: of x_out; G: of
+// dx_out and dx. GATE kNoGate also takes the one gate row of all tokens, which
+// rides on the gain. VPT: 8 features a thread, with the gains in registers, or
+// for the widest rows 16 (one team a CTA), with the gains in shared memory and
+// rings that may hold a single row.
+template <typename F, typename X, typename G, int GATE, int VPT>
+__global__ void __launch_bounds__((VPT == 1 ? gated_warps(GATE) : kWideWarps) * 32, 1)
     residual_bwd_kernel(ResidualBwdArgs a, const __grid_constant__ TeamGeom g, float* sums, float* shared_part) {
   extern __shared__ __align__(128) unsigned char smem[];
   init_bars(g, smem);
@@ -186,21 +189,48 @@ __global__ void __launch_bounds__(gated_warps(GATE) * 32, 1)
   pdl_trigger();
   pdl_wait();
   fill_ring(m, g);
-  const int d = a.d, k = m.tid * 8;
-  const bool mine = k < d, post_norm = a.gpost != nullptr;
+  const int d = a.d, k0 = m.tid * 8, step = m.warps * 256;
+  const bool post_norm = a.gpost != nullptr;
   const float inv_d = 1.0f / static_cast<float>(d);
-  // scale * gamma_post, with a shared gate times its value too.
-  V8 gain = fill8(0.f), gpre = fill8(0.f), slope;
-  if (mine) {
-    if (GATE != kSharedGate) gain = scaled_gain(a, k);
-    if (GATE == kNoGate && a.gate) gain = mul8(gain, shared_act(a, 0, k, slope));
-    if (a.dn) gpre = ld8(a.gpre + k);
-  }
+  // scale * gamma_post, with a shared gate times its value too; gamma_pre; the
+  // sums over the tokens of earlier runs. What is in shared memory is each
+  // thread's own part.
+  V8 gain_reg = fill8(0.f), gpre_reg = fill8(0.f), slope;
+  auto kept = [&](int which) { return reinterpret_cast<float*>(smem + g.gain) + which * d; };
+  auto earlier = [&]() { return VPT == 1 ? kept(0) + static_cast<int>(threadIdx.x) / (g.warps * 32) * d : kept(2); };
+  auto gain = [&](int k) { return VPT == 1 ? gain_reg : ld8(kept(0) + k); };
+  auto gpre = [&](int k) { return VPT == 1 ? gpre_reg : ld8(kept(1) + k); };
+  auto set_gain = [&](int64_t group) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int k = k0 + v * step;
+      if (k < d) {
+        V8 c = scaled_gain(a, k);
+        if (GATE != kTokenGate && a.gate) c = mul8(c, shared_act(a, group, k, slope));
+        if (VPT == 1)
+          gain_reg = c;
+        else
+          st8(kept(0) + k, c);
+      }
+    }
+  };
+  if (GATE != kSharedGate) set_gain(0);
   // Sums over tokens: q D (with a gate per token act q D), of the current run of
-  // a shared gate row; dn u. Those of the runs before wait in shared memory.
-  V8 acc = fill8(0.f), pre[1] = {fill8(0.f)};
-  float* const earlier = reinterpret_cast<float*>(smem + g.gain) + m.team * d + k;
-  if (GATE == kSharedGate && mine) st8(earlier, acc);
+  // a shared gate row; dn u.
+  V8 acc[VPT], pre[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int k = k0 + v * step;
+    acc[v] = pre[v] = fill8(0.f);
+    if (k < d) {
+      const V8 c = a.dn ? ld8(a.gpre + k) : fill8(0.f);
+      if (VPT == 1)
+        gpre_reg = c;
+      else
+        st8(kept(1) + k, c);
+      if (GATE == kSharedGate) st8(earlier() + k, acc[v]);
+    }
+  }
 
   // Waits for a row and takes its part of sum x^2, sum h x and sum f^2.
   int stage = 0;
@@ -208,15 +238,21 @@ __global__ void __launch_bounds__(gated_warps(GATE) * 32, 1)
   float s[4] = {};  // those of a row, and last sum gamma_post dy q of the row before
   auto begin_row = [&]() {
     const bool ok = mbar_wait(m.bars + stage * 8, parity);
-    if (ok && mine) {
-      const unsigned char* st = m.ring + stage * g.stage_bytes;
-      if (a.dn) {
-        const V8 x = ld8(reinterpret_cast<const X*>(st + g.x) + k);
-        s[0] = dot8(x, x);
-        s[1] = dot8(mul8(gpre, ld8(reinterpret_cast<const F*>(st + g.dn) + k)), x);
+    const unsigned char* st = m.ring + stage * g.stage_bytes;
+    if (ok) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int k = k0 + v * step;
+        if (k < d) {
+          if (a.dn) {
+            const V8 x = ld8(reinterpret_cast<const X*>(st + g.x) + k);
+            s[0] += dot8(x, x);
+            s[1] += dot8(mul8(gpre(k), ld8(reinterpret_cast<const F*>(st + g.dn) + k)), x);
+          }
+          const V8 f = ld8(reinterpret_cast<const F*>(st + g.f) + k);
+          s[2] += dot8(f, f);
+        }
       }
-      const V8 f = ld8(reinterpret_cast<const F*>(st + g.f) + k);
-      s[2] = dot8(f, f);
     }
     return ok;
   };
@@ -230,208 +266,90 @@ __global__ void __launch_bounds__(gated_warps(GATE) * 32, 1)
       const int64_t group = (m.r0 + r) / a.gate_rows;
       const int64_t end = (group + 1) * a.gate_rows - m.r0;
       if (end < run_end) run_end = static_cast<int>(end);
-      if (mine) gain = mul8(scaled_gain(a, k), shared_act(a, group, k, slope));
+      set_gain(group);
     }
     for (; r < run_end; ++r) {
-      const int64_t at = (m.r0 + r) * d + k;
+      const int64_t row = (m.r0 + r) * d;
       const unsigned char* st = m.ring + stage * g.stage_bytes;
       const float rx = a.dn ? rsqrtf(s[0] * inv_d + a.eps_pre) : 0.f, mx = rx * (s[1] * inv_d);
       const float rf = post_norm ? rsqrtf(s[2] * inv_d + a.eps_post) : 1.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] = 0.f;
-      V8 q, t;  // t = gamma_post dy = scale gamma_post act D
-      if (mine) {
-        V8 D = a.dxo ? ld8(reinterpret_cast<const G*>(st + g.dxo) + k) : fill8(0.f);
-        if (a.dn) {
-          const V8 u = mul8(ld8(reinterpret_cast<const X*>(st + g.x) + k), rx);
-          const V8 h = ld8(reinterpret_cast<const F*>(st + g.dn) + k);
-          pre[0] = fma8(h, u, pre[0]);
-          D = fma8(fma8(u, -mx, mul8(gpre, h)), rx, D);
+      V8 q[VPT], t[VPT];  // t = gamma_post dy = scale gamma_post act D
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int k = k0 + v * step;
+        if (k < d) {
+          V8 D = a.dxo ? ld8(reinterpret_cast<const G*>(st + g.dxo) + k) : fill8(0.f);
+          if (a.dn) {
+            const V8 u = mul8(ld8(reinterpret_cast<const X*>(st + g.x) + k), rx);
+            const V8 h = ld8(reinterpret_cast<const F*>(st + g.dn) + k);
+            pre[v] = fma8(h, u, pre[v]);
+            D = fma8(fma8(u, -mx, mul8(gpre(k), h)), rx, D);
+          }
+          if (a.dx) st8(static_cast<G*>(a.dx) + row + k, D);
+          q[v] = mul8(ld8(reinterpret_cast<const F*>(st + g.f) + k), rf);
+          if (GATE == kTokenGate) {
+            V8 act = ld8(st + g.gate, k, a.g_bf16);
+            activate8<true>(act, slope, a.sigmoid);
+            const V8 qD = mul8(q[v], D), c = gain(k);
+            acc[v] = fma8(act, qD, acc[v]);
+            if (a.dgate) st8(a.dgate, row + k, a.g_bf16, mul8(slope, mul8(c, qD)));
+            t[v] = mul8(mul8(c, act), D);
+          } else {
+            acc[v] = fma8(q[v], D, acc[v]);
+            t[v] = mul8(gain(k), D);
+          }
+          s[3] += dot8(t[v], q[v]);
         }
-        if (a.dx) st8(static_cast<G*>(a.dx) + at, D);
-        q = mul8(ld8(reinterpret_cast<const F*>(st + g.f) + k), rf);
-        if (GATE == kTokenGate) {
-          V8 act = ld8(st + g.gate, k, a.g_bf16);
-          activate8<true>(act, slope, a.sigmoid);
-          const V8 qD = mul8(q, D);
-          acc = fma8(act, qD, acc);
-          if (a.dgate) st8(a.dgate, at, a.g_bf16, mul8(slope, mul8(gain, qD)));
-          t = mul8(mul8(gain, act), D);
-        } else {
-          acc = fma8(q, D, acc);
-          t = mul8(gain, D);
-        }
-        s[3] = dot8(t, q);
       }
       if (++stage == m.nst) stage = 0, parity ^= 1u;
-      if (r + 1 < m.rows) ok = begin_row();
+      if (r + 1 < m.rows) {
+        if (VPT > 1 && m.nst == 1) {  // a ring of one row: the next one comes when all are past this one
+          team_sync(m);
+          if (m.tid == 0) issue_row(m, g);
+        }
+        ok = begin_row();
+      }
       ok = team_sum(m, s, r & 1, ok);
       if (!ok) {
         give_up(m, g, r + 1, &g_timeout);
         break;
       }
       // Every thread has what it needs of row r: its stage is free.
-      if (m.tid == 0 && m.issued < m.rows) issue_row(m, g);
-      if (mine && a.df)
-        st8(static_cast<F*>(a.df) + at, post_norm ? mul8(fma8(q, -(s[3] * inv_d), t), rf) : t);
-    }
-    if (GATE == kSharedGate && mine) {
-      const V8 post = flush_gate(a, m, shared_part, g.teams, (m.r0 + run_end - 1) / a.gate_rows, k, acc);
-      st8(earlier, add8(ld8(earlier), post));
-      acc = fill8(0.f);
-    }
-  }
-  V8 post[1] = {acc}, gate[1] = {acc};
-  if (mine) {
-    if (GATE == kSharedGate) post[0] = ld8(earlier);
-    if (GATE == kNoGate && a.gate) post[0] = flush_gate(a, m, nullptr, g.teams, 0, k, gate[0]);
-  }
-  write_sums<1>(a, m, g, reinterpret_cast<float*>(smem + g.stages), sums, post_norm && a.dgpost,
-                GATE == kNoGate && a.gate && a.dgate, post, pre, gate);
-}
-
-// The gated backward of wider rows: 16 features a thread, so only D and the
-// sums over tokens stay in registers; the row is read from its stage again in
-// each step, and the gains from shared memory. A stage is refilled after the
-// next row's first sum, when every thread is past its last read of it.
-template <int GATE>
-__global__ void __launch_bounds__(kWideWarps * 32, 1)
-    residual_bwd_wide_kernel(ResidualBwdArgs a, const __grid_constant__ TeamGeom g, float* sums, float* shared_part) {
-  constexpr int kV = 2;
-  extern __shared__ __align__(128) unsigned char smem[];
-  init_bars(g, smem);
-  Team m = make_team<false>(g, a.T, smem);
-  pdl_trigger();
-  pdl_wait();
-  fill_ring(m, g);
-  const int d = a.d, step = m.warps * 256;
-  const bool post_norm = a.gpost != nullptr;
-  const float inv_d = 1.0f / static_cast<float>(d);
-  float* gains = reinterpret_cast<float*>(smem + g.gain);  // scale * gamma_post, gamma_pre
-  for (int k = threadIdx.x; k < d; k += blockDim.x) {
-    gains[k] = post_norm ? a.gpost[k] * a.scale : a.scale;
-    gains[d + k] = a.dn ? a.gpre[k] : 0.f;
-  }
-  __syncthreads();
-  if (GATE == kNoGate && a.gate) {  // one row for all tokens
-    for (int k = threadIdx.x * 8; k < d; k += blockDim.x * 8) {
-      V8 slope;
-      st8(gains + k, mul8(ld8(gains + k), shared_act(a, 0, k, slope)));
-    }
-    __syncthreads();
-  }
-  int64_t group = 0, group_end = a.T;
-  if (GATE == kSharedGate) {
-    group = m.r0 / a.gate_rows;
-    if (a.gate_rows < a.T) group_end = (group + 1) * a.gate_rows;
-  }
-  V8 post[kV], pre[kV], gsum[kV];
+      if ((VPT == 1 || m.nst > 1) && m.tid == 0 && m.issued < m.rows) issue_row(m, g);
+      if (a.df)
 #pragma unroll
-  for (int v = 0; v < kV; ++v) post[v] = pre[v] = gsum[v] = fill8(0.f);
-
-  int stage = 0;
-  uint32_t parity = 0;
-  for (int r = 0; r < m.rows; ++r) {
-    const int64_t row = m.r0 + r;
-    if (GATE == kSharedGate && row == group_end) {
-      ++group;
-      group_end += a.gate_rows;
+        for (int v = 0; v < VPT; ++v) {
+          const int k = k0 + v * step;
+          if (k < d)
+            st8(static_cast<F*>(a.df) + row + k, post_norm ? mul8(fma8(q[v], -(s[3] * inv_d), t[v]), rf) : t[v]);
+        }
     }
-    const unsigned char* st = m.ring + stage * g.stage_bytes;
-    bool ok = mbar_wait(m.bars + stage * 8, parity);
-    if (++stage == m.nst) stage = 0, parity ^= 1u;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (ok) {
+    if (GATE == kSharedGate) {
 #pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        const int k = v * step + m.tid * 8;
+      for (int v = 0; v < VPT; ++v) {
+        const int k = k0 + v * step;
         if (k < d) {
-          if (a.dn) {
-            const V8 x = ld8(st + g.x, k, a.x_bf16);
-            s[0] += dot8(x, x);
-            s[1] += dot8(mul8(ld8(gains + d + k), ld8(st + g.dn, k, a.f_bf16)), x);
-          }
-          if (post_norm) {
-            const V8 f = ld8(st + g.f, k, a.f_bf16);
-            s[2] += dot8(f, f);
-          }
+          const V8 post = flush_gate(a, m, shared_part, g.teams, (m.r0 + run_end - 1) / a.gate_rows, k, acc[v]);
+          st8(earlier() + k, add8(ld8(earlier() + k), post));
+          acc[v] = fill8(0.f);
         }
       }
-    }
-    ok = team_sum(m, s, 0, ok);
-    if (!ok) {
-      give_up(m, g, r, &g_timeout);
-      break;
-    }
-    if (m.tid == 0 && r > 0 && m.nst > 1 && m.issued < m.rows) issue_row(m, g);
-    const float rx = a.dn ? rsqrtf(s[0] * inv_d + a.eps_pre) : 0.f, mx = rx * (s[1] * inv_d);
-    const float rf = post_norm ? rsqrtf(s[2] * inv_d + a.eps_post) : 1.f;
-    // act(gate) at 8 features, and a token's own gate's slope.
-    auto act_at = [&](V8& slope, int k) {
-      if (GATE == kSharedGate) return shared_act(a, group, k, slope);
-      if (GATE == kNoGate) return fill8(1.f);
-      V8 act = ld8(st + g.gate, k, a.g_bf16);
-      activate8<true>(act, slope, a.sigmoid);
-      return act;
-    };
-
-    V8 D[kV], slope;
-    float q[1] = {0.f};
-#pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      const int k = v * step + m.tid * 8;
-      if (k < d) {
-        D[v] = a.dxo ? ld8(st + g.dxo, k, a.dx_bf16) : fill8(0.f);
-        if (a.dn) {
-          const V8 x = mul8(ld8(st + g.x, k, a.x_bf16), rx), h = ld8(st + g.dn, k, a.f_bf16);
-          pre[v] = fma8(h, x, pre[v]);
-          D[v] = fma8(fma8(x, -mx, mul8(ld8(gains + d + k), h)), rx, D[v]);
-        }
-        if (a.dx) st8(a.dx, row * d + k, a.dx_bf16, D[v]);
-        if (post_norm)
-          q[0] += dot8(mul8(ld8(gains + k), mul8(act_at(slope, k), D[v])), mul8(ld8(st + g.f, k, a.f_bf16), rf));
-      }
-    }
-    (void)team_sum(m, q, 1, true);
-    const float mf = post_norm ? q[0] * inv_d : 0.f;
-#pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      const int k = v * step + m.tid * 8;
-      if (k < d) {
-        const V8 f = mul8(ld8(st + g.f, k, a.f_bf16), rf), c = ld8(gains + k), qD = mul8(f, D[v]);
-        const V8 act = act_at(slope, k);
-        if (GATE == kSharedGate) {
-          gsum[v] = fma8(f, D[v], gsum[v]);
-        } else {
-          post[v] = fma8(act, qD, post[v]);
-          if (GATE == kTokenGate && a.dgate) st8(a.dgate, row * d + k, a.g_bf16, mul8(slope, mul8(c, qD)));
-        }
-        if (a.df) {
-          const V8 t = mul8(mul8(c, act), D[v]);
-          st8(a.df, row * d + k, a.f_bf16, post_norm ? mul8(fma8(f, -mf, t), rf) : t);
-        }
-        if (GATE == kSharedGate && (r + 1 == m.rows || row + 1 == group_end)) {
-          post[v] = add8(post[v], flush_gate(a, m, shared_part, g.teams, group, k, gsum[v]));
-          gsum[v] = fill8(0.f);
-        }
-      }
-    }
-    // A ring of one stage: the next row's copies start when all are done with this one.
-    if (m.nst == 1 && r + 1 < m.rows) {
-      team_sync(m);
-      if (m.tid == 0) issue_row(m, g);
     }
   }
-  if (GATE == kNoGate && a.gate) {
+  V8 post[VPT], gate[VPT];
 #pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      const int k = v * step + m.tid * 8;
-      gsum[v] = post[v];
-      if (k < d) post[v] = flush_gate(a, m, nullptr, g.teams, 0, k, gsum[v]);
+  for (int v = 0; v < VPT; ++v) {
+    const int k = k0 + v * step;
+    post[v] = gate[v] = acc[v];
+    if (k < d) {
+      if (GATE == kSharedGate) post[v] = ld8(earlier() + k);
+      if (GATE == kNoGate && a.gate) post[v] = flush_gate(a, m, nullptr, g.teams, 0, k, gate[v]);
     }
   }
-  write_sums<kV>(a, m, g, reinterpret_cast<float*>(smem + g.stages), sums, post_norm && a.dgpost,
-                 GATE == kNoGate && a.gate && a.dgate, post, pre, gsum);
+  write_sums<VPT>(a, m, g, reinterpret_cast<float*>(smem + g.stages), sums, post_norm && a.dgpost,
+                  GATE == kNoGate && a.gate && a.dgate, post, pre, gate);
 }
 
 bool geom_of(const ResidualBwdArgs& a, TeamGeom* g) {
@@ -445,11 +363,8 @@ bool geom_of(const ResidualBwdArgs& a, TeamGeom* g) {
   const TeamShape s = shape_of(a);
   // Past 8 features a thread the gated kernel's gains, and where runs of tokens
   // share gate rows the sums of earlier runs.
-  int gain_bytes = 0;
-  if (a.f && s.vectors > 1)
-    gain_bytes = 8 * a.d;
-  else if (a.f && gate_kind(a.T, a.gate_rows, a.gate != nullptr) == kSharedGate)
-    gain_bytes = 4 * s.teams * a.d;
+  int gain_bytes = a.f && s.vectors > 1 ? 8 * a.d : 0;
+  if (a.f && gate_kind(a.T, a.gate_rows, a.gate != nullptr) == kSharedGate) gain_bytes += 4 * s.teams * a.d;
   // The teams' sums go through the rings' space: 4 bytes a feature and team.
   return finish_geom(*g, s, gain_bytes, a.f && s.vectors > 1 ? 1 : 2, a.f ? kGatedRing : kNormRing) && g->nst * g->stage_bytes >= 4 * a.d;
 }
@@ -463,12 +378,16 @@ struct Plan {
   int gate;
 };
 
+template <typename F, typename X, typename G, int GATE>
+cudaError_t launch_gate(const ResidualBwdArgs& a, const Plan& p) {
+  if (shape_of(a).vectors > 1)
+    return launch_teams(residual_bwd_kernel<F, X, G, GATE, 2>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  return launch_teams(residual_bwd_kernel<F, X, G, GATE, 1>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+}
 template <typename F, typename X, typename G>
 cudaError_t launch_typed(const ResidualBwdArgs& a, const Plan& p) {
-  if (p.gate == kNoGate) return launch_teams(residual_bwd_kernel<F, X, G, kNoGate>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
-  if (p.gate == kTokenGate)
-    return launch_teams(residual_bwd_kernel<F, X, G, kTokenGate>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
-  return launch_teams(residual_bwd_kernel<F, X, G, kSharedGate>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  if (p.gate == kNoGate) return launch_gate<F, X, G, kNoGate>(a, p);
+  return p.gate == kTokenGate ? launch_gate<F, X, G, kTokenGate>(a, p) : launch_gate<F, X, G, kSharedGate>(a, p);
 }
 template <typename F, typename G>
 cudaError_t launch_norm(const ResidualBwdArgs& a, const Plan& p) {
@@ -508,12 +427,6 @@ cudaError_t launch_residual_bwd_fast(const ResidualBwdArgs& a, cudaStream_t s) {
   if (!a.f) {
     if (!a.f_bf16) return launch_norm<float, float>(a, p);
     return a.dx_bf16 ? launch_norm<bf16, bf16>(a, p) : launch_norm<bf16, float>(a, p);
-  }
-  if (shape_of(a).vectors > 1) {
-    if (p.gate == kNoGate) return launch_teams(residual_bwd_wide_kernel<kNoGate>, p.g, p.ctas, s, a, p.g, p.sums, p.shared);
-    if (p.gate == kTokenGate)
-      return launch_teams(residual_bwd_wide_kernel<kTokenGate>, p.g, p.ctas, s, a, p.g, p.sums, p.shared);
-    return launch_teams(residual_bwd_wide_kernel<kSharedGate>, p.g, p.ctas, s, a, p.g, p.sums, p.shared);
   }
   if (!a.f_bf16) return launch_typed<float, float, float>(a, p);
   if (a.x_bf16) return a.dx_bf16 ? launch_typed<bf16, bf16, bf16>(a, p) : launch_typed<bf16, bf16, float>(a, p);
