@@ -157,10 +157,10 @@ def _slices(t: torch.Tensor) -> tuple[int, int, int, int]:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device: int | None = None) -> int | None:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -363,7 +363,11 @@ def _like(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: 
 
 
 def _opt(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, device: int) -> int | None:
-    return None if t is None else _like(name, t, shape, dtype, device)
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    return _like(name, t, shape, dtype, device)  # says what is wrong
 
 
 def _two_dims(name: str, t: torch.Tensor) -> torch.Size:
@@ -411,7 +415,7 @@ def attnres_gated_residual(f: torch.Tensor, x: torch.Tensor | None, gamma_post: 
         _opt("gamma_post", gamma_post, (d,), f32, device), eps_post, gptr, gate_rows, gcode, gate_act, scale, T, d,
         _dtype(f), _dtype(x_out), _like("x_out", x_out, shape, xt, device),
         _opt("gamma_pre", gamma_pre, (d,), f32, device), eps_pre, _opt("normed", normed, shape, dt, device),
-        _stream(stream)))
+        _stream(stream, device)))
     return x_out
 
 
@@ -455,7 +459,7 @@ def attnres_gated_residual_bwd(f: torch.Tensor, gamma_post: torch.Tensor | None,
         _opt("dx", dx, shape, gt, device),
         None if dgate is None else _like("dgate", dgate, gate.shape, gate.dtype, device),
         _opt("dgamma_post", dgamma_post, (d,), f32, device), _opt("dgamma_pre", dgamma_pre, (d,), f32, device),
-        1 if accumulate else 0, scratch.data_ptr(), scratch.numel(), _stream(stream)))
+        1 if accumulate else 0, scratch.data_ptr(), scratch.numel(), _stream(stream, device)))
 
 
 def attnres_rmsnorm_bwd_scratch_floats(T: int, d: int) -> int:
@@ -477,7 +481,7 @@ def attnres_rmsnorm_bwd(x: torch.Tensor, gamma: torch.Tensor, eps: float, dy: to
         _like("x", x, shape, dt, device), T, d, _dtype(x), _like("gamma", gamma, (d,), f32, device), eps,
         _like("dy", dy, shape, dt, device), _opt("dres", dres, shape, gt, device), _dtype(dx),
         _like("dx", dx, shape, gt, device), _opt("dgamma", dgamma, (d,), f32, device), 1 if accumulate else 0,
-        scratch.data_ptr(), scratch.numel(), _stream(stream)))
+        scratch.data_ptr(), scratch.numel(), _stream(stream, device)))
     return dx
 
 
@@ -517,8 +521,8 @@ class GradList:
         self.scratch_floats = attnres_grad_norm_scratch_floats(n)
 
 
-def _grad_call(grads, outs, norm, scratch, stream) -> tuple[GradList, torch.Tensor]:
-    """The list, its scratch and checks of a gradient call."""
+def _grad_call(grads, outs, norm, scratch, stream) -> tuple[GradList, torch.Tensor, int]:
+    """The list, its scratch, checks of a gradient call, and the stream."""
     if not isinstance(grads, GradList):
         grads = GradList(grads, outs)
     elif outs is not None:
@@ -530,7 +534,7 @@ def _grad_call(grads, outs, norm, scratch, stream) -> tuple[GradList, torch.Tens
         raise ValueError("norm must be one fp32 element on the current CUDA device")
     if scratch is not None and scratch.numel() < grads.scratch_floats:
         raise ValueError(f"scratch must hold at least {grads.scratch_floats} elements")
-    return grads, _scratch(scratch, lambda: grads.scratch_floats, device, stream)
+    return grads, _scratch(scratch, lambda: grads.scratch_floats, device, stream), _stream(stream, device)
 
 
 def attnres_grad_norm_scratch_floats(n: int) -> int:
@@ -540,10 +544,10 @@ def attnres_grad_norm_scratch_floats(n: int) -> int:
 
 def attnres_grad_norm(grads, norm: torch.Tensor, scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """norm (fp32, one element) = sqrt of the sum of squares of every element of a list of tensors or a GradList."""
-    grads, scratch = _grad_call(grads, None, norm, scratch, stream)
+    grads, scratch, handle = _grad_call(grads, None, norm, scratch, stream)
     _check("attnres_grad_norm", (_lib or lib()).attnres_grad_norm(
         grads.pointers, grads.counts, grads.codes, grads.n, norm.data_ptr(), scratch.data_ptr(), scratch.numel(),
-        _stream(stream)))
+        handle))
     return norm
 
 
@@ -552,10 +556,10 @@ def attnres_grad_clip(grads, max_norm: float, norm: torch.Tensor, outs=None, scr
     """The gradients times max_norm / norm where their norm (returned in `norm`, before clipping) is finite and
     above max_norm, else times 1: in place, or into `outs` (fp32 or bf16, all elements written; a GradList holds
     its own)."""
-    grads, scratch = _grad_call(grads, outs, norm, scratch, stream)
+    grads, scratch, handle = _grad_call(grads, outs, norm, scratch, stream)
     _check("attnres_grad_clip", (_lib or lib()).attnres_grad_clip(
         grads.pointers, grads.counts, grads.codes, grads.out_pointers, grads.out_codes, grads.n, max_norm,
-        norm.data_ptr(), scratch.data_ptr(), scratch.numel(), _stream(stream)))
+        norm.data_ptr(), scratch.data_ptr(), scratch.numel(), handle))
     return norm
 
 

@@ -15,6 +15,7 @@
 
 #include "attnres.h"
 #include "internal.h"
+#include "residual.cuh"
 
 namespace attnres {
 
@@ -1240,6 +1241,29 @@ int attnres_kernel_path(int32_t op, const void* src, const void* out, int32_t n_
     case 4:
       if (dtype != ATTNRES_BF16) return -1;
       return proj_path(src, src, reinterpret_cast<const float*>(out), T, d);
+    case 5: {
+      const int b = dtype == ATTNRES_BF16;
+      void* o = const_cast<void*>(out);
+      return residual_fast_ok(ResidualArgs{src, src, src, 1, wp, wp, 0.f, 0.f, 1.f, T, d, b, b, b, 0, o, o}) ? 1 : 0;
+    }
+    case 6:
+    case 7: {
+      const int b = dtype == ATTNRES_BF16;
+      ResidualBwdArgs a{};
+      a.gate_rows = 1;
+      a.xo = a.dxo = a.dn = src;
+      a.gpre = wp;
+      a.T = T;
+      a.d = d;
+      a.f_bf16 = a.x_bf16 = a.g_bf16 = a.dx_bf16 = b;
+      a.dx = const_cast<void*>(out);
+      if (op == 6) {
+        a.f = a.gate = src;
+        a.gpost = wp;
+        a.df = a.dgate = a.dx;
+      }
+      return residual_bwd_fast_ok(a) ? 1 : 0;
+    }
     default: return -1;
   }
 }

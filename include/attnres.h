@@ -684,7 +684,9 @@ const char* attnres_status_string(int32_t status);
 /*
  * attnres_kernel_path - which kernel a call with these arguments would use:
  * 1 = the fast kernel, 0 = the general kernel, negative = invalid arguments.
- * op: 0 full read, 1 stage 1, 2 merge, 3 accumulate, 4 query projection
+ * op: 0 full read, 1 stage 1, 2 merge, 3 accumulate, 5 gated residual, 6 its
+ * backward (5 and 6: every array at src or out and of dtype, all of them given,
+ * a gate per token; scratch at out), 7 the RMSNorm backward, 4 query projection
  * (attnres_query_projection with H = Wq = src and Q = out; dtype must be
  * ATTNRES_BF16): 2 = tensor-core tiles shared by pairs of CTAs, 1 = tensor-core
  * tiles of one CTA, 0 = another kernel. Pointers are only inspected for

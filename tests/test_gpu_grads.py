@@ -238,3 +238,16 @@ def test_refusals():
         ar.attnres_grad_norm([g], norm, scratch=torch.empty(3, device=dev()))
     with pytest.raises(ar.AttnResError):
         ar.attnres_grad_clip([g], -1.0, norm)
+
+
+def test_a_tensor_past_32_bit_offsets():
+    n = (1 << 31) + 12345
+    t = torch.zeros(n, device=dev(), dtype=torch.bfloat16)
+    t[-3:], t[5] = 2.0, 1.0
+    norm = torch.empty(1, device=dev())
+    ar.attnres_grad_clip([t], 1.0, norm)
+    want = math.sqrt(13.0)
+    assert abs(float(norm) - want) <= norm_bound() * want
+    ref.check(t[-3:], torch.full((3,), 2.0 / want, dtype=torch.float64, device=dev()),
+              torch.full((3,), 40 * U, dtype=torch.float64, device=dev()), "clipped")
+    assert int((t != 0).sum()) == 4

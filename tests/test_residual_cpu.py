@@ -225,3 +225,17 @@ def test_grad_norm_refusals(lib):
 def test_binding_refuses_cpu_tensors(lib):
     with pytest.raises(ValueError):
         binding.GradList([torch.zeros(4)])
+
+
+def test_kernel_selection(lib):
+    A = 1 << 20
+    for op in (5, 6, 7):
+        for dt in (0, 1):
+            for d in (8, 256, 640, 896, 1024, 2048, 5120):
+                assert binding.attnres_kernel_path(op, A, 2 * A, 0, 0, 8192, d, dt) == 1, (op, d, dt)
+        assert binding.attnres_kernel_path(op, A, 2 * A, 0, 0, 8192, 8192, 1) == 1
+        assert binding.attnres_kernel_path(op, A + 8, 2 * A, 0, 0, 8192, 640, 1) == 0     # unaligned rows
+        assert binding.attnres_kernel_path(op, A, 2 * A, 0, 0, 8192, 100, 1) == 0         # d % 8
+        assert binding.attnres_kernel_path(op, A, 2 * A, 0, 0, 8192, 8200, 1) == 0        # wider than a CTA's teams
+    # Five fp32 arrays of 8192 features and the gains do not fit in an SM's shared memory.
+    assert binding.attnres_kernel_path(6, A, 2 * A, 0, 0, 8192, 8192, 0) == 0
