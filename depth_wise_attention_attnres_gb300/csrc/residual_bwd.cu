@@ -16,13 +16,14 @@ namespace {
 
 __device__ unsigned int g_timeout = 0;
 
-// Warps of a CTA. The backward of RMSNorm: 28 of 72 registers, or 16 of 128 for
-// 16 features a thread. The gated one: 20 of 96, or 16 of 128 where runs of
+// Warps of a CTA. The backward of RMSNorm: 28 of 72 registers, 16 of 128 for
+// 16 features a thread, 12 of 168 for 24. The gated one: 20 of 96, or 16 of 128 where runs of
 // tokens share gate rows; past the width that 8 features a thread cover its
 // threads take 16, and 128 registers.
-constexpr int norm_warps(int vectors) { return vectors == 1 ? 28 : 16; }
-constexpr int gated_warps(int gate) { return gate == kSharedGate ? 16 : 20; }
-constexpr int kWideWarps = 16;
+constexpr int norm_warps(int vectors) { return vectors == 1 ? 28 : vectors == 2 ? 16 : 12; }
+constexpr int gated_warps(int gate, int vectors) {
+  return vectors == 3 ? 8 : vectors == 2 || gate == kSharedGate ? 16 : 20;
+}
 // Rows in flight per SM (as the forward's: the rings of the RMSNorm backward
 // are held to what left the writes room; the gated one, with more arithmetic to
 // cover, lost by it).
@@ -34,12 +35,17 @@ int gate_kind(int64_t T, int64_t gate_rows, bool gate) {
   if (!gate || (gate_rows > 1 && gate_rows >= T)) return kNoGate;
   return gate_rows == 1 ? kTokenGate : kSharedGate;
 }
+// Where three warps of 8 features a thread would idle, one warp takes the row
+// with 24 (104857 x 640 bf16 at 77 % of the copy bandwidth, with three 51).
 TeamShape norm_shape(int64_t T, int d) {
-  const int v = d > 256 * norm_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1;
+  const int v = d > 512 && d <= 768 ? 3 : (d > 256 * norm_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1);
   return team_shape(T, d, v, norm_warps(v));
 }
 TeamShape gated_shape(int64_t T, int d, int gate) {
-  return d <= 256 * gated_warps(gate) ? team_shape(T, d, 1, gated_warps(gate)) : team_shape(T, d, 2, kWideWarps);
+  // (Not with shared gates, whose runs end more often on more teams: 32749 x 640
+  // took 80 us by single warps, 77 by three.)
+  const int v = d > 512 && d <= 704 && gate != kSharedGate ? 3 : (d > 256 * gated_warps(gate, 1) ? 2 : 1);
+  return team_shape(T, d, v, gated_warps(gate, v));
 }
 TeamShape shape_of(const ResidualBwdArgs& a) {
   return a.f ? gated_shape(a.T, a.d, gate_kind(a.T, a.gate_rows, a.gate != nullptr)) : norm_shape(a.T, a.d);
@@ -83,16 +89,6 @@ __device__ __forceinline__ V8 flush_gate(const ResidualBwdArgs& a, const Team& m
   return post;
 }
 
-// A thread's part of a sum over tokens, for its team.
-template <int VPT>
-__device__ __forceinline__ void park(float* buf, const Team& m, int d, const V8 (&t)[VPT], float scale) {
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int k = (v * m.warps * 32 + m.tid) * 8;
-    if (k < d) st8(buf + m.team * d + k, mul8(t[v], scale));
-  }
-}
-
 // The CTA's partial rows, its teams added in order: sums [3][gridDim.x][d]
 // (dgamma_post, dgamma_pre, the one gate row of all tokens). The rings are
 // free: every copy has landed and been read.
@@ -100,15 +96,20 @@ template <int VPT>
 __device__ __forceinline__ void write_sums(const ResidualBwdArgs& a, const Team& m, const TeamGeom& g, float* buf,
                                            float* sums, bool with_post, bool with_gate, const V8 (&post)[VPT],
                                            const V8 (&pre)[VPT], const V8 (&gate)[VPT]) {
+  const bool direct = g.teams == 1 && (reinterpret_cast<uintptr_t>(sums) & 15) == 0;
   for (int which = 0; which < 3; ++which) {
     if (which == 0 ? !with_post : (which == 1 ? !(a.dn && a.dgpre) : !with_gate)) continue;
+    float* const part = sums + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.d;
+    if (!direct) __syncthreads();
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int k = (v * m.warps * 32 + m.tid) * 8;
+      if (k < a.d)
+        st8((direct ? part : buf + m.team * a.d) + k,
+            which == 0 ? mul8(post[v], a.scale) : (which == 1 ? pre[v] : gate[v]));
+    }
+    if (direct) continue;
     __syncthreads();
-    if (which == 0)
-      park(buf, m, a.d, post, a.scale);
-    else
-      park(buf, m, a.d, which == 1 ? pre : gate, 1.f);
-    __syncthreads();
-    float* part = sums + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.d;
     for (int k = threadIdx.x; k < a.d; k += blockDim.x) {
       float t = 0.f;
       for (int i = 0; i < g.teams; ++i) t += buf[i * a.d + k];
@@ -177,11 +178,11 @@ __global__ void __launch_bounds__(norm_warps(VPT) * 32, 1)
 
 // The gated backward. F: the type of f, dnormed and df; X: of x_out; G: of
 // dx_out and dx. GATE kNoGate also takes the one gate row of all tokens, which
-// rides on the gain. VPT: 8 features a thread, with the gains in registers, or
-// for the widest rows 16 (one team a CTA), with the gains in shared memory and
-// rings that may hold a single row.
+// rides on the gain. VPT: 8 or 24 features a thread, with the gains in registers,
+// or for the widest rows 16 (one team a CTA), with the gains in shared memory
+// and rings that may hold a single row.
 template <typename F, typename X, typename G, int GATE, int VPT>
-__global__ void __launch_bounds__((VPT == 1 ? gated_warps(GATE) : kWideWarps) * 32, 1)
+__global__ void __launch_bounds__(gated_warps(GATE, VPT) * 32, 1)
     residual_bwd_kernel(ResidualBwdArgs a, const __grid_constant__ TeamGeom g, float* sums, float* shared_part) {
   extern __shared__ __align__(128) unsigned char smem[];
   init_bars(g, smem);
@@ -195,22 +196,30 @@ __global__ void __launch_bounds__((VPT == 1 ? gated_warps(GATE) : kWideWarps) * 
   // scale * gamma_post, with a shared gate times its value too; gamma_pre; the
   // sums over the tokens of earlier runs. What is in shared memory is each
   // thread's own part.
-  V8 gain_reg = fill8(0.f), gpre_reg = fill8(0.f), slope;
+  constexpr bool kWide = VPT == 2;
+  V8 gain_reg[VPT], gpre_reg[VPT], slope;
   auto kept = [&](int which) { return reinterpret_cast<float*>(smem + g.gain) + which * d; };
-  auto earlier = [&]() { return VPT == 1 ? kept(0) + static_cast<int>(threadIdx.x) / (g.warps * 32) * d : kept(2); };
-  auto gain = [&](int k) { return VPT == 1 ? gain_reg : ld8(kept(0) + k); };
-  auto gpre = [&](int k) { return VPT == 1 ? gpre_reg : ld8(kept(1) + k); };
+  auto earlier = [&]() { return !kWide ? kept(0) + static_cast<int>(threadIdx.x) / (g.warps * 32) * d : kept(2); };
+  auto gain = [&](int v, int k) {
+    if constexpr (kWide) return ld8(kept(0) + k);
+    else return gain_reg[v];
+  };
+  auto gpre = [&](int v, int k) {
+    if constexpr (kWide) return ld8(kept(1) + k);
+    else return gpre_reg[v];
+  };
   auto set_gain = [&](int64_t group) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int k = k0 + v * step;
+      gain_reg[v] = fill8(0.f);
       if (k < d) {
         V8 c = scaled_gain(a, k);
         if (GATE != kTokenGate && a.gate) c = mul8(c, shared_act(a, group, k, slope));
-        if (VPT == 1)
-          gain_reg = c;
-        else
+        if (kWide)
           st8(kept(0) + k, c);
+        else
+          gain_reg[v] = c;
       }
     }
   };
@@ -221,13 +230,12 @@ __global__ void __launch_bounds__((VPT == 1 ? gated_warps(GATE) : kWideWarps) * 
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int k = k0 + v * step;
-    acc[v] = pre[v] = fill8(0.f);
+    acc[v] = pre[v] = gpre_reg[v] = fill8(0.f);
     if (k < d) {
-      const V8 c = a.dn ? ld8(a.gpre + k) : fill8(0.f);
-      if (VPT == 1)
-        gpre_reg = c;
-      else
-        st8(kept(1) + k, c);
+      if (kWide)
+        st8(kept(1) + k, a.dn ? ld8(a.gpre + k) : gpre_reg[v]);
+      else if (a.dn)
+        gpre_reg[v] = ld8(a.gpre + k);
       if (GATE == kSharedGate) st8(earlier() + k, acc[v]);
     }
   }
@@ -247,7 +255,7 @@ __global__ void __launch_bounds__((VPT == 1 ? gated_warps(GATE) : kWideWarps) * 
           if (a.dn) {
             const V8 x = ld8(reinterpret_cast<const X*>(st + g.x) + k);
             s[0] += dot8(x, x);
-            s[1] += dot8(mul8(gpre(k), ld8(reinterpret_cast<const F*>(st + g.dn) + k)), x);
+            s[1] += dot8(mul8(gpre(v, k), ld8(reinterpret_cast<const F*>(st + g.dn) + k)), x);
           }
           const V8 f = ld8(reinterpret_cast<const F*>(st + g.f) + k);
           s[2] += dot8(f, f);
@@ -285,27 +293,27 @@ __global__ void __launch_bounds__((VPT == 1 ? gated_warps(GATE) : kWideWarps) * 
             const V8 u = mul8(ld8(reinterpret_cast<const X*>(st + g.x) + k), rx);
             const V8 h = ld8(reinterpret_cast<const F*>(st + g.dn) + k);
             pre[v] = fma8(h, u, pre[v]);
-            D = fma8(fma8(u, -mx, mul8(gpre(k), h)), rx, D);
+            D = fma8(fma8(u, -mx, mul8(gpre(v, k), h)), rx, D);
           }
           if (a.dx) st8(static_cast<G*>(a.dx) + row + k, D);
           q[v] = mul8(ld8(reinterpret_cast<const F*>(st + g.f) + k), rf);
           if (GATE == kTokenGate) {
             V8 act = ld8(st + g.gate, k, a.g_bf16);
             activate8<true>(act, slope, a.sigmoid);
-            const V8 qD = mul8(q[v], D), c = gain(k);
+            const V8 qD = mul8(q[v], D), c = gain(v, k);
             acc[v] = fma8(act, qD, acc[v]);
             if (a.dgate) st8(a.dgate, row + k, a.g_bf16, mul8(slope, mul8(c, qD)));
             t[v] = mul8(mul8(c, act), D);
           } else {
             acc[v] = fma8(q[v], D, acc[v]);
-            t[v] = mul8(gain(k), D);
+            t[v] = mul8(gain(v, k), D);
           }
           s[3] += dot8(t[v], q[v]);
         }
       }
       if (++stage == m.nst) stage = 0, parity ^= 1u;
       if (r + 1 < m.rows) {
-        if (VPT > 1 && m.nst == 1) {  // a ring of one row: the next one comes when all are past this one
+        if (kWide && m.nst == 1) {  // a ring of one row: the next one comes when all are past this one
           team_sync(m);
           if (m.tid == 0) issue_row(m, g);
         }
@@ -317,7 +325,7 @@ __global__ void __launch_bounds__((VPT == 1 ? gated_warps(GATE) : kWideWarps) * 
         break;
       }
       // Every thread has what it needs of row r: its stage is free.
-      if ((VPT == 1 || m.nst > 1) && m.tid == 0 && m.issued < m.rows) issue_row(m, g);
+      if ((!kWide || m.nst > 1) && m.tid == 0 && m.issued < m.rows) issue_row(m, g);
       if (a.df)
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
@@ -361,12 +369,12 @@ bool geom_of(const ResidualBwdArgs& a, TeamGeom* g) {
   add_input(*g, a.dn, a.d * es, &g->dn);
   add_input(*g, a.gate && a.gate_rows == 1 ? a.gate : nullptr, a.d * (a.g_bf16 ? 2 : 4), &g->gate);
   const TeamShape s = shape_of(a);
-  // Past 8 features a thread the gated kernel's gains, and where runs of tokens
+  // With 16 features a thread the gated kernel's gains, and where runs of tokens
   // share gate rows the sums of earlier runs.
-  int gain_bytes = a.f && s.vectors > 1 ? 8 * a.d : 0;
+  int gain_bytes = a.f && s.vectors == 2 ? 8 * a.d : 0;
   if (a.f && gate_kind(a.T, a.gate_rows, a.gate != nullptr) == kSharedGate) gain_bytes += 4 * s.teams * a.d;
   // The teams' sums go through the rings' space: 4 bytes a feature and team.
-  return finish_geom(*g, s, gain_bytes, a.f && s.vectors > 1 ? 1 : 2, a.f ? kGatedRing : kNormRing) && g->nst * g->stage_bytes >= 4 * a.d;
+  return finish_geom(*g, s, gain_bytes, a.f && s.vectors == 2 ? 1 : 2, a.f ? kGatedRing : kNormRing) && g->nst * g->stage_bytes >= 4 * a.d;
 }
 
 struct Plan {
@@ -380,9 +388,12 @@ struct Plan {
 
 template <typename F, typename X, typename G, int GATE>
 cudaError_t launch_gate(const ResidualBwdArgs& a, const Plan& p) {
-  if (shape_of(a).vectors > 1)
-    return launch_teams(residual_bwd_kernel<F, X, G, GATE, 2>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
-  return launch_teams(residual_bwd_kernel<F, X, G, GATE, 1>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  const int v = shape_of(a).vectors;
+  if (v == 1) return launch_teams(residual_bwd_kernel<F, X, G, GATE, 1>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  if (v == 2) return launch_teams(residual_bwd_kernel<F, X, G, GATE, 2>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  if constexpr (GATE != kSharedGate)
+    return launch_teams(residual_bwd_kernel<F, X, G, GATE, 3>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  return cudaErrorInvalidValue;
 }
 template <typename F, typename X, typename G>
 cudaError_t launch_typed(const ResidualBwdArgs& a, const Plan& p) {
@@ -391,8 +402,10 @@ cudaError_t launch_typed(const ResidualBwdArgs& a, const Plan& p) {
 }
 template <typename F, typename G>
 cudaError_t launch_norm(const ResidualBwdArgs& a, const Plan& p) {
-  if (norm_shape(a.T, a.d).vectors > 1) return launch_teams(rmsnorm_bwd_kernel<F, G, 2>, p.g, p.ctas, p.s, a, p.g, p.sums);
-  return launch_teams(rmsnorm_bwd_kernel<F, G, 1>, p.g, p.ctas, p.s, a, p.g, p.sums);
+  const int v = norm_shape(a.T, a.d).vectors;
+  if (v == 1) return launch_teams(rmsnorm_bwd_kernel<F, G, 1>, p.g, p.ctas, p.s, a, p.g, p.sums);
+  if (v == 2) return launch_teams(rmsnorm_bwd_kernel<F, G, 2>, p.g, p.ctas, p.s, a, p.g, p.sums);
+  return launch_teams(rmsnorm_bwd_kernel<F, G, 3>, p.g, p.ctas, p.s, a, p.g, p.sums);
 }
 
 }  // namespace

@@ -14,10 +14,10 @@ namespace {
 
 __device__ unsigned int g_timeout = 0;
 
-// 28 warps of 72 registers, or 16 of 128 for 16 features a thread: with 32 of 64
-// and 20 of 96 the spills cost more than the warps brought (131072 x 2048 in 364
-// us against 319).
-constexpr int max_warps(int vectors) { return vectors == 1 ? 28 : 16; }
+// 28 warps of 72 registers, 16 of 128 for 16 features a thread, 12 of 168 for
+// 24: with 32 of 64 and 20 of 96 the spills cost more than the warps brought
+// (131072 x 2048 in 364 us against 319).
+constexpr int max_warps(int vectors) { return vectors == 1 ? 28 : vectors == 2 ? 16 : 12; }
 // Rows in flight per SM: with all of the 227 KB the reads crowd out the writes
 // (65536 x 1024 with an fp32 stream at 84 % of the copy bandwidth, with this 97).
 constexpr int kRingBytes = 146 * 1024;
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(max_warps(VPT) * 32, 1)
     residual_fast_kernel(ResidualArgs a, const __grid_constant__ TeamGeom g) {
   extern __shared__ __align__(128) unsigned char smem[];
   init_bars(g, smem);
-  Team m = make_team<VPT == 2 && GATE != kSharedGate>(g, a.T, smem);
+  Team m = make_team<VPT >= 2 && GATE != kSharedGate>(g, a.T, smem);
   pdl_trigger();
   pdl_wait();
   fill_ring(m, g);
@@ -131,8 +131,11 @@ __global__ void __launch_bounds__(max_warps(VPT) * 32, 1)
   }
 }
 
+// Rows that three warps of 8 features a thread would leave partly idle go to one
+// warp with 24: no barrier, and no lanes without work (104857 x 640 bf16 at 92 %
+// of the copy bandwidth, with three warps 74; at d = 768 three were better).
 TeamShape shape_of(int64_t T, int d) {
-  const int v = d > 256 * max_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1;
+  const int v = d > 512 && d <= 704 ? 3 : (d > 256 * max_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1);
   return team_shape(T, d, v, max_warps(v));
 }
 
@@ -153,6 +156,12 @@ cudaError_t launch_typed(const ResidualArgs& a, const TeamGeom& g, int64_t ctas,
   return launch_teams(residual_fast_kernel<F, X, kSharedGate, VPT>, g, ctas, s, a, g);
 }
 
+template <int VPT>
+cudaError_t launch_vectors(const ResidualArgs& a, const TeamGeom& g, int64_t ctas, cudaStream_t s) {
+  if (!a.f_bf16) return launch_typed<float, float, VPT>(a, g, ctas, s);
+  return a.x_bf16 ? launch_typed<bf16, bf16, VPT>(a, g, ctas, s) : launch_typed<bf16, float, VPT>(a, g, ctas, s);
+}
+
 }  // namespace
 
 bool residual_fast_ok(const ResidualArgs& a) {
@@ -166,12 +175,8 @@ cudaError_t launch_residual_fast(const ResidualArgs& a, cudaStream_t s) {
   if (!geom_of(a, &g)) return cudaErrorInvalidValue;
   const TeamShape t = shape_of(a.T, a.d);
   const int64_t ctas = team_ctas(a.T, t, cta_cap());
-  if (t.vectors == 1) {
-    if (!a.f_bf16) return launch_typed<float, float, 1>(a, g, ctas, s);
-    return a.x_bf16 ? launch_typed<bf16, bf16, 1>(a, g, ctas, s) : launch_typed<bf16, float, 1>(a, g, ctas, s);
-  }
-  if (!a.f_bf16) return launch_typed<float, float, 2>(a, g, ctas, s);
-  return a.x_bf16 ? launch_typed<bf16, bf16, 2>(a, g, ctas, s) : launch_typed<bf16, float, 2>(a, g, ctas, s);
+  return t.vectors == 1 ? launch_vectors<1>(a, g, ctas, s)
+                        : (t.vectors == 2 ? launch_vectors<2>(a, g, ctas, s) : launch_vectors<3>(a, g, ctas, s));
 }
 
 cudaError_t take_timeout_residual_fwd(unsigned int* flag) {

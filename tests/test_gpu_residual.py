@@ -139,7 +139,7 @@ def test_scales(T, d, gate_rows, scale):
 # Rows on both sides of where the kernels change: teams of one warp and several, 8 and 16 features a thread, the last
 # widths of each, and fp32 rows that leave room for one row or none in shared memory.
 @pytest.mark.parametrize("types", [("bf16", "bf16", "bf16"), ("f32", "f32", "f32")])
-@pytest.mark.parametrize("d", [248, 264, 504, 512, 520, 768, 776, 4096, 4104, 5120, 5128, 7168, 7176, 8184])
+@pytest.mark.parametrize("d", [248, 264, 504, 512, 520, 704, 712, 768, 776, 4096, 4104, 5120, 5128, 7168, 7176, 8184])
 def test_widths(d, types):
     for gate, rows in (("none", 1), ("sigmoid", 1), ("sigmoid", 9)):
         c = Case(23, d, types, gate=gate, gate_rows=rows, gate_type="f32", seed=d)
