@@ -204,7 +204,9 @@ bool any_overlap(const Range (&out)[NO], const Range (&in)[NI]) {
 }
 
 // Whether a pointer is off the boundary of its elements.
-bool off_element(const void* p, int64_t es) { return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(es - 1)) != 0; }
+bool off_element(const void* p, int64_t es) {
+  return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(es - 1)) != 0;
+}
 
 // Elements of one tensor beyond which byte offsets would not fit (none is that large).
 constexpr int64_t kMaxElements = int64_t{1} << 56;

@@ -35,6 +35,7 @@ __device__ __forceinline__ void st(void* p, int64_t i, int is_bf16, float v) {
   else
     static_cast<float*>(p)[i] = v;
 }
+
 // Sums of a CTA of kThreads threads; every thread gets them.
 template <int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* red) {

@@ -1,4 +1,4 @@
-// What the two files of the gated residual share.
+// What the files of the gated residual share.
 #pragma once
 
 #include "common.cuh"
@@ -8,9 +8,11 @@ namespace attnres {
 
 // sigmoid(g) and its slope from e = exp(-|g|), which neither overflows nor
 // loses the small factor of the slope e / (1 + e)^2 to cancellation. e is the
-// square of 2^(t/2), t = -|g| log2(e) in two parts (the second one's power to
-// first order), so that the result may be subnormal where 2^(t/2) is not;
-// e^-110 is 0 in fp32. Within 10 x 2^-24 of the exact value, relative.
+// square of 2^(t/2), so that it may be subnormal where 2^(t/2) is not; t =
+// -|g| log2(e) is taken in two parts, as Cody and Waite reduce arguments, and
+// the power of the second one to first order. e^-110 is 0 in fp32. With 2^t and
+// the reciprocal within 3 and 2 x 2^-24 both results are within 20 x 2^-24,
+// relative (e: 2 x (3 + 2) and its product; the rest: two roundings each).
 __device__ __forceinline__ float sigmoid(float g, float* slope) {
   float m = fabsf(g);
   m = m > 110.f ? 110.f : m;  // a NaN stays

@@ -5,9 +5,9 @@ evaluation may be off, before the result's own rounding: with u = 2^-24, a sum
 of n terms in any tree of depth L is within L u of the sum of the terms'
 magnitudes, and a product of k rounded factors within k u. `MEAN` bounds what a
 row mean and everything built on it carries: depth at most d/256 + 32 (a thread
-adds at most max(16, d/256) terms of its own, then 5 levels of a warp and at most
-16 warps), rsqrtf within 2 ulp (4 u, its argument's error counts half), and at
-most 16 further factors, expf (2 ulp) and division among them. Bounds are
+adds at most max(24, d/256) terms of its own, then 5 levels of a warp and its
+warps' sums), which counts half in r, rsqrtf within 2 ulp (4 u), a sigmoid (20 u,
+beside an r of half the depth), and at most 16 further factors. Bounds are
 therefore MEAN times the sum of the magnitudes that enter; a difference such as
 h - u <h u> is bounded through |h| + |u| <|h u|>.
 """

@@ -1,4 +1,4 @@
-"""Gated residual, its backward and the RMSNorm backward on the GPU against fp64, with the bounds of tests/_residual.py."""
+"""Gated residual, its backward and the RMSNorm backward on the GPU against fp64, within the bounds of tests/_residual.py."""
 import pytest
 import torch
 
@@ -412,3 +412,17 @@ def test_withheld_row_times_out_and_recovers():
     c.forward()
     c.backward(again)
     assert torch.equal(c.xo, want) and all(torch.equal(again[k], good[k]) for k in good)
+
+
+@pytest.mark.parametrize("d", [512, 100])
+def test_sigmoid_alone(d):
+    # f = 1, x = 0, no norms, scale 1: x_out is the sigmoid itself and with dx_out = 1 dgate is its slope; over the
+    # whole range of fp32's results, subnormal ones too (half a step of 2^-149 more).
+    g = torch.cat([torch.linspace(-106, 106, 400 * d - 4 * d, device=dev()),
+                   torch.logspace(-30, 2, 2 * d, device=dev()), -torch.logspace(-30, 2, 2 * d, device=dev())]).view(400, d)
+    f, out, dgate = torch.ones(400, d, device=dev()), torch.empty(400, d, device=dev()), torch.empty(400, d, device=dev())
+    ar.attnres_gated_residual(f, None, None, 0.0, g, 1, ar.GATE_SIGMOID, 1.0, out)
+    ar.attnres_gated_residual_bwd(f, None, 0.0, g, 1, ar.GATE_SIGMOID, 1.0, None, None, 0.0, f, None, None, None, dgate)
+    want, slope = ref.act(g.double(), True)
+    for got, value in ((out, want), (dgate, slope)):
+        assert ((got.double() - value).abs() <= 20 * ref.U * value + 2.0 ** -149).all()
