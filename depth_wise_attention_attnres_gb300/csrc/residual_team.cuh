@@ -215,13 +215,15 @@ __device__ __forceinline__ Team make_team(const TeamGeom& g, int64_t T, unsigned
   m.red = reinterpret_cast<float*>(smem + kRedOff) + m.team * kRedFloats * ((g.warps + 3) / 4);
   m.bars = smem_u32(smem) + m.team * g.nst * 8;
   m.ring = smem + g.stages + static_cast<size_t>(m.team) * g.nst * g.stage_bytes;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * g.teams + m.team;
   const int64_t all = static_cast<int64_t>(gridDim.x) * g.teams;
   if (INTERLEAVED) {
+    // By turns over the CTAs first: the last rows then spread over all SMs.
+    const int64_t id = static_cast<int64_t>(m.team) * gridDim.x + blockIdx.x;
     m.r0 = id;
     m.rows = T > id ? static_cast<int>((T - id - 1) / all + 1) : 0;
     m.stride = static_cast<int>(all);
   } else {
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * g.teams + m.team;
     m.r0 = T * id / all;
     m.rows = static_cast<int>(T * (id + 1) / all - m.r0);
     m.stride = 1;
