@@ -334,8 +334,13 @@ __global__ void __launch_bounds__(1024)
   const int64_t end = a.gate_rows < T - start ? start + a.gate_rows : T;
   const int64_t last = (end * n - 1) / T;
   float s = j.part[(first * 2 + 1) * a.d + k];
-  for (int64_t u = t; u <= last; ++u)
-    if (T >= n || T * u / n < T * (u + 1) / n) s += j.part[u * 2 * a.d + k];
+  if (T >= n) {
+#pragma unroll 4
+    for (int64_t u = t; u <= last; ++u) s += j.part[u * 2 * a.d + k];
+  } else {  // a team without rows has written nothing
+    for (int64_t u = t; u <= last; ++u)
+      if (T * u / n < T * (u + 1) / n) s += j.part[u * 2 * a.d + k];
+  }
   st(a.dgate, group * a.d + k, a.g_bf16, s);
 }
 

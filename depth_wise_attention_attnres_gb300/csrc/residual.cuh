@@ -39,8 +39,8 @@ inline bool residual_bwd_sums_gate(const ResidualBwdArgs& a) {
 
 // How the gate rows whose tokens several teams had are summed from the teams'
 // parts ([teams][2][d]: of a row that began before the team's tokens, and of one
-// that goes on after them): a block for each gate row and 32 features, or where
-// there are more rows than teams for each team's first row and 1024 features.
+// that goes on after them): a block for each gate row and 32 features, or a
+// block for each team's first row and 1024 features.
 struct ResidualJoin {
   const float* part = nullptr;
   int64_t teams = 0, blocks = 0;

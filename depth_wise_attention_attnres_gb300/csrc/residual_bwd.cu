@@ -28,7 +28,7 @@ constexpr int gated_warps(int gate, int vectors) {
 // Rows in flight per SM (as the forward's: the rings of the RMSNorm backward
 // are held to what left the writes room; the gated one, with more arithmetic to
 // cover, lost by it).
-constexpr int kNormRing = 146 * 1024, kGatedRing = kTeamSmem;
+constexpr int kNormRing = 120 * 1024, kGatedRing = kTeamSmem;
 
 // The gate of a call: none or one row for all tokens, one per token, or rows
 // that runs of tokens share.
@@ -454,7 +454,10 @@ ResidualJoin residual_bwd_join(const ResidualBwdArgs& a) {
   const int64_t ctas = residual_bwd_parts(a), groups = (a.T - 1) / a.gate_rows + 1;
   j.part = a.scratch + 3 * ctas * a.d;
   j.teams = ctas * shape_of(a).teams;
-  j.by_group = groups < j.teams;
+  // Rows that many teams had tokens of take many lanes to a sum; where they are
+  // many themselves, that is more blocks than it gains (32768 x 896 with rows of 256
+  // tokens: 133 us by rows, 100 by teams).
+  j.by_group = groups <= j.teams / 16;
   j.blocks = j.by_group ? groups * ((a.d - 1) / 32 + 1) : (j.teams - 1) * ((a.d - 1) / 1024 + 1);
   return j;
 }

@@ -18,9 +18,11 @@ __device__ unsigned int g_timeout = 0;
 // 24: with 32 of 64 and 20 of 96 the spills cost more than the warps brought
 // (131072 x 2048 in 364 us against 319).
 constexpr int max_warps(int vectors) { return vectors == 1 ? 28 : vectors == 2 ? 16 : 12; }
-// Rows in flight per SM: with all of the 227 KB the reads crowd out the writes
-// (65536 x 1024 with an fp32 stream at 84 % of the copy bandwidth, with this 97).
-constexpr int kRingBytes = 146 * 1024;
+// Rows in flight per SM: with all of the 227 KB the reads crowd out the writes,
+// the wider ones of an fp32 stream sooner (65536 x 1024 with a gate at 84 % of the
+// copy bandwidth, with 146 and 120 KB at 94; without one at 79 with 146, at 90 with
+// 120). bf16 rows gain by the deeper ring (32768 x 1024 with a gate 86 against 82).
+constexpr int kRingF32 = 120 * 1024, kRingBf16 = 146 * 1024;
 
 // F: the type of f and normed; X: of x and x_out. GATE kNoGate also takes the
 // one gate row of all tokens, which then rides on the gain.
@@ -145,7 +147,7 @@ bool geom_of(const ResidualArgs& a, TeamGeom* g) {
   add_input(*g, a.f, a.d * es, &g->f);
   add_input(*g, a.x, a.d * xs, &g->x);
   add_input(*g, a.gate && a.gate_rows == 1 ? a.gate : nullptr, a.d * (a.g_bf16 ? 2 : 4), &g->gate);
-  return finish_geom(*g, shape_of(a.T, a.d), 0, 2, kRingBytes);
+  return finish_geom(*g, shape_of(a.T, a.d), 0, 2, a.x_bf16 ? kRingBf16 : kRingF32);
 }
 
 template <typename F, typename X, int VPT>

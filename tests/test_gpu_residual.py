@@ -107,10 +107,12 @@ def test_backward_shapes(T, d, types):
     check_backward(Case(T, d, types, seed=T + d))
 
 
-# One row for all tokens, more rows than tokens, runs that end inside a CTA's share, runs of 2, a short last run.
+# One row for all tokens, more rows than tokens, runs that end inside a CTA's share, runs of 2, a short last run, and
+# token counts that leave some team of the grid without a row (153, 305, 457).
 @pytest.mark.parametrize("gate,gate_type", [("sigmoid", "bf16"), ("identity", "f32"), ("identity", "bf16")])
 @pytest.mark.parametrize("T,d,gate_rows", [(50, 256, 50), (50, 256, 1000), (333, 640, 2), (1000, 320, 17), (700, 1024, 699),
-                                           (1, 512, 1), (2, 512, 1), (1700, 264, 800), (40, 100, 7), (90, 8192, 31)])
+                                           (1, 512, 1), (2, 512, 1), (1700, 264, 800), (40, 100, 7), (90, 8192, 31),
+                                           (153, 256, 4), (153, 256, 100), (305, 264, 7), (457, 512, 150), (3000, 136, 40)])
 def test_gate_rows(T, d, gate_rows, gate, gate_type):
     c = Case(T, d, gate=gate, gate_rows=gate_rows, gate_type=gate_type, seed=gate_rows)
     check_forward(c)
