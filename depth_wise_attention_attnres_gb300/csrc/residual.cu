@@ -289,8 +289,15 @@ __global__ void __launch_bounds__(1024)
     // Without the norm its gain has no part in anything.
     if (first + x < a.d && (which != 0 || a.gpost) && (which != 1 || a.dn)) {
       const float* p = part + static_cast<int64_t>(which) * parts * a.d + first + x;
-#pragma unroll 5
-      for (int i = y; i < parts; i += 32) s += p[static_cast<int64_t>(i) * a.d];
+      // Five loads at once, cut by predicates: a loop with a rest would run the
+      // rest's loads one after the other.
+      for (int i = y; i < parts; i += 160) {
+        float v[5];
+#pragma unroll
+        for (int u = 0; u < 5; ++u) v[u] = i + 32 * u < parts ? p[static_cast<int64_t>(i + 32 * u) * a.d] : 0.f;
+#pragma unroll
+        for (int u = 0; u < 5; ++u) s += v[u];
+      }
     }
     red[y][x] = s;
     __syncthreads();
@@ -313,9 +320,15 @@ __global__ void __launch_bounds__(1024)
     if (first == last) return;
     float s = 0.f;
     if (k < a.d)
-      for (int64_t u = first + y; u <= last; u += 32)
-        if (T >= n || T * u / n < T * (u + 1) / n)  // a team without rows has written nothing
-          s += j.part[(u * 2 + (u == first ? 1 : 0)) * a.d + k];
+      for (int64_t i = first + y; i <= last; i += 128) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t u = i + 32 * e;  // (a team without rows has written nothing)
+          v[e] = u <= last && (T >= n || T * u / n < T * (u + 1) / n) ? j.part[(u * 2 + (u == first ? 1 : 0)) * a.d + k] : 0.f;
+        }
+        s += (v[0] + v[1]) + (v[2] + v[3]);
+      }
     red[y][x] = s;
     __syncthreads();
     s = warp_sum(red[x][y]);

@@ -58,7 +58,10 @@ inline int64_t team_ctas(int64_t T, const TeamShape& s, int64_t cap) {
   const int64_t want = (T - 1) / s.teams + 1;
   return want < cap ? want : cap;
 }
-inline int64_t cta_cap() { return sm_count() < kMaxCtas ? sm_count() : kMaxCtas; }
+inline int64_t cta_cap() {
+  const int n = sm_count();
+  return n < kMaxCtas ? n : kMaxCtas;
+}
 
 inline void add_input(TeamGeom& g, const void* p, int bytes, int* at) {
   *at = g.stage_bytes;
