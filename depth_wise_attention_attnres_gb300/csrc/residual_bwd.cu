@@ -77,7 +77,7 @@ __device__ __forceinline__ V8 flush_gate(const ResidualBwdArgs& a, const Team& m
   const int64_t start = group * a.gate_rows;
   const int64_t end = a.gate_rows < a.T - start ? start + a.gate_rows : a.T;
   if (start >= m.r0 && end <= m.r0 + m.rows) {
-    st8(a.dgate, group * a.d + k, a.g_bf16, acc);
+    out8(a.dgate, group * a.d + k, a.g_bf16, acc);
     return post;
   }
   const int64_t id = static_cast<int64_t>(blockIdx.x) * teams + m.team;
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(norm_warps(VPT) * 32, 1)
       if (k < d) {
         const V8 u = mul8(x[v], rx);
         sum[v] = fma8(h[v], u, sum[v]);
-        st8(static_cast<G*>(a.dx) + (m.r0 + r) * d + k, fma8(fma8(u, -mx, mul8(gain[v], h[v])), rx, D[v]));
+        out8(static_cast<G*>(a.dx) + (m.r0 + r) * d + k, fma8(fma8(u, -mx, mul8(gain[v], h[v])), rx, D[v]));
       }
     }
   }
@@ -296,14 +296,14 @@ __global__ void __launch_bounds__(gated_warps(GATE, VPT) * 32, 1)
             pre[v] = fma8(h, u, pre[v]);
             D = fma8(fma8(u, -mx, mul8(gpre(v, k), h)), rx, D);
           }
-          if (a.dx) st8(static_cast<G*>(a.dx) + row + k, D);
+          if (a.dx) out8(static_cast<G*>(a.dx) + row + k, D);
           q[v] = mul8(ld8(reinterpret_cast<const F*>(st + g.f) + k), rf);
           if (GATE == kTokenGate) {
             V8 act = ld8(st + g.gate, k, a.g_bf16);
             activate8<true>(act, slope, a.sigmoid);
             const V8 qD = mul8(q[v], D), c = gain(v, k);
             acc[v] = fma8(act, qD, acc[v]);
-            if (a.dgate) st8(a.dgate, row + k, a.g_bf16, mul8(slope, mul8(c, qD)));
+            if (a.dgate) out8(a.dgate, row + k, a.g_bf16, mul8(slope, mul8(c, qD)));
             t[v] = mul8(mul8(c, act), D);
           } else {
             acc[v] = fma8(q[v], D, acc[v]);
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(gated_warps(GATE, VPT) * 32, 1)
         for (int v = 0; v < VPT; ++v) {
           const int k = k0 + v * step;
           if (k < d)
-            st8(static_cast<F*>(a.df) + row + k, post_norm ? mul8(fma8(q[v], -(s[3] * inv_d), t[v]), rf) : t[v]);
+            out8(static_cast<F*>(a.df) + row + k, post_norm ? mul8(fma8(q[v], -(s[3] * inv_d), t[v]), rf) : t[v]);
         }
     }
     if (GATE == kSharedGate) {

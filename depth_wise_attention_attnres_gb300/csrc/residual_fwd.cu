@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(max_warps(VPT) * 32, 1)
             w = mul8(w, gate);
           }
           x[v] = fma8(w, f[v], x[v]);
-          st8(static_cast<X*>(a.x_out) + row + k, x[v]);
+          out8(static_cast<X*>(a.x_out) + row + k, x[v]);
           s[0] += dot8(x[v], x[v]);
         }
       }
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(max_warps(VPT) * 32, 1)
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           const int k = k0 + v * step;
-          if (k < d) st8(static_cast<F*>(a.normed) + row + k, mul8(mul8(gpre[v], rx), x[v]));
+          if (k < d) out8(static_cast<F*>(a.normed) + row + k, mul8(mul8(gpre[v], rx), x[v]));
         }
       }
     }

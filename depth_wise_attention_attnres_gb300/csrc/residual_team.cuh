@@ -130,11 +130,23 @@ __device__ __forceinline__ void st8(float* p, const V8& x) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x.p[0].x, x.p[0].y, x.p[1].x, x.p[1].y);
   reinterpret_cast<float4*>(p)[1] = make_float4(x.p[2].x, x.p[2].y, x.p[3].x, x.p[3].y);
 }
-__device__ __forceinline__ void st8(void* p, int64_t i, int is_bf16, const V8& x) {
+// Results, in global memory: written once, so marked to leave the L2 first, as
+// the rows read are. Either mark alone did nothing; with both, 131072 x 2048
+// forward took 317 us instead of 342 (calls that the L2 holds keep their results
+// in it all the same).
+__device__ __forceinline__ void out8(bf16* p, const V8& x) {
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(x.p[0].x, x.p[0].y), pack_bf16x2(x.p[1].x, x.p[1].y),
+                                                 pack_bf16x2(x.p[2].x, x.p[2].y), pack_bf16x2(x.p[3].x, x.p[3].y)));
+}
+__device__ __forceinline__ void out8(float* p, const V8& x) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(x.p[0].x, x.p[0].y, x.p[1].x, x.p[1].y));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x.p[2].x, x.p[2].y, x.p[3].x, x.p[3].y));
+}
+__device__ __forceinline__ void out8(void* p, int64_t i, int is_bf16, const V8& x) {
   if (is_bf16)
-    st8(static_cast<bf16*>(p) + i, x);
+    out8(static_cast<bf16*>(p) + i, x);
   else
-    st8(static_cast<float*>(p) + i, x);
+    out8(static_cast<float*>(p) + i, x);
 }
 __device__ __forceinline__ V8 mul8(const V8& a, const V8& b) {
   V8 r;
@@ -245,6 +257,17 @@ __device__ __forceinline__ void init_bars(const TeamGeom& g, unsigned char* smem
   __syncthreads();
 }
 
+// A bulk copy of bytes that are read once: they leave the L2 first.
+__device__ __forceinline__ void bulk_g2s_once(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // Starts the copies of the next row of the team's run (its first thread only).
 __device__ __forceinline__ void issue_row(Team& m, const TeamGeom& g) {
   const int s = m.next;
@@ -253,7 +276,7 @@ __device__ __forceinline__ void issue_row(Team& m, const TeamGeom& g) {
     const uint32_t bar = m.bars + s * 8, dst = smem_u32(m.ring) + s * g.stage_bytes;
     mbar_arrive_expect_tx(bar, g.stage_bytes);
     const int64_t row = m.r0 + static_cast<int64_t>(m.issued) * m.stride;
-    for (int i = 0; i < g.n; ++i) bulk_g2s(dst + g.off[i], g.src[i] + row * g.bytes[i], g.bytes[i], bar);
+    for (int i = 0; i < g.n; ++i) bulk_g2s_once(dst + g.off[i], g.src[i] + row * g.bytes[i], g.bytes[i], bar);
   }
   ++m.issued;
 }
