@@ -25,10 +25,10 @@ constexpr int norm_warps(int vectors) { return vectors == 1 ? 28 : vectors == 2 
 constexpr int gated_warps(int gate, int vectors) {
   return vectors == 3 ? 8 : vectors == 2 || gate == kSharedGate ? 16 : 20;
 }
-// Rows in flight per SM (as the forward's: the rings of the RMSNorm backward
-// are held to what left the writes room; the gated one, with more arithmetic to
-// cover, lost by it).
-constexpr int kNormRing = 120 * 1024, kGatedRing = kTeamSmem;
+// Rows in flight per SM, held as the forward's to what leaves the writes room
+// (131072 x 256 with an fp32 stream, gated: 92 % of the copy bandwidth with 180 KB, 79
+// with all 227; with 146 the wide rows lost, 16384 x 2048 at 79 against 90).
+constexpr int kNormRing = 120 * 1024, kGatedRing = 180 * 1024;
 
 // The gate of a call: none or one row for all tokens, one per token, or rows
 // that runs of tokens share.
