@@ -26,9 +26,12 @@ constexpr int gated_warps(int gate, int vectors) {
   return vectors == 3 ? 8 : vectors == 2 || gate == kSharedGate ? 16 : 20;
 }
 // Rows in flight per SM, held as the forward's to what leaves the writes room
-// (131072 x 256 with an fp32 stream, gated: 92 % of the copy bandwidth with 180 KB, 79
+// (131072 x 256 with an fp32 stream, gated: 92 % of the copy bandwidth with 190 KB, 79
 // with all 227; with 146 the wide rows lost, 16384 x 2048 at 79 against 90).
-constexpr int kNormRing = 120 * 1024, kGatedRing = 180 * 1024;
+// The RMSNorm backward's single warps want a third row each where rows are long
+// enough that 120 KB hold only two (262144 x 256: 94 % with 180 KB, 75 with 120;
+// other widths lose 2 to 8 % by it).
+constexpr int kNormRing = 120 * 1024, kNarrowNormRing = 180 * 1024, kGatedRing = 190 * 1024;
 
 // The gate of a call: none or one row for all tokens, one per token, or rows
 // that runs of tokens share.
@@ -374,8 +377,9 @@ bool geom_of(const ResidualBwdArgs& a, TeamGeom* g) {
   // share gate rows the sums of earlier runs.
   int gain_bytes = a.f && s.vectors == 2 ? 8 * a.d : 0;
   if (a.f && gate_kind(a.T, a.gate_rows, a.gate != nullptr) == kSharedGate) gain_bytes += 4 * s.teams * a.d;
+  const int ring = a.f ? kGatedRing : (a.d > 200 && a.d <= 256 ? kNarrowNormRing : kNormRing);
   // The teams' sums go through the rings' space: 4 bytes a feature and team.
-  return finish_geom(*g, s, gain_bytes, a.f && s.vectors == 2 ? 1 : 2, a.f ? kGatedRing : kNormRing) &&
+  return finish_geom(*g, s, gain_bytes, a.f && s.vectors == 2 ? 1 : 2, ring) &&
          g->nst * g->stage_bytes >= 4 * a.d;
 }
 
