@@ -18,13 +18,11 @@ __device__ unsigned int g_timeout = 0;
 
 // Warps of a CTA. The backward of RMSNorm: 28 of 72 registers, 16 of 128 for
 // 16 features a thread, 12 of 168 for 24. The gated one: 20 of 96 (8192 x 896 in
-// 34.6 us, with 16 of 128 36.0), 16 of 128 where runs of tokens share gate rows,
-// 8 of 255 for 24 features a thread; past the width that 8 features cover its
-// threads take 16, and 128 registers.
+// 34.6 us, with 16 of 128 36.0; 32749 x 640 with shared gate rows 72, with 16 77), 8 of
+// 255 for 24 features a thread; past the width that 8 features cover its threads
+// take 16, and 128 registers.
 constexpr int norm_warps(int vectors) { return vectors == 1 ? 28 : vectors == 2 ? 16 : 12; }
-constexpr int gated_warps(int gate, int vectors) {
-  return vectors == 3 ? 8 : vectors == 2 || gate == kSharedGate ? 16 : 20;
-}
+constexpr int gated_warps(int vectors) { return vectors == 1 ? 20 : vectors == 2 ? 16 : 8; }
 // Rows in flight per SM, held as the forward's to what leaves the writes room
 // (131072 x 256 with an fp32 stream, gated: 92 % of the copy bandwidth with 190 KB, 79
 // with all 227; with 146 the wide rows lost, 16384 x 2048 at 79 against 90).
@@ -47,9 +45,9 @@ TeamShape norm_shape(int64_t T, int d) {
 }
 TeamShape gated_shape(int64_t T, int d, int gate) {
   // (Not with shared gates, whose runs end more often on more teams: 32749 x 640
-  // took 80 us by single warps, 77 by three.)
-  const int v = d > 512 && d <= 704 && gate != kSharedGate ? 3 : (d > 256 * gated_warps(gate, 1) ? 2 : 1);
-  return team_shape(T, d, v, gated_warps(gate, v));
+  // took 77 us by single warps, 72 by three.)
+  const int v = d > 512 && d <= 704 && gate != kSharedGate ? 3 : (d > 256 * gated_warps(1) ? 2 : 1);
+  return team_shape(T, d, v, gated_warps(v));
 }
 TeamShape shape_of(const ResidualBwdArgs& a) {
   return a.f ? gated_shape(a.T, a.d, gate_kind(a.T, a.gate_rows, a.gate != nullptr)) : norm_shape(a.T, a.d);
@@ -186,7 +184,7 @@ __global__ void __launch_bounds__(norm_warps(VPT) * 32, 1)
 // or for the widest rows 16 (one team a CTA), with the gains in shared memory
 // and rings that may hold a single row.
 template <typename F, typename X, typename G, int GATE, int VPT>
-__global__ void __launch_bounds__(gated_warps(GATE, VPT) * 32, 1)
+__global__ void __launch_bounds__(gated_warps(VPT) * 32, 1)
     residual_bwd_kernel(ResidualBwdArgs a, const __grid_constant__ TeamGeom g, float* sums, float* shared_part) {
   extern __shared__ __align__(128) unsigned char smem[];
   init_bars(g, smem);
@@ -201,7 +199,7 @@ __global__ void __launch_bounds__(gated_warps(GATE, VPT) * 32, 1)
   // sums over the tokens of earlier runs. What is in shared memory is each
   // thread's own part.
   constexpr bool kWide = VPT == 2;
-  V8 gain_reg[VPT], gpre_reg[VPT], slope;
+  V8 gain_reg[VPT] = {}, gpre_reg[VPT] = {}, slope;
   auto kept = [&](int which) { return reinterpret_cast<float*>(smem + g.gain) + which * d; };
   auto earlier = [&]() { return !kWide ? kept(0) + static_cast<int>(threadIdx.x) / (g.warps * 32) * d : kept(2); };
   auto gain = [&](int v, int k) {
