@@ -7,8 +7,8 @@
 // scaled tensors. Bound by memory: the norm reads every gradient once, the
 // scaling reads them again and writes them (a list larger than the L2 has to be
 // read twice: no scaling before the norm is known). Measured: 400M bf16 elements'
-// norm in 116 to 123 us (6.5 to 6.9 TB/s), 800M fp32 clipped to bf16 in 1.16 ms
-// (6.9 TB/s over both readings and the writing).
+// norm in 117 us (6.8 TB/s), 800M fp32 clipped to bf16 in 1.16 ms (6.9 TB/s over
+// both readings and the writing).
 //
 // Squares are summed in three scales at once, of g, g 2^80 and g 2^-80: fp32
 // holds g^2 only for 2^-63 < |g| < 2^63, and bf16 and fp32 gradients go far
@@ -95,7 +95,9 @@ __device__ __forceinline__ int64_t head_of(const T* p, int64_t n) {
 
 template <typename T>
 __device__ __forceinline__ void sum_segment(Total& total, const T* p, int64_t n) {
-  constexpr int kV = 16 / sizeof(T), kU = 8;
+  // Four loads in flight a thread on three CTAs an SM: with eight 400M bf16
+  // elements took 120 us (117), with two or four CTAs 123 and 146.
+  constexpr int kV = 16 / sizeof(T), kU = 4;
   const int64_t head = head_of(p, n);
   const uint4* v = reinterpret_cast<const uint4*>(p + head);
   const int64_t nv = (n - head) / kV;

@@ -1,7 +1,7 @@
 """The global gradient norm and clipping on the GPU against fp64.
 
-Tolerances: the norm's square is a sum of squares: batches of at most 64 (a chain of at most 32 packed additions
-and one more), their sum with its rounding carried (4), a warp's and a CTA's trees (10), the CTAs' (13), each
+Tolerances: the norm's square is a sum of squares: batches of at most 32 (a chain of at most 16 packed additions
+and one more; allowed for: 32), their sum with its rounding carried (4), a warp's and a CTA's trees (10), the CTAs' (13), each
 addition within 2^-24 of positive terms: 64 x 2^-24, half of which reaches the norm, with a square root and its
 own rounding 2 more. A clipped element is one product with max_norm / norm (the norm's error, a division and the
 product: 2 more roundings), then its own rounding.
