@@ -6,26 +6,36 @@
 
 namespace attnres {
 
-// sigmoid(g) and its slope from e = exp(-|g|), which neither overflows nor
-// loses the small factor of the slope e / (1 + e)^2 to cancellation. e is the
-// square of 2^(t/2), so that it may be subnormal where 2^(t/2) is not; t =
+// sigmoid(g) and its slope, of two values, from e = exp(-|g|), which neither
+// overflows nor loses the small factor of the slope e / (1 + e)^2 to cancellation.
+// e is the square of 2^(t/2), so that it may be subnormal where 2^(t/2) is not; t =
 // -|g| log2(e) is taken in two parts, as Cody and Waite reduce arguments, and
 // the power of the second one to first order. e^-110 is 0 in fp32. With 2^t and
 // the reciprocal within 3 and 2 x 2^-24 both results are within 20 x 2^-24,
 // relative (e: 2 x (3 + 2) and its product; the rest: two roundings each).
+__device__ __forceinline__ float2 sigmoid2(float2 g, float2* slope) {
+  float2 m, y, r;
+  asm("min.NaN.f32 %0, %1, 0f42DC0000;" : "=f"(m.x) : "f"(fabsf(g.x)));  // 110; a NaN stays
+  asm("min.NaN.f32 %0, %1, 0f42DC0000;" : "=f"(m.y) : "f"(fabsf(g.y)));
+  const float2 h = fmul2(m, make_float2(0.72134752f, 0.72134752f));  // log2(e) / 2
+  // What fp32 leaves of -m log2(e) / 2 when -h is taken.
+  float2 rest = ffma2(m, make_float2(-0.72134752f, -0.72134752f), h);
+  rest = ffma2(m, make_float2(-9.62981e-9f, -9.62981e-9f), rest);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(-h.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(-h.y));
+  y = ffma2(y, fmul2(rest, make_float2(0.69314718f, 0.69314718f)), y);
+  const float2 e = fmul2(y, y), d = ffma2(y, y, make_float2(1.f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  const float2 er = fmul2(e, r);
+  *slope = fmul2(er, r);
+  return make_float2(g.x < 0.f ? er.x : r.x, g.y < 0.f ? er.y : r.y);
+}
 __device__ __forceinline__ float sigmoid(float g, float* slope) {
-  float m = fabsf(g);
-  m = m > 110.f ? 110.f : m;  // a NaN stays
-  const float t = m * -0.72134752f;                      // -log2(e) / 2
-  const float rest = fmaf(m, -0.72134752f, -t) - m * 9.62981e-9f;  // and what fp32 leaves of it
-  float y, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
-  y = fmaf(y, rest * 0.69314718f, y);
-  const float e = y * y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  const float er = e * r;
-  *slope = er * r;
-  return g < 0.f ? er : r;
+  float2 s;
+  const float2 a = sigmoid2(make_float2(g, 0.f), &s);
+  *slope = s.x;
+  return a.x;
 }
 
 // Whether runs of tokens, but not all of them, share gate rows whose gradient

@@ -182,8 +182,7 @@ __device__ __forceinline__ void activate8(V8& g, V8& slope, int is_sigmoid) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 s;
-      g.p[i].x = sigmoid(g.p[i].x, &s.x);
-      g.p[i].y = sigmoid(g.p[i].y, &s.y);
+      g.p[i] = sigmoid2(g.p[i], &s);
       if (SLOPE) slope.p[i] = s;
     }
   } else if (SLOPE) {
