@@ -221,6 +221,20 @@ def test_list_kept_and_replayed_on_new_values():
     assert abs(float(norm2) - want) <= norm_bound() * want
 
 
+def test_another_stream_and_lists_made_for_the_call():
+    grads = make([300_000, 5, 4097], ["f32", "bf16"])
+    want = ref.norm_of(grads)
+    s, norm = torch.cuda.Stream(), torch.full((1,), -1.0, device=dev())
+    s.wait_stream(torch.cuda.current_stream())
+    ar.attnres_grad_norm(grads, norm, stream=s)
+    s.synchronize()
+    assert abs(float(norm) - want) <= norm_bound() * want
+    torch.cuda.synchronize()
+    ar.attnres_grad_clip(tuple(grads), want / 3, norm, stream=s.cuda_stream)
+    s.synchronize()
+    assert abs(ref.norm_of(grads) - want / 3) <= 2.0 ** -8 * want
+
+
 def test_refusals():
     norm = torch.empty(1, device=dev())
     g = torch.ones(10, 10, device=dev())

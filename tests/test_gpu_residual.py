@@ -303,6 +303,23 @@ def test_no_tokens(d):
     assert torch.equal(out["dgamma_post"], kept["dgamma_post"])
     c.backward(out)
     assert (out["dgamma_post"] == 0).all() and (out["dgamma_pre"] == 0).all()
+    c, dgamma = Case(0, d, ("bf16", "bf16", "bf16"), gate="none"), c.make((d,), "f32")
+    ar.attnres_rmsnorm_bwd(c.xo, c.gpre, EPS_PRE, c.dn, None, torch.empty_like(c.xo), dgamma, accumulate=False)
+    assert (dgamma == 0).all()
+
+
+@pytest.mark.parametrize("d", [256, 100, 8192])
+def test_one_gate_row_whatever_the_run(d):
+    # Any gate_rows from T on means the one row, up to the largest number the call takes.
+    want = None
+    for rows in (20, 21, 2**31, 2**62):
+        c = Case(20, d, gate_rows=rows, gate_type="f32", seed=7)
+        out = c.outputs()
+        c.forward()
+        c.backward(out)
+        got = [c.xo, c.normed] + [out[k] for k in sorted(out)]
+        assert want is None or all(torch.equal(a, b) for a, b in zip(want, got))
+        want = got
 
 
 @pytest.mark.parametrize("gate_rows", [1, 130, 400])
