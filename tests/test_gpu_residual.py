@@ -209,7 +209,10 @@ def test_in_place(T, d):
     assert all(torch.equal(out[k], again[k]) for k in out)
 
 
-@pytest.mark.parametrize("T,d,gate_rows", [(700, 896, 1), (700, 896, 700), (500, 640, 37), (60, 100, 60), (30, 8192, 30)])
+# (The last ones: a few rows, with a gate row for each, for runs of them, and for all.)
+@pytest.mark.parametrize("T,d,gate_rows", [(700, 896, 1), (700, 896, 700), (500, 640, 37), (60, 100, 60), (30, 8192, 30),
+                                           (3, 896, 1), (10, 896, 10), (11, 896, 11), (40, 256, 3), (41, 256, 3),
+                                           (40, 256, 40), (2, 8192, 2), (2, 8192, 1), (16, 640, 1), (9, 896, 4)])
 def test_same_bits_and_accumulate(T, d, gate_rows):
     c = Case(T, d, gate_rows=gate_rows, gate_type="f32")
     a, b = c.outputs(), c.outputs()
