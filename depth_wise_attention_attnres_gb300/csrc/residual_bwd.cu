@@ -24,12 +24,16 @@ __device__ unsigned int g_timeout = 0;
 constexpr int norm_warps(int vectors) { return vectors == 1 ? 28 : vectors == 2 ? 16 : 12; }
 constexpr int gated_warps(int vectors) { return vectors == 1 ? 20 : vectors == 2 ? 16 : 8; }
 // Rows in flight per SM, held as the forward's to what leaves the writes room
-// (131072 x 256 with an fp32 stream, gated: 92 % of the copy bandwidth with 190 KB, 79
-// with all 227; with 146 the wide rows lost, 16384 x 2048 at 79 against 90).
+// (ungated, an fp32 stream: 131072 x 256 at 91 % of the copy bandwidth with 146 KB,
+// 80 with 190). Fewer than 10 teams want a third row, of up to 196 KB (16384 x 2048
+// fp32: 90 % against 82; with 215 KB 1024 and 1536 lose 4 to 5), a team alone
+// wherever it fits (8192 x 4096 fp32 with gates: 89 % with 221 KB, 75 with two rows).
 // The RMSNorm backward's single warps want a third row each where rows are long
 // enough that 120 KB hold only two (262144 x 256: 94 % with 180 KB, 75 with 120;
-// other widths lose 2 to 8 % by it).
-constexpr int kNormRing = 120 * 1024, kNarrowNormRing = 180 * 1024, kGatedRing = 190 * 1024;
+// other widths lose 2 to 8 % by it), and past 512 features all-bf16 rows gain up to
+// 2.7 % by 146 KB (9362 x 3584: 83 % against 81).
+constexpr int kNormRing = 120 * 1024, kNarrowNormRing = 180 * 1024, kBf16NormRing = 146 * 1024;
+constexpr int kGatedRing = 146 * 1024, kGatedThird = 196 * 1024;
 
 // The gate of a call: none or one row for all tokens, one per token, or rows
 // that runs of tokens share.
@@ -37,10 +41,11 @@ int gate_kind(int64_t T, int64_t gate_rows, bool gate) {
   if (!gate || (gate_rows > 1 && gate_rows >= T)) return kNoGate;
   return gate_rows == 1 ? kTokenGate : kSharedGate;
 }
-// Where three warps of 8 features a thread would idle, one warp takes the row
-// with 24 (104857 x 640 bf16 at 77 % of the copy bandwidth, with three 51).
-TeamShape norm_shape(int64_t T, int d) {
-  const int v = d > 512 && d <= 768 ? 3 : (d > 256 * norm_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1);
+// Where three warps of 8 features a thread would be short of instructions, one
+// warp takes the row with 24 (104857 x 640, all bf16, at 91 % of the copy bandwidth,
+// with three 71; with fp32 gradients, which give them more time, 86 against 94).
+TeamShape norm_shape(int64_t T, int d, bool all_bf16) {
+  const int v = d > 512 && d <= 768 && all_bf16 ? 3 : (d > 256 * norm_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1);
   return team_shape(T, d, v, norm_warps(v));
 }
 TeamShape gated_shape(int64_t T, int d, int gate) {
@@ -50,7 +55,7 @@ TeamShape gated_shape(int64_t T, int d, int gate) {
   return team_shape(T, d, v, gated_warps(v));
 }
 TeamShape shape_of(const ResidualBwdArgs& a) {
-  return a.f ? gated_shape(a.T, a.d, gate_kind(a.T, a.gate_rows, a.gate != nullptr)) : norm_shape(a.T, a.d);
+  return a.f ? gated_shape(a.T, a.d, gate_kind(a.T, a.gate_rows, a.gate != nullptr)) : norm_shape(a.T, a.d, a.f_bf16 && a.dx_bf16);
 }
 
 // 8 features of a gate row that tokens share: act(gate), and its slope.
@@ -375,9 +380,14 @@ bool geom_of(const ResidualBwdArgs& a, TeamGeom* g) {
   // share gate rows the sums of earlier runs.
   int gain_bytes = a.f && s.vectors == 2 ? 8 * a.d : 0;
   if (a.f && gate_kind(a.T, a.gate_rows, a.gate != nullptr) == kSharedGate) gain_bytes += 4 * s.teams * a.d;
-  const int ring = a.f ? kGatedRing : (a.d > 200 && a.d <= 256 ? kNarrowNormRing : kNormRing);
+  const bool all_bf16 = a.f_bf16 && a.dx_bf16;
+  const int ring = a.f                            ? kGatedRing
+                   : a.d > 200 && a.d <= 256      ? kNarrowNormRing
+                   : all_bf16 && a.d > 512        ? kBf16NormRing
+                                                  : kNormRing;
+  const int third = !a.f ? 0 : s.teams == 1 ? kTeamSmem : s.teams < 10 ? kGatedThird : 0;
   // The teams' sums go through the rings' space: 4 bytes a feature and team.
-  return finish_geom(*g, s, gain_bytes, a.f && s.vectors == 2 ? 1 : 2, ring) &&
+  return finish_geom(*g, s, gain_bytes, a.f && s.vectors == 2 ? 1 : 2, ring, third) &&
          g->nst * g->stage_bytes >= 4 * a.d;
 }
 
@@ -406,10 +416,12 @@ cudaError_t launch_typed(const ResidualBwdArgs& a, const Plan& p) {
 }
 template <typename F, typename G>
 cudaError_t launch_norm(const ResidualBwdArgs& a, const Plan& p) {
-  const int v = norm_shape(a.T, a.d).vectors;
+  const int v = shape_of(a).vectors;
   if (v == 1) return launch_teams(rmsnorm_bwd_kernel<F, G, 1>, p.g, p.ctas, p.s, a, p.g, p.sums);
   if (v == 2) return launch_teams(rmsnorm_bwd_kernel<F, G, 2>, p.g, p.ctas, p.s, a, p.g, p.sums);
-  return launch_teams(rmsnorm_bwd_kernel<F, G, 3>, p.g, p.ctas, p.s, a, p.g, p.sums);
+  if constexpr (sizeof(F) == 2 && sizeof(G) == 2)
+    return launch_teams(rmsnorm_bwd_kernel<F, G, 3>, p.g, p.ctas, p.s, a, p.g, p.sums);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -427,8 +439,10 @@ int64_t residual_bwd_fast_scratch(int64_t T, int d, int64_t gate_rows) {
   if (T == 0 || d % 8 != 0 || d > kMaxTeamD) return 0;
   const int gate = gate_kind(T, gate_rows, true);
   TeamShape s = gated_shape(T, d, gate);
-  const TeamShape n = norm_shape(T, d);
-  if (gate == kTokenGate && n.teams < s.teams) s = n;
+  for (const bool all_bf16 : {false, true}) {
+    const TeamShape n = norm_shape(T, d, all_bf16);
+    if (gate == kTokenGate && n.teams < s.teams) s = n;
+  }
   const int64_t ctas = team_ctas(T, s, kMaxCtas);
   return 3 * ctas * d + (gate == kSharedGate ? ctas * s.teams * 2 * d : 0);
 }
@@ -458,7 +472,7 @@ ResidualJoin residual_bwd_join(const ResidualBwdArgs& a) {
   j.teams = ctas * shape_of(a).teams;
   // Rows that many teams had tokens of take many lanes to a sum; where they are
   // many themselves, that is more blocks than it gains (32768 x 896 with rows of 256
-  // tokens: 133 us by rows, 100 by teams).
+  // tokens: 126 us by rows, 96 by teams).
   j.by_group = groups <= j.teams / 16;
   j.blocks = j.by_group ? groups * ((a.d - 1) / 32 + 1) : (j.teams - 1) * ((a.d - 1) / 1024 + 1);
   return j;

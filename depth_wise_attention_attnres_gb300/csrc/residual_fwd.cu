@@ -20,9 +20,13 @@ __device__ unsigned int g_timeout = 0;
 constexpr int max_warps(int vectors) { return vectors == 1 ? 28 : vectors == 2 ? 16 : 12; }
 // Rows in flight per SM: with all of the 227 KB the reads crowd out the writes,
 // the wider ones of an fp32 stream sooner (65536 x 1024 with a gate at 84 % of the
-// copy bandwidth, with 146 and 120 KB at 94; without one at 79 with 146, at 90 with
-// 120). bf16 rows gain by the deeper ring (32768 x 1024 with a gate 86 against 82).
-constexpr int kRingF32 = 120 * 1024, kRingBf16 = 146 * 1024;
+// copy bandwidth, with 146 and 120 KB at 98; without one at 86 with 146, at 96 with
+// 120). bf16 rows gain by the deeper ring (32768 x 1024 with a gate 86 against 83).
+// A team alone wants a third row (6553 x 5120 fp32 with bf16 gates at 92 % of the copy
+// bandwidth, with two 67; only 4096 x 8192 with an fp32 stream and bf16 gates lost by
+// it, 83 against 87), and so do single warps of fp32 (131072 x 256: 87 % with
+// 168 KB, 77 with 120).
+constexpr int kRingF32 = 120 * 1024, kRingBf16 = 146 * 1024, kWarpF32Third = 168 * 1024;
 
 // F: the type of f and normed; X: of x and x_out. GATE kNoGate also takes the
 // one gate row of all tokens, which then rides on the gain.
@@ -134,8 +138,8 @@ __global__ void __launch_bounds__(max_warps(VPT) * 32, 1)
 }
 
 // Rows that three warps of 8 features a thread would leave partly idle go to one
-// warp with 24: no barrier, and no lanes without work (104857 x 640 bf16 at 92 %
-// of the copy bandwidth, with three warps 74; at d = 768 three were better).
+// warp with 24: no barrier, and no lanes without work (104857 x 640 bf16 at 94 %
+// of the copy bandwidth, with three warps 71; at d = 768 three were better).
 TeamShape shape_of(int64_t T, int d) {
   const int v = d > 512 && d <= 704 ? 3 : (d > 256 * max_warps(1) || (d > 512 && sixteen_pay(d)) ? 2 : 1);
   return team_shape(T, d, v, max_warps(v));
@@ -147,7 +151,9 @@ bool geom_of(const ResidualArgs& a, TeamGeom* g) {
   add_input(*g, a.f, a.d * es, &g->f);
   add_input(*g, a.x, a.d * xs, &g->x);
   add_input(*g, a.gate && a.gate_rows == 1 ? a.gate : nullptr, a.d * (a.g_bf16 ? 2 : 4), &g->gate);
-  return finish_geom(*g, shape_of(a.T, a.d), 0, 2, a.x_bf16 ? kRingBf16 : kRingF32);
+  const TeamShape s = shape_of(a.T, a.d);
+  const int third = s.warps == 1 && !a.f_bf16 ? kWarpF32Third : s.teams == 1 ? kTeamSmem : 0;
+  return finish_geom(*g, s, 0, 2, a.x_bf16 ? kRingBf16 : kRingF32, third);
 }
 
 template <typename F, typename X, int VPT>

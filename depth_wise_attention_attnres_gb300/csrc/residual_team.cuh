@@ -72,15 +72,17 @@ inline void add_input(TeamGeom& g, const void* p, int bytes, int* at) {
   g.stage_bytes += bytes;
 }
 // Cuts the teams' rings out of `budget` bytes of shared memory, or of all of it
-// where the budget does not hold `least` rows; false if that does not either.
-inline bool finish_geom(TeamGeom& g, const TeamShape& s, int gain_bytes, int least, int budget) {
+// where the budget does not hold two rows; false if that does not hold `least`. A
+// third row of every team may take up to `third` bytes.
+inline bool finish_geom(TeamGeom& g, const TeamShape& s, int gain_bytes, int least, int budget, int third) {
   g.warps = s.warps;
   g.teams = s.teams;
   g.gain = kGainOff;
   g.stages = kGainOff + gain_bytes;
   const int most = (kTeamSmem - g.stages) / (g.teams * g.stage_bytes);
   g.nst = budget / (g.teams * g.stage_bytes);
-  if (g.nst < least) g.nst = least;
+  if (g.nst < 3 && most >= 3 && 3 * g.teams * g.stage_bytes <= third) g.nst = 3;
+  if (g.nst < 2) g.nst = 2;
   if (g.nst > most) g.nst = most;
   if (g.nst > kMaxStages) g.nst = kMaxStages;
   g.total = g.stages + g.nst * g.teams * g.stage_bytes;
