@@ -201,12 +201,30 @@ __global__ void __launch_bounds__(gated_warps(VPT) * 32, 1)
   const bool post_norm = a.gpost != nullptr;
   const float inv_d = 1.0f / static_cast<float>(d);
   // scale * gamma_post, with a shared gate times its value too; gamma_pre; the
-  // sums over the tokens of earlier runs. What is in shared memory is each
-  // thread's own part.
+  // sums over the tokens of earlier runs (of the widest rows, whose one team needs
+  // the room for a row, in the CTA's partial row: 4096 x 8192 bf16 with shared gate
+  // rows at 51 % of the copy bandwidth, in shared memory 39). What is in memory is
+  // each thread's own part.
   constexpr bool kWide = VPT == 2;
   V8 gain_reg[VPT] = {}, gpre_reg[VPT] = {}, slope;
   auto kept = [&](int which) { return reinterpret_cast<float*>(smem + g.gain) + which * d; };
-  auto earlier = [&]() { return !kWide ? kept(0) + static_cast<int>(threadIdx.x) / (g.warps * 32) * d : kept(2); };
+  auto ld_earlier = [&](int k) {
+    if constexpr (!kWide) return ld8(kept(0) + static_cast<int>(threadIdx.x) / (g.warps * 32) * d + k);
+    const float* p = sums + static_cast<int64_t>(blockIdx.x) * d + k;
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = make_float2(p[2 * i], p[2 * i + 1]);
+    return r;
+  };
+  auto st_earlier = [&](int k, const V8& x) {
+    if constexpr (!kWide) {
+      st8(kept(0) + static_cast<int>(threadIdx.x) / (g.warps * 32) * d + k, x);
+    } else {
+      float* p = sums + static_cast<int64_t>(blockIdx.x) * d + k;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[2 * i] = x.p[i].x, p[2 * i + 1] = x.p[i].y;
+    }
+  };
   auto gain = [&](int v, int k) {
     if constexpr (kWide) return ld8(kept(0) + k);
     else return gain_reg[v];
@@ -243,7 +261,7 @@ __global__ void __launch_bounds__(gated_warps(VPT) * 32, 1)
         st8(kept(1) + k, a.dn ? ld8(a.gpre + k) : gpre_reg[v]);
       else if (a.dn)
         gpre_reg[v] = ld8(a.gpre + k);
-      if (GATE == kSharedGate) st8(earlier() + k, acc[v]);
+      if (GATE == kSharedGate) st_earlier(k, acc[v]);
     }
   }
 
@@ -347,7 +365,7 @@ __global__ void __launch_bounds__(gated_warps(VPT) * 32, 1)
         const int k = k0 + v * step;
         if (k < d) {
           const V8 post = flush_gate(a, m, shared_part, g.teams, (m.r0 + run_end - 1) / a.gate_rows, k, acc[v]);
-          st8(earlier() + k, add8(ld8(earlier() + k), post));
+          st_earlier(k, add8(ld_earlier(k), post));
           acc[v] = fill8(0.f);
         }
       }
@@ -359,7 +377,7 @@ __global__ void __launch_bounds__(gated_warps(VPT) * 32, 1)
     const int k = k0 + v * step;
     post[v] = gate[v] = acc[v];
     if (k < d) {
-      if (GATE == kSharedGate) post[v] = ld8(earlier() + k);
+      if (GATE == kSharedGate) post[v] = ld_earlier(k);
       if (GATE == kNoGate && a.gate) post[v] = flush_gate(a, m, nullptr, g.teams, 0, k, gate[v]);
     }
   }
@@ -376,10 +394,11 @@ bool geom_of(const ResidualBwdArgs& a, TeamGeom* g) {
   add_input(*g, a.dn, a.d * es, &g->dn);
   add_input(*g, a.gate && a.gate_rows == 1 ? a.gate : nullptr, a.d * (a.g_bf16 ? 2 : 4), &g->gate);
   const TeamShape s = shape_of(a);
-  // With 16 features a thread the gated kernel's gains, and where runs of tokens
-  // share gate rows the sums of earlier runs.
+  // With 16 features a thread the gated kernel's gains; else, where runs of tokens
+  // share gate rows, the sums of earlier runs.
   int gain_bytes = a.f && s.vectors == 2 ? 8 * a.d : 0;
-  if (a.f && gate_kind(a.T, a.gate_rows, a.gate != nullptr) == kSharedGate) gain_bytes += 4 * s.teams * a.d;
+  if (a.f && s.vectors != 2 && gate_kind(a.T, a.gate_rows, a.gate != nullptr) == kSharedGate)
+    gain_bytes = 4 * s.teams * a.d;
   const bool all_bf16 = a.f_bf16 && a.dx_bf16;
   const int ring = a.f                            ? kGatedRing
                    : a.d > 200 && a.d <= 256      ? kNarrowNormRing

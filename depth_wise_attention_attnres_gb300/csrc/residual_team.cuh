@@ -18,7 +18,6 @@ constexpr int kMaxTeamD = 8192;
 constexpr int kMaxStages = 8;
 constexpr int kRedOff = 2048;          // after the barriers (at most 32 teams x 8 stages)
 constexpr int kRedFloats = 32;         // of a team, for every 4 warps: 2 x 4 values x 4
-constexpr int kGainOff = 4096;         // after the teams' sums (at most 15 teams of 2 to 4 warps, or 8 quads)
 constexpr int kTeamSmem = 227 * 1024;
 
 struct TeamGeom {
@@ -77,8 +76,8 @@ inline void add_input(TeamGeom& g, const void* p, int bytes, int* at) {
 inline bool finish_geom(TeamGeom& g, const TeamShape& s, int gain_bytes, int least, int budget, int third) {
   g.warps = s.warps;
   g.teams = s.teams;
-  g.gain = kGainOff;
-  g.stages = kGainOff + gain_bytes;
+  g.gain = kRedOff + (s.warps > 1 ? s.teams * ((s.warps + 3) / 4) * kRedFloats * 4 : 0);  // after the teams' sums
+  g.stages = g.gain + gain_bytes;
   const int most = (kTeamSmem - g.stages) / (g.teams * g.stage_bytes);
   g.nst = budget / (g.teams * g.stage_bytes);
   if (g.nst < 3 && most >= 3 && 3 * g.teams * g.stage_bytes <= third) g.nst = 3;
@@ -254,7 +253,7 @@ __device__ __forceinline__ void init_bars(const TeamGeom& g, unsigned char* smem
     mbar_fence_init();
   }
   float* red = reinterpret_cast<float*>(smem + kRedOff);
-  for (int i = threadIdx.x; i < (kGainOff - kRedOff) / 4; i += blockDim.x) red[i] = 0.f;
+  for (int i = threadIdx.x; i < (g.gain - kRedOff) / 4; i += blockDim.x) red[i] = 0.f;
   __syncthreads();
 }
 

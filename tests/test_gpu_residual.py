@@ -226,6 +226,20 @@ def test_same_bits_and_accumulate(T, d, gate_rows):
     assert all(torch.equal(acc[k], start[k] + a[k]) for k in acc)
 
 
+# Rings of one row and of two, several runs of a gate row to a team, scratch that is not on 16 bytes.
+@pytest.mark.parametrize("types", [("bf16", "bf16", "bf16"), ("bf16", "f32", "f32"), ("f32", "f32", "f32")])
+@pytest.mark.parametrize("T,gate_rows", [(500, 1), (500, 2), (500, 3), (500, 200), (1, 2), (7, 2)])
+def test_widest_rows(T, gate_rows, types):
+    c = Case(T, 8192, types, gate_rows=gate_rows, gate_type="f32")
+    check_backward(c)
+    need = ar.attnres_gated_residual_bwd_scratch_floats(T, 8192, gate_rows)
+    a, b = c.outputs(), c.outputs()
+    c.backward(a, scratch=torch.empty(need, device=dev()))
+    c.backward(b, scratch=torch.full((need + 1,), float("nan"), device=dev())[1:])
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    assert ar.attnres_device_status() == 0
+
+
 @pytest.mark.parametrize("T,d", [(50, 640), (50, 100), (12, 8192)])
 def test_outputs_not_wanted(T, d):
     c = Case(T, d, gate_rows=50, gate_type="f32")
