@@ -187,8 +187,10 @@ __global__ void __launch_bounds__(norm_warps(VPT) * 32, 1)
 // dx_out and dx. GATE kNoGate also takes the one gate row of all tokens, which
 // rides on the gain. VPT: 8 or 24 features a thread, with the gains in registers,
 // or for the widest rows 16 (one team a CTA), with the gains in shared memory
-// and rings that may hold a single row.
-template <typename F, typename X, typename G, int GATE, int VPT>
+// and rings that may hold a single row. FAR: gamma_pre is read from the L2 for each
+// row, which leaves room for a second one (a switch while running cost the
+// others up to 6 %).
+template <typename F, typename X, typename G, int GATE, int VPT, bool FAR = false>
 __global__ void __launch_bounds__(gated_warps(VPT) * 32, 1)
     residual_bwd_kernel(ResidualBwdArgs a, const __grid_constant__ TeamGeom g, float* sums, float* shared_part) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(gated_warps(VPT) * 32, 1)
     else return gain_reg[v];
   };
   auto gpre = [&](int v, int k) {
-    if constexpr (kWide) return ld8(kept(1) + k);
+    if constexpr (kWide) return ld8((FAR ? a.gpre : kept(1)) + k);
     else return gpre_reg[v];
   };
   auto set_gain = [&](int64_t group) {
@@ -257,10 +259,10 @@ __global__ void __launch_bounds__(gated_warps(VPT) * 32, 1)
     const int k = k0 + v * step;
     acc[v] = pre[v] = gpre_reg[v] = fill8(0.f);
     if (k < d) {
-      if (kWide)
-        st8(kept(1) + k, a.dn ? ld8(a.gpre + k) : gpre_reg[v]);
-      else if (a.dn)
+      if (a.dn) {
         gpre_reg[v] = ld8(a.gpre + k);
+        if (kWide && !FAR) st8(kept(1) + k, gpre_reg[v]);
+      }
       if (GATE == kSharedGate) st_earlier(k, acc[v]);
     }
   }
@@ -397,6 +399,14 @@ bool geom_of(const ResidualBwdArgs& a, TeamGeom* g) {
   // With 16 features a thread the gated kernel's gains; else, where runs of tokens
   // share gate rows, the sums of earlier runs.
   int gain_bytes = a.f && s.vectors == 2 ? 8 * a.d : 0;
+  // Where two rows fit only without it, gamma_pre is read from the L2 for each row
+  // (4096 x 8192 ungated with an fp32 stream at 72 % of the copy bandwidth, by single
+  // rows 57).
+  if (gain_bytes && a.dn && kTeamSmem - rows_offset(s) - gain_bytes < 2 * g->stage_bytes &&
+      kTeamSmem - rows_offset(s) - gain_bytes / 2 >= 2 * g->stage_bytes) {
+    g->far_gain = 1;
+    gain_bytes /= 2;
+  }
   if (a.f && s.vectors != 2 && gate_kind(a.T, a.gate_rows, a.gate != nullptr) == kSharedGate)
     gain_bytes = 4 * s.teams * a.d;
   const bool all_bf16 = a.f_bf16 && a.dx_bf16;
@@ -423,6 +433,11 @@ template <typename F, typename X, typename G, int GATE>
 cudaError_t launch_gate(const ResidualBwdArgs& a, const Plan& p) {
   const int v = shape_of(a).vectors;
   if (v == 1) return launch_teams(residual_bwd_kernel<F, X, G, GATE, 1>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  // (Rows of fewer bytes leave room for two beside both gains.)
+  if constexpr (GATE == kTokenGate || 2 * sizeof(F) + sizeof(X) + sizeof(G) > 10)
+    if (p.g.far_gain)
+      return launch_teams(residual_bwd_kernel<F, X, G, GATE, 2, true>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
+  if (p.g.far_gain) return cudaErrorInvalidValue;
   if (v == 2) return launch_teams(residual_bwd_kernel<F, X, G, GATE, 2>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);
   if constexpr (GATE != kSharedGate)
     return launch_teams(residual_bwd_kernel<F, X, G, GATE, 3>, p.g, p.ctas, p.s, a, p.g, p.sums, p.shared);

@@ -27,6 +27,7 @@ struct TeamGeom {
   int bytes[5], off[5];       // of one row
   int f, x, dxo, dn, gate;    // offsets in a stage of what is there
   int gain, stages;           // where gains kept in shared memory and the rings begin
+  int far_gain;               // gamma_pre is not kept
   int64_t withhold;
 };
 
@@ -70,13 +71,17 @@ inline void add_input(TeamGeom& g, const void* p, int bytes, int* at) {
   g.off[g.n++] = g.stage_bytes;
   g.stage_bytes += bytes;
 }
+// What lies before the rings and the gains: the barriers, and the sums of teams of several warps.
+inline int rows_offset(const TeamShape& s) {
+  return kRedOff + (s.warps > 1 ? s.teams * ((s.warps + 3) / 4) * kRedFloats * 4 : 0);
+}
 // Cuts the teams' rings out of `budget` bytes of shared memory, or of all of it
 // where the budget does not hold two rows; false if that does not hold `least`. A
 // third row of every team may take up to `third` bytes.
 inline bool finish_geom(TeamGeom& g, const TeamShape& s, int gain_bytes, int least, int budget, int third) {
   g.warps = s.warps;
   g.teams = s.teams;
-  g.gain = kRedOff + (s.warps > 1 ? s.teams * ((s.warps + 3) / 4) * kRedFloats * 4 : 0);  // after the teams' sums
+  g.gain = rows_offset(s);
   g.stages = g.gain + gain_bytes;
   const int most = (kTeamSmem - g.stages) / (g.teams * g.stage_bytes);
   g.nst = budget / (g.teams * g.stage_bytes);

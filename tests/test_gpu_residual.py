@@ -240,6 +240,18 @@ def test_widest_rows(T, gate_rows, types):
     assert ar.attnres_device_status() == 0
 
 
+# Rows of which an SM holds two when gamma_pre is not kept there, and the widths on both sides.
+@pytest.mark.parametrize("types,gate,gate_rows,gate_type,d", [
+    (types, gate, rows, gate_type, d) for types, gate, rows, gate_type, edges in [
+        (("bf16", "f32", "f32"), "none", 1, "bf16", (7184, 8192)), (("bf16", "f32", "f32"), "sigmoid", 3, "f32", (7184, 8192)),
+        (("bf16", "f32", "f32"), "sigmoid", 1, "bf16", (6384, 7184)), (("f32", "f32", "f32"), "none", 1, "bf16", (5744, 6384)),
+        (("f32", "f32", "f32"), "sigmoid", 3, "f32", (5744, 6384)), (("f32", "f32", "f32"), "sigmoid", 1, "bf16", (5224, 5744)),
+        (("bf16", "bf16", "bf16"), "sigmoid", 1, "f32", (7184, 8192))]
+    for d in (edges[0] - 8, edges[0], edges[0] + 8, edges[1] - 8, edges[1], min(edges[1] + 8, 8192))])
+def test_two_rows_in_an_sm(types, gate, gate_rows, gate_type, d):
+    check_backward(Case(400, d, types, gate=gate, gate_rows=gate_rows, gate_type=gate_type, seed=d))
+
+
 @pytest.mark.parametrize("T,d", [(50, 640), (50, 100), (12, 8192)])
 def test_outputs_not_wanted(T, d):
     c = Case(T, d, gate_rows=50, gate_type="f32")
