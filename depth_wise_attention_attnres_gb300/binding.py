@@ -167,6 +167,19 @@ def _stream(stream, device: int | None = None) -> int | None:
     return int(stream)
 
 
+def _new_scratch(floats: int, device: torch.device, stream) -> torch.Tensor:
+    """fp32 scratch for a call on `stream`, from that stream's pool. A block of the current stream's pool could still be
+    in use by work queued there, which the call does not wait for; a block of the call's own stream is used in its
+    order, before the call and after it. (A handle of another library's stream stands for that stream for as long as
+    the program runs; 0 is the default stream.)"""
+    if stream is None:
+        return torch.empty(floats, device=device, dtype=torch.float32)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(floats, device=device, dtype=torch.float32)
+
+
 def _check(name: str, status: int) -> None:
     if status != 0:
         raise AttnResError(name, status)
@@ -284,7 +297,7 @@ def attnres_block_bwd(Src: torch.Tensor, F: torch.Tensor, N: int, S: int, W: tor
             raise ValueError("dW and dGamma must be contiguous fp32 [N*S, d]")
     need = attnres_block_bwd_scratch_floats(N, S, T, d)
     if scratch is None:
-        scratch = torch.empty(need, device=F.device, dtype=torch.float32)
+        scratch = _new_scratch(need, F.device, stream)
     if scratch.dtype != torch.float32 or scratch.numel() < need:
         raise ValueError(f"scratch must be fp32 with at least {need} elements")
     _check("attnres_block_bwd", lib().attnres_block_bwd(
@@ -377,14 +390,10 @@ def _two_dims(name: str, t: torch.Tensor) -> torch.Size:
 
 
 def _scratch(scratch, need, device: int, stream) -> torch.Tensor:
-    """A call's scratch: the caller's (whose size the library checks), or a new one of need() elements that lives
-    until `stream` is done with it."""
+    """A call's scratch: the caller's (whose size the library checks), or a new one of need() elements."""
     if scratch is None:
-        scratch = torch.empty(need(), device=torch.device("cuda", device), dtype=torch.float32)
-        if stream is not None:
-            scratch.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                  torch.cuda.ExternalStream(int(stream)))
-    elif scratch.dtype is not torch.float32 or not scratch.is_contiguous() or scratch.get_device() != device:
+        return _new_scratch(need(), torch.device("cuda", device), stream)
+    if scratch.dtype is not torch.float32 or not scratch.is_contiguous() or scratch.get_device() != device:
         raise ValueError("scratch must be contiguous fp32 on the current CUDA device")
     return scratch
 
