@@ -248,6 +248,22 @@ __device__ __forceinline__ void scale_segment(const TI* src, TO* dst, int64_t n,
   }
 }
 
+// The same where max_norm / norm is below fp32's normal range, and so off by up to all of itself, while the scaled
+// elements need not be: (g 2^-80) (1 / (norm 2^-80)) max_norm. Here norm > 2^126 max_norm, so max_norm < 4 and the
+// reciprocal is normal; a subnormal product is off by half a step of 2^-149, which max_norm makes at most 2^-148.
+// Element by element: norms that large are rare.
+__device__ __forceinline__ void scale_segment_far(const void* src, void* dst, int kind, int64_t first, int64_t n,
+                                                  float inv, float max_norm) {
+  for (int64_t k = first + threadIdx.x; k < first + n; k += kThreads) {
+    const float g = kind & 1 ? to_f32(static_cast<const bf16*>(src)[k]) : static_cast<const float*>(src)[k];
+    const float r = g * 0x1p-80f * inv * max_norm;
+    if (kind & 2)
+      static_cast<bf16*>(dst)[k] = from_f32<bf16>(r);
+    else
+      static_cast<float*>(dst)[k] = r;
+  }
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads)
     grad_scale_kernel(const __grid_constant__ Table<N> t, const float* part, int parts, float max_norm, float* norm) {
@@ -257,6 +273,13 @@ __global__ void __launch_bounds__(kThreads)
   const float r = norm_of(part, parts, red);
   if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = r;
   const float c = (r > max_norm && r < INFINITY) ? max_norm / r : 1.0f;
+  if (c < 0x1p-126f && max_norm > 0.f) {
+    const float inv = 1.0f / (r * 0x1p-80f);
+    for_segments(t, [&](int i, int64_t a, int64_t n) {
+      scale_segment_far(t.src[i], t.dst[i], t.kind[i], a, n, inv, max_norm);
+    });
+    return;
+  }
   for_segments(t, [&](int i, int64_t a, int64_t n) {
     if (c == 1.0f && t.src[i] == t.dst[i]) return;
     switch (t.kind[i]) {

@@ -265,3 +265,30 @@ def test_a_tensor_past_32_bit_offsets():
     ref.check(t[-3:], torch.full((3,), 2.0 / want, dtype=torch.float64, device=dev()),
               torch.full((3,), 40 * U, dtype=torch.float64, device=dev()), "clipped")
     assert int((t != 0).sum()) == 4
+
+
+@pytest.mark.parametrize("max_norm", [1e-3, 1e-8, 1e-20, 1e-30])
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 1e12, 1e30, 2e36])
+@pytest.mark.parametrize("kind,out", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
+def test_clipping_over_the_whole_range(kind, out, size, max_norm):
+    # max_norm / norm goes far below fp32's normal range here; the clipped elements do not. Each is a product of at
+    # most three rounded factors (the norm's error, its reciprocal, two products), then its own rounding; a factor
+    # or an element below 2^-126 is off by at most half a step of 2^-149, the factor times a max_norm under 4.
+    grads = [(inputs.randn((n,), "f32", inputs.generator(n, dev()), dev()).clamp_(-3, 3) * size).to(dtype_of(kind))
+             for n in (3000, 11, 8, 2049)]
+    want = ref.norm_of(grads)
+    by = min(1.0, max_norm / want)
+    for outs in (None, [torch.full(t.shape, float("nan"), device=dev(), dtype=dtype_of(out)) for t in grads]):
+        if outs is None and kind != out:
+            continue
+        mine = [t.clone() for t in grads]
+        norm = torch.empty(1, device=dev())
+        ar.attnres_grad_clip(mine, max_norm, norm, outs)
+        for a, b in zip(grads, mine if outs is None else outs):
+            value = a.double() * by
+            half = ref.HALF[b.dtype]
+            tiny = 2.0 ** -134 if b.dtype == torch.bfloat16 else 2.0 ** -150   # half a step below the normal range
+            limit = (norm_bound() + 3 * U) * value.abs() + 2.0 ** -148
+            limit = limit + torch.clamp(half * (value.abs() + limit), min=tiny)
+            assert torch.isfinite(b.float()).all()
+            assert ((b.double() - value).abs() <= limit).all()
