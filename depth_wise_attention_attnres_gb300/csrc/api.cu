@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <map>
 #include <memory>
 #include <mutex>
@@ -220,7 +221,7 @@ int check_residual(int64_t T, int32_t d, int32_t dtype, int32_t x_dtype, float e
                    const void* gate, int64_t gate_rows, int32_t gate_dtype, int32_t gate_act, float scale) {
   if (d < 1 || T < 0 || T > kMaxElements / d || !valid_dtype(dtype) || !valid_dtype(x_dtype) ||
       (dtype == ATTNRES_F32 && x_dtype != ATTNRES_F32) || !valid_eps(eps_post) || !valid_eps(eps_pre) ||
-      !(scale > -3.4e38f && scale < 3.4e38f))
+      !std::isfinite(scale))
     return ATTNRES_ERR_INVALID_ARG;
   if (gate_act != ATTNRES_GATE_IDENTITY && gate_act != ATTNRES_GATE_SIGMOID) return ATTNRES_ERR_INVALID_ARG;
   if (gate && (gate_rows < 1 || !valid_dtype(gate_dtype))) return ATTNRES_ERR_INVALID_ARG;

@@ -197,7 +197,8 @@ int attnres_rmsnorm(const void* x, int64_t T, int32_t d, int32_t dtype, const fl
  *               last run may be short).
  *   gate_rows   >= 1 (not looked at without a gate).
  *   gate_act    ATTNRES_GATE_IDENTITY, or ATTNRES_GATE_SIGMOID: 1/(1+exp(-g)).
- *   scale       host, finite.
+ *   scale       host, finite; so is scale * gamma_post, which the fast kernel
+ *               forms first.
  *   x_out       device, [T, d] of x_dtype; may be x (in place).
  *   gamma_pre   device, fp32 [d], and normed, device, [T, d] of dtype: both
  *               given, or both NULL (no pre-norm).
