@@ -298,22 +298,17 @@ __device__ __forceinline__ void give_up(const Team& m, const TeamGeom& g, int r,
     if (r != g.withhold) (void)mbar_wait(m.bars + r % m.nst * 8, static_cast<uint32_t>(r / m.nst & 1));
 }
 
-// Sums of N (1, 2 or 4) values over the team; every thread gets them. Also a
+// Sums of N (2 or 4) values over the team; every thread gets them. Also a
 // barrier of the team, which agrees on `ok`. Consecutive calls take the two
 // `buf`s in turn. In a warp the lanes' halves (and then quarters) each take one
 // of the values that are left, so 4 values cost 6 shuffles and not 20; lanes
 // 0, 16, 8 and 24 end with them.
 template <int N>
 __device__ __forceinline__ bool team_sum(const Team& m, float (&v)[N], int buf, bool ok) {
-  static_assert(N == 1 || N == 2 || N == 4, "one, two or four values");
+  static_assert(N == 2 || N == 4, "two or four values");
   const int lane = m.tid & 31;
   const bool upper = lane & 16, odd = lane & 8;
-  float c;
-  if constexpr (N == 1) {
-    c = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
-  } else {
-    c = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], 16);
-  }
+  float c = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], 16);
   if constexpr (N == 4) {
     const float b = (upper ? v[3] : v[2]) + __shfl_xor_sync(0xffffffffu, upper ? v[2] : v[3], 16);
     c = (odd ? b : c) + __shfl_xor_sync(0xffffffffu, odd ? c : b, 8);
@@ -325,7 +320,7 @@ __device__ __forceinline__ bool team_sum(const Team& m, float (&v)[N], int buf, 
   c += __shfl_xor_sync(0xffffffffu, c, 1);
   if (m.warps == 1) {
     v[0] = __shfl_sync(0xffffffffu, c, 0);
-    if constexpr (N > 1) v[1] = __shfl_sync(0xffffffffu, c, 16);
+    v[1] = __shfl_sync(0xffffffffu, c, 16);
     if constexpr (N > 2) {
       v[2] = __shfl_sync(0xffffffffu, c, 8);
       v[3] = __shfl_sync(0xffffffffu, c, 24);
