@@ -1144,8 +1144,12 @@ int attnres_block_pass(const void* F, int64_t f_stride, int32_t N, int32_t S, in
                             eps, T, d, dtype, outb + (k0 + j) * out_stride * es, nullptr, &a);
       if (st != ATTNRES_OK) return st;
       // The merge before this one writes neither O[j] nor any output f;
-      // stage 1 (before merge 1) writes O[j] but no output f.
-      a.early = j >= 2 ? 1 : 2;
+      // stage 1 (before merge 1) writes O[j] but no output f. The first
+      // block's merge 1 waits all the same: stage 1 lets it start before it
+      // has itself waited for the kernel before the pass, which may still be
+      // writing the outputs f (attnres_gated_residual lets the next kernel
+      // start at once). Every later kernel starts after a merge that waited.
+      a.early = j >= 2 ? 1 : (n > 0 ? 2 : 0);
       st = launched([&] { return launch_merge(a, as_stream(stream), merge_fast_ok(a)); });
       if (st != ATTNRES_OK) return st;
       if (plan[j]) m = j;
