@@ -1158,7 +1158,7 @@ int attnres_block_pass(const void* F, int64_t f_stride, int32_t N, int32_t S, in
     // reads the outputs and a kept sum from before that merge, and the merge
     // neither writes those nor reads Src[n + 1]; it lets the freeze start only
     // once it has waited for the kernel before it. So the freeze need not
-    // wait, unless the last merge kept the sum it reads.
+    // wait before it ends, unless the last merge kept the sum it reads.
     if (n + 1 < N || freeze_last) {
       AccumArgs a{};
       st = make_accum_parts(m > 0 ? P_scratch : nullptr, Fb + (k0 + m) * f_stride * es, f_stride, S - m, nullptr,

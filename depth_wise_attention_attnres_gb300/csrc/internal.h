@@ -151,9 +151,9 @@ struct AccumArgs {
   int64_t T;
   int d;
   int bf16;
-  // Skip the wait for the previous kernel: only when no kernel that may still
-  // be running writes what this one reads or reads what it writes (in a Block
-  // pass, the freeze after the block's last merge).
+  // Wait for the previous kernel at the end only: when no kernel that may
+  // still be running writes what this one reads or reads what it writes (in a
+  // Block pass, the freeze after the block's last merge).
   int no_wait = 0;
 };
 

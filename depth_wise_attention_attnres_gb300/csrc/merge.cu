@@ -536,6 +536,10 @@ __global__ void __launch_bounds__(kBlock) accum_fast_kernel(AccumArgs a, int64_t
     else
       st4(a.P_out + off, p);
   }
+  // A freeze that did not wait for the merge before it does so before it ends:
+  // the kernel after it waits for the freeze alone, and may read or overwrite
+  // what that merge writes and reads.
+  if (a.no_wait) pdl_wait();
 }
 
 template <typename T>

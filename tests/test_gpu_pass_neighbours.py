@@ -91,3 +91,11 @@ def test_the_pass_reads_what_the_call_before_it_wrote(N, S, T, d):
     keep = torch.empty_like(p.out)
     # Twice with another first output each, so that what was there before is never the right one.
     check([lambda: p.source(0), p.run, lambda: keep.copy_(p.out), lambda: p.source(1), p.run], [keep, p.out])
+
+
+@pytest.mark.parametrize("N,S,T,d", SHAPES)
+def test_the_call_after_a_frozen_pass_reads_what_it_wrote(N, S, T, d):
+    p = Pass(N, S, T, d)
+    # The last merge writes out[-1], and the freeze after it, which need not wait for the merge, ends the pass.
+    check([lambda: p.source(0), lambda: p.run(True), lambda: p.reader(0), lambda: p.source(1), lambda: p.run(True),
+           lambda: p.reader(1)], p.rows + [p.out, p.Src[1:]])
