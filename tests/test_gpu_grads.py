@@ -292,3 +292,22 @@ def test_clipping_over_the_whole_range(kind, out, size, max_norm):
             limit = limit + torch.clamp(half * (value.abs() + limit), min=tiny)
             assert torch.isfinite(b.float()).all()
             assert ((b.double() - value).abs() <= limit).all()
+
+
+def test_the_longest_table_captured():
+    # More tensors than one launch takes, their addresses as a captured kernel's arguments.
+    grads = make([100] * 1100 + [70_000], ["f32", "bf16"])
+    outs = [torch.empty_like(t) for t in grads]
+    kept, norm = ar.GradList(grads, outs), torch.empty(1, device=dev())
+    scratch = torch.empty(kept.scratch_floats, device=dev())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ar.attnres_grad_clip(kept, 1.0, norm, scratch=scratch)
+    for t in grads:
+        t.mul_(2)
+    graph.replay()
+    torch.cuda.synchronize()
+    want = ref.norm_of(grads)
+    assert abs(float(norm) - want) <= norm_bound() * want
+    for a, b in zip(grads, outs):
+        ref.check(b, a.double() / want, (norm_bound() + 3 * U) * a.double().abs() / want, "clipped")
