@@ -500,7 +500,10 @@ class GradList:
     Holds its tensors (contiguous fp32 or bf16, of any shape) and, for clipping
     out of place, where each goes. A program whose gradients stay in the same
     buffers keeps one; the values are read anew in every call. Tensors must not
-    be given other storage (set_, resize_) while it is in use."""
+    be given other storage (set_, resize_) while it is in use. Making one takes
+    about 0.7 us of host time a tensor and 0.6 an output (75 tensors: 54 us, with
+    outputs 99; a call with it 13 to 15), which a call with a plain list pays
+    every time (72 and 122 us)."""
 
     def __init__(self, grads, outs=None):
         self.grads, self.outs = list(grads), None if outs is None else list(outs)

@@ -2,13 +2,20 @@
 // 8192 with aligned rows (the formulas stand at the top of residual.cu, the
 // teams in residual_team.cuh).
 //
-// Bound by memory: each row is read and written once. The sums over tokens stay
-// in registers for the whole run of rows (a thread's features never change),
-// are added over the CTA's teams in shared memory and leave one partial row per
-// CTA; a gate row that some tokens share is written by the team that has all of
-// them, or left in two parts per team for one more kernel. The sums of row r's
-// second mean and of row r + 1's first ones go through the team together, so a
-// row costs one barrier.
+// Each row is read and written once, which bounds rows with an fp32 stream or
+// gradient (64M elements with a gate per token at 90 to 95 % of the copy bandwidth
+// from 512 to 5120 features). Rows of bf16 throughout take the same time for 1.4
+// times fewer bytes (32768 x 896 in 109 us, 63 %; 63 to 79 % from 512 to 8192
+// features, 58 at 384): a row's instructions and its barrier bound them, not its
+// bytes. Short runs of shared gate rows pay for their ends (32768 x 896 with an fp32
+// stream: 139 us with runs of 2 tokens, 108 with 8, 109 with a row each).
+//
+// The sums over tokens stay in registers for the whole run of rows (a thread's
+// features never change), are added over the CTA's teams in shared memory and
+// leave one partial row per CTA; a gate row that some tokens share is written by
+// the team that has all of them, or left in two parts per team for one more
+// kernel. The sums of row r's second mean and of row r + 1's first ones go through
+// the team together, so a row costs one barrier.
 #include "residual_team.cuh"
 
 namespace attnres {
@@ -17,10 +24,10 @@ namespace {
 __device__ unsigned int g_timeout = 0;
 
 // Warps of a CTA. The backward of RMSNorm: 28 of 72 registers, 16 of 128 for
-// 16 features a thread, 12 of 168 for 24. The gated one: 20 of 96 (8192 x 896 in
-// 34.6 us, with 16 of 128 36.0; 32749 x 640 with shared gate rows 72, with 16 77), 8 of
-// 255 for 24 features a thread; past the width that 8 features cover its threads
-// take 16, and 128 registers.
+// 16 features a thread, 12 of 168 for 24. The gated one: 20 of 96 (8192 x 896 takes
+// 4 % less than with 16 of 128, 32749 x 640 with shared gate rows 6 %), 8 of 255 for
+// 24 features a thread; past the width that 8 features cover its threads take 16, and
+// 128 registers. (With shared gate rows these spill 8 and 16 to 32 bytes.)
 constexpr int norm_warps(int vectors) { return vectors == 1 ? 28 : vectors == 2 ? 16 : 12; }
 constexpr int gated_warps(int vectors) { return vectors == 1 ? 20 : vectors == 2 ? 16 : 8; }
 // Rows in flight per SM, held as the forward's to what leaves the writes room
@@ -49,8 +56,8 @@ TeamShape norm_shape(int64_t T, int d, bool all_bf16) {
   return team_shape(T, d, v, norm_warps(v));
 }
 TeamShape gated_shape(int64_t T, int d, int gate) {
-  // (Not with shared gates, whose runs end more often on more teams: 32749 x 640
-  // took 77 us by single warps, 72 by three.)
+  // (Not with shared gates: 32749 x 640 in runs of 2048 tokens took 77 us by single
+  // warps, 72 by three.)
   const int v = d > 512 && d <= 704 && gate != kSharedGate ? 3 : (d > 256 * gated_warps(1) ? 2 : 1);
   return team_shape(T, d, v, gated_warps(v));
 }

@@ -1,12 +1,15 @@
 // The gated residual for d a multiple of 8 up to 8192 with aligned rows (the
 // formulas stand at the top of residual.cu, the teams in residual_team.cuh).
 //
-// Bound by memory: each row is read and written once. A thread holds its 8 or
+// Bound by memory: each row is read and written once (131072 x 2048 bf16 in 317
+// to 324 us by machine, 98 to 100 % of the copy bandwidth). Rows of few bytes are
+// bound by a row's fixed work instead: bf16 rows of 384 features run at 53 to 62 %,
+// of 5120 at 65 to 69, of 896 without x and normed at 51. A thread holds its 8 or
 // 16 features of the row and of the gains. The sum of squares of row r's result
 // and that of row r + 1's f go through the team together, so a row costs one
 // barrier. With 16 features a thread the teams take rows in turn (131072 x 2048
-// in 322 us, with a run of rows each 354); with 8 a run each was better (104857 x
-// 640: 92 % of the copy bandwidth against 86).
+// takes 9 % less by it than with a run of rows each); with 8 a run each was better
+// (104857 x 640: 92 % of the copy bandwidth against 86).
 #include "residual_team.cuh"
 
 namespace attnres {
@@ -14,9 +17,9 @@ namespace {
 
 __device__ unsigned int g_timeout = 0;
 
-// 28 warps of 72 registers, 16 of 128 for 16 features a thread, 12 of 168 for
-// 24: with 32 of 64 and 20 of 96 the spills cost more than the warps brought
-// (131072 x 2048 in 364 us against 319).
+// 28 warps of 72 registers (which spills 4 to 20 bytes), 16 of 128 for 16 features a
+// thread, 12 of 168 for 24: with 32 of 64 and 20 of 96 the spills cost more than the
+// warps brought (131072 x 2048 took 14 % longer).
 constexpr int max_warps(int vectors) { return vectors == 1 ? 28 : vectors == 2 ? 16 : 12; }
 // Rows in flight per SM: with all of the 227 KB the reads crowd out the writes,
 // the wider ones of an fp32 stream sooner (65536 x 1024 with a gate at 84 % of the

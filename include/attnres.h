@@ -207,7 +207,9 @@ int attnres_rmsnorm(const void* x, int64_t T, int32_t d, int32_t dtype, const fl
  * Outputs overlap nothing but, for x_out, x itself. Rows whose squares
  * overflow fp32 (elements of about 1e19) are outside what RMSNorm computes
  * here, as in attnres_rmsnorm. Any d >= 1; d a multiple of 8 up to 8192 with
- * 16-byte aligned pointers takes the fast kernel.
+ * 16-byte aligned pointers takes the fast kernel. Others take a general one,
+ * here and in the two backwards below: about 3 times as long forward, 6 to 8
+ * times backward, where measured.
  */
 typedef enum { ATTNRES_GATE_IDENTITY = 0, ATTNRES_GATE_SIGMOID = 1 } attnres_gate_act;
 
