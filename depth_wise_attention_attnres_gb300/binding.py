@@ -68,6 +68,13 @@ _SIGNATURES = {
     "attnres_grad_norm": [_VP, _VP, _VP, _I32, _VP, _VP, _I64, _VP],
     "attnres_grad_clip": [_VP, _VP, _VP, _VP, _VP, _I32, _F, _VP, _VP, _I64, _VP],
     "attnres_grad_norm_scratch_floats": [_I32],
+    "attnres_q8_row_bytes": [_I32],
+    "attnres_q8_write": [_VP, _I64, _I32, _I64, _I32, _I32, _VP, _I64, _VP],
+    "attnres_q8_read": [_VP, _I64, _I32, _I64, _I32, _VP, _I64, _I32, _VP],
+    "attnres_full_fwd_q8": [_VP, _I64, _I32, _I64, _I32, _VP, _VP, _VP, _F, _VP, _F, _VP, _VP, _I32, _VP],
+    "attnres_q8_weight": [_VP, _I32, _I32, _I32, _VP, _VP],
+    "attnres_q8_weight_bytes": [_I32, _I32],
+    "attnres_query_projection_q8": [_VP, _I64, _I32, _VP, _I32, _VP, _VP],
     "attnres_device_status": [_VP],
     "attnres_selftest_wait_timeout": [_VP],
     "attnres_test_fail_launch": [_I64],
@@ -104,7 +111,7 @@ def lib() -> ctypes.CDLL:
                 fn = getattr(handle, name)
                 fn.argtypes = args
                 fn.restype = (ctypes.c_char_p if name == "attnres_status_string" else
-                              ctypes.c_int64 if name.endswith("_scratch_floats") or
+                              ctypes.c_int64 if name.endswith(("_scratch_floats", "_bytes")) or
                               name == "attnres_test_fail_launch" else ctypes.c_int)
             _lib = handle
     return _lib
@@ -575,6 +582,173 @@ def attnres_grad_clip(grads, max_norm: float, norm: torch.Tensor, outs=None, scr
     return norm
 
 
+Q8_GROUP = 128
+
+
+def attnres_q8_row_bytes(d: int) -> int:
+    """Bytes of one 8-bit row of d features (-1 for a width that has none)."""
+    return int(lib().attnres_q8_row_bytes(d))
+
+
+def attnres_q8_weight_bytes(m: int, d: int) -> int:
+    """Bytes of an 8-bit weight matrix [m, d] (-1 for sizes that have none)."""
+    return int(lib().attnres_q8_weight_bytes(m, d))
+
+
+class Q8Rows:
+    """n sources of T rows of d features in 8 bits: an AttnRes history, or (n = 1) hidden states.
+
+    Owns its storage (`buffer`, uint8 [n, T, attnres_q8_row_bytes(d)], zero at
+    first) or takes a given one; its pointer is kept, so the buffer must not be
+    given other storage (set_, resize_). `codes` (float8_e4m3fn [n, T, d]),
+    `exponents` (uint8 [n, T, ceil(d / 128)]: the scale of a group is
+    2^(exponent - 127)) and `mean_square` (fp32 [n, T]) are views of it.
+    tokens(t) is the same rows' first t tokens, for a batch smaller than T."""
+
+    def __init__(self, n: int, T: int, d: int, device=None, buffer: torch.Tensor | None = None):
+        row = attnres_q8_row_bytes(d)
+        if n < 1 or T < 0 or row < 0:
+            raise ValueError("n and d must be at least 1, T at least 0")
+        if buffer is None:
+            buffer = torch.zeros(n, T, row, dtype=torch.uint8, device="cuda" if device is None else device)
+        if buffer.dtype is not torch.uint8 or tuple(buffer.shape) != (n, T, row) or not buffer.is_cuda or T > 0 and (
+                buffer.stride(2) != 1 or T > 1 and buffer.stride(1) != row or n > 1 and buffer.stride(0) < T * row):
+            raise ValueError(f"buffer must be uint8 [{n}, {T}, {row}] on a CUDA device, with consecutive rows")
+        self.n, self.T, self.d, self.buffer = n, T, d, buffer
+        self.row, self.stride = row, buffer.stride(0) if n > 1 else T * row
+        self.pointer, self.device = buffer.data_ptr(), buffer.get_device()
+
+    def tokens(self, T: int) -> "Q8Rows":
+        if not 0 <= T <= self.T:
+            raise ValueError(f"0 to {self.T} tokens")
+        return Q8Rows(self.n, T, self.d, buffer=self.buffer[:, :T])
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self.buffer[..., :self.d].view(torch.float8_e4m3fn)
+
+    @property
+    def exponents(self) -> torch.Tensor:
+        groups = -(-self.d // Q8_GROUP)
+        return self.buffer[..., Q8_GROUP * groups:(Q8_GROUP + 1) * groups]
+
+    @property
+    def mean_square(self) -> torch.Tensor:
+        groups = -(-self.d // Q8_GROUP)
+        at = Q8_GROUP * groups + (groups + 3) // 4 * 4
+        return self.buffer[..., at:at + 4].view(torch.float32)[..., 0]
+
+
+class Q8Weight:
+    """A weight matrix [m, d] in 8 bits, one scale for each block of 128 x 128: attnres_q8_weight fills it.
+
+    `codes` (float8_e4m3fn [m, d]) and `exponents` (uint8 [ceil(m / 128),
+    ceil(d / 128)]) are views of its `buffer` (zero at first)."""
+
+    def __init__(self, m: int, d: int, device=None):
+        size = attnres_q8_weight_bytes(m, d)
+        if size < 0:
+            raise ValueError("m and d must be at least 1")
+        self.m, self.d = m, d
+        self.buffer = torch.zeros(size, dtype=torch.uint8, device="cuda" if device is None else device)
+        self.pointer, self.device = self.buffer.data_ptr(), self.buffer.get_device()
+
+    @property
+    def codes(self) -> torch.Tensor:
+        width = -(-self.d // Q8_GROUP) * Q8_GROUP
+        return self.buffer[:self.m * width].view(self.m, width)[:, :self.d].view(torch.float8_e4m3fn)
+
+    @property
+    def exponents(self) -> torch.Tensor:
+        groups = -(-self.d // Q8_GROUP)
+        return self.buffer[self.m * groups * Q8_GROUP:].view(-1, -(-groups // 16) * 16)[:, :groups]
+
+
+def _q8_side(name: str, x: torch.Tensor, rows: Q8Rows, src: int) -> tuple[int, int, int]:
+    """(n, T, stride) of a [T, d] tensor, or of [n, T, d] slices, that stands for the first T tokens of `rows` from
+    source `src` on."""
+    if x.dim() == 2:
+        n, (T, d), stride = 1, x.shape, 0
+        ok = T == 0 or (x.stride(1) == 1 or d == 1) and (x.stride(0) == d or T == 1)
+    else:
+        n, T, d, stride = _slices(x)
+        ok = n > 0
+    if not ok or d != rows.d or T > rows.T or src < 0 or src + n > rows.n:
+        raise ValueError(f"{name} must be [T, d] or [n, T, d] slices that fit the rows, got {list(x.shape)} at source {src} "
+                         f"of {[rows.n, rows.T, rows.d]}")
+    device = torch.cuda.current_device()
+    if x.get_device() != device or rows.device != device:
+        raise ValueError(f"{name} and the rows must be on the current CUDA device")
+    return n, T, stride
+
+
+def attnres_q8_write(x: torch.Tensor, rows: Q8Rows, src: int = 0, stream=None) -> Q8Rows:
+    """The sources x ([T, d], or n slices [n, T, d]; fp32 or bf16) into `rows`, sources src to src + n - 1, their
+    first T tokens."""
+    n, T, stride = _q8_side("x", x, rows, src)
+    _check("attnres_q8_write", (_lib or lib()).attnres_q8_write(
+        x.data_ptr(), stride, n, T, rows.d, _dtype(x), rows.pointer + src * rows.stride, rows.stride,
+        _stream(stream, rows.device)))
+    return rows
+
+
+def attnres_q8_read(rows: Q8Rows, out: torch.Tensor, src: int = 0, stream=None) -> torch.Tensor:
+    """The values of the sources src, src + 1, .. of `rows` into out ([T, d], or [n, T, d]; fp32 or bf16)."""
+    n, T, stride = _q8_side("out", out, rows, src)
+    _check("attnres_q8_read", (_lib or lib()).attnres_q8_read(
+        rows.pointer + src * rows.stride, rows.stride, n, T, rows.d, out.data_ptr(), stride, _dtype(out),
+        _stream(stream, rows.device)))
+    return out
+
+
+def attnres_full_fwd_q8(rows: Q8Rows, n_src: int, w: torch.Tensor | None, gamma: torch.Tensor, eps: float,
+                        out: torch.Tensor | None, Q: torch.Tensor | None = None, gamma_pre: torch.Tensor | None = None,
+                        eps_pre: float = 0.0, out_normed: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The Full read over the sources 0 .. n_src - 1 of `rows` into out [T, d] (their first T tokens), scored by the
+    query w (fp32 [d]) or by a query for each token, Q (fp32 [T, d]); with gamma_pre and out_normed also the
+    consuming sublayer's pre-norm of the result (out may then be None)."""
+    main = out if out is not None else out_normed
+    if main is None:
+        raise ValueError("out or out_normed must be given")
+    shape = T, d = _two_dims("out", main)
+    device, f32 = torch.cuda.current_device(), torch.float32
+    if d != rows.d or T > rows.T or not 1 <= n_src <= rows.n:
+        raise ValueError(f"{n_src} sources of [{T}, {d}] do not fit rows of {[rows.n, rows.T, rows.d]}")
+    if rows.device != device:
+        raise ValueError("rows must be on the current CUDA device")
+    _check("attnres_full_fwd_q8", (_lib or lib()).attnres_full_fwd_q8(
+        rows.pointer, rows.stride, n_src, T, d, _opt("w", w, (d,), f32, device), _opt("Q", Q, shape, f32, device),
+        _like("gamma", gamma, (d,), f32, device), eps, _opt("gamma_pre", gamma_pre, (d,), f32, device), eps_pre,
+        _opt("out", out, shape, main.dtype, device), _opt("out_normed", out_normed, shape, main.dtype, device),
+        _dtype(main), _stream(stream, device)))
+    return main
+
+
+def attnres_q8_weight(W: torch.Tensor, W8: Q8Weight, stream=None) -> Q8Weight:
+    """The weight matrix W (fp32 or bf16 [m, d]) into W8."""
+    device = torch.cuda.current_device()
+    if W8.device != device:
+        raise ValueError("W8 must be on the current CUDA device")
+    _check("attnres_q8_weight", (_lib or lib()).attnres_q8_weight(
+        _like("W", W, (W8.m, W8.d), W.dtype, device), W8.m, W8.d, _dtype(W), W8.pointer, _stream(stream, device)))
+    return W8
+
+
+def attnres_query_projection_q8(rows: Q8Rows, src: int, W8: Q8Weight, Q: torch.Tensor, stream=None) -> torch.Tensor:
+    """Q (fp32 [T, m]) = the first T tokens of source `src` of `rows`, times W8's transpose: the input-dependent query."""
+    T, m = _two_dims("Q", Q)
+    device = torch.cuda.current_device()
+    if m != W8.m or rows.d != W8.d or T > rows.T or not 0 <= src < rows.n:
+        raise ValueError(f"Q [{T}, {m}] does not fit source {src} of rows {[rows.n, rows.T, rows.d]} and weights "
+                         f"{[W8.m, W8.d]}")
+    if rows.device != device or W8.device != device:
+        raise ValueError("rows and W8 must be on the current CUDA device")
+    _check("attnres_query_projection_q8", (_lib or lib()).attnres_query_projection_q8(
+        rows.pointer + src * rows.stride, T, rows.d, W8.pointer, m, _like("Q", Q, (T, m), torch.float32, device),
+        _stream(stream, device)))
+    return Q
+
+
 def attnres_block_stage1(Src: torch.Tensor, n_src: int, W: torch.Tensor, Gamma: torch.Tensor,
                          eps: float, O: list, lse: torch.Tensor | None, stream=None) -> None:
     """Stage 1: the S = len(O) queries of W [S, d] over Src[0 .. n_src)."""
@@ -707,7 +881,7 @@ def attnres_test_fail_launch(after: int) -> int:
 
 
 # Kernels whose copy producer attnres_test_withhold_stage can starve.
-WITHHOLD_NONE, WITHHOLD_FULL, WITHHOLD_STAGE1_TC, WITHHOLD_MERGE, WITHHOLD_RESIDUAL = 0, 1, 2, 3, 4
+WITHHOLD_NONE, WITHHOLD_FULL, WITHHOLD_STAGE1_TC, WITHHOLD_MERGE, WITHHOLD_RESIDUAL, WITHHOLD_Q8_READ = 0, 1, 2, 3, 4, 5
 
 
 def attnres_test_withhold_stage(kernel: int, index: int = 0) -> None:

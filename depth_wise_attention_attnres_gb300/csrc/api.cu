@@ -316,6 +316,30 @@ int check_grads(const GradArgs& a, int64_t scratch_floats) {
   return ATTNRES_OK;
 }
 
+// n sources of T 8-bit rows, row_stride bytes apart, and the memory they span.
+int check_q8_span(const void* rows, int64_t row_stride, int32_t n, int64_t T, int32_t d, Range* span) {
+  const int64_t row = attnres_q8_row_bytes(d);
+  if (row < 0 || n < 1 || T < 0 || T > kMaxElements / row) return ATTNRES_ERR_INVALID_ARG;
+  if (T == 0) return ATTNRES_OK;
+  if (!rows || !aligned16(rows)) return ATTNRES_ERR_INVALID_ARG;
+  if (n > 1 && (row_stride < T * row || row_stride % 16 != 0 || row_stride > 2 * kMaxElements / n))
+    return ATTNRES_ERR_INVALID_ARG;
+  *span = range_of(rows, (n - 1) * (n > 1 ? row_stride : 0) + T * row);
+  return ATTNRES_OK;
+}
+
+// The same with the [T, d] slices that are written from or read back into.
+int check_q8_rows(const Q8Rows& a, int32_t dtype, Range* other, Range* span) {
+  if (!valid_dtype(dtype)) return ATTNRES_ERR_INVALID_ARG;
+  const int st = check_q8_span(a.rows, a.row_stride, a.n, a.T, a.d, span);
+  if (st != ATTNRES_OK || a.T == 0) return st;
+  const int64_t E = a.T * a.d;
+  if (!a.x || off_element(a.x, elem_size(dtype))) return ATTNRES_ERR_INVALID_ARG;
+  if (a.n > 1 && (a.x_stride < E || a.x_stride > 2 * kMaxElements / a.n)) return ATTNRES_ERR_INVALID_ARG;
+  *other = range_of(a.x, ((a.n - 1) * (a.n > 1 ? a.x_stride : 0) + E) * elem_size(dtype));
+  return ATTNRES_OK;
+}
+
 // Checks and fills the arguments of one full read. Returns a status.
 int make_full(const void* V, int64_t src_stride, int32_t n_src, int64_t T, int32_t d,
               int32_t v_dtype, const float* w, const float* gamma, float eps, void* out,
@@ -698,6 +722,75 @@ int attnres_full_fwd_dynq(const void* V, int64_t src_stride, int32_t n_src, int6
   a.w = nullptr;
   a.Q = Q;
   return run_full(a, as_stream(stream));
+}
+
+int64_t attnres_q8_row_bytes(int32_t d) { return d < 1 || d > kQ8MaxWidth ? -1 : q8_row_bytes(d); }
+
+int64_t attnres_q8_weight_bytes(int32_t m, int32_t d) {
+  if (m < 1 || d < 1 || m > kQ8MaxWidth || d > kQ8MaxWidth) return -1;
+  const int G = q8_groups(d);
+  return static_cast<int64_t>(m) * (128 * G) + static_cast<int64_t>(q8_groups(m)) * q8_block_row(G);
+}
+
+int attnres_q8_write(const void* x, int64_t x_stride, int32_t n, int64_t T, int32_t d, int32_t dtype, void* rows,
+                     int64_t row_stride, void* stream) {
+  Q8Rows a{x, x_stride, rows, row_stride, n, T, d, dtype == ATTNRES_BF16};
+  Range rx, rr;
+  const int st = check_q8_rows(a, dtype, &rx, &rr);
+  if (st != ATTNRES_OK || T == 0) return st;
+  if (overlap(rx, rr)) return ATTNRES_ERR_INVALID_ARG;
+  return launched([&] { return launch_q8_write(a, as_stream(stream)); });
+}
+
+int attnres_q8_read(const void* rows, int64_t row_stride, int32_t n, int64_t T, int32_t d, void* out,
+                    int64_t out_stride, int32_t out_dtype, void* stream) {
+  Q8Rows a{out, out_stride, const_cast<void*>(rows), row_stride, n, T, d, out_dtype == ATTNRES_BF16};
+  Range ro, rr;
+  const int st = check_q8_rows(a, out_dtype, &ro, &rr);
+  if (st != ATTNRES_OK || T == 0) return st;
+  if (overlap(ro, rr)) return ATTNRES_ERR_INVALID_ARG;
+  return launched([&] { return launch_q8_back(a, as_stream(stream)); });
+}
+
+int attnres_full_fwd_q8(const void* rows, int64_t row_stride, int32_t n_src, int64_t T, int32_t d, const float* w,
+                        const float* Q, const float* gamma, float eps, const float* gamma_pre, float eps_pre, void* out,
+                        void* out_normed, int32_t out_dtype, void* stream) {
+  if (!valid_dtype(out_dtype) || !valid_eps(eps) || (gamma_pre && !valid_eps(eps_pre))) return ATTNRES_ERR_INVALID_ARG;
+  Range rr;
+  const int st = check_q8_span(rows, row_stride, n_src, T, d, &rr);
+  if (st != ATTNRES_OK || T == 0) return st;
+  const int64_t os = elem_size(out_dtype), E = T * d;
+  if (!gamma || !w == !Q || !gamma_pre != !out_normed || (!out && !out_normed)) return ATTNRES_ERR_INVALID_ARG;
+  if (off_element(w, 4) || off_element(Q, 4) || off_element(gamma, 4) || off_element(gamma_pre, 4) || off_element(out, os) ||
+      off_element(out_normed, os))
+    return ATTNRES_ERR_INVALID_ARG;
+  const Range in[] = {rr, range_if(w, d * 4ll), range_if(Q, E * 4), range_of(gamma, d * 4ll), range_if(gamma_pre, d * 4ll)};
+  const Range outs[] = {range_if(out, E * os), range_if(out_normed, E * os)};
+  if (any_overlap(outs, in)) return ATTNRES_ERR_INVALID_ARG;
+  Q8ReadArgs a{rows, row_stride, n_src, T, d, w, Q, gamma, eps, {gamma_pre, eps_pre, out_normed}, out,
+               out_dtype == ATTNRES_BF16, withhold_for(kWithholdQ8Read)};
+  return launched([&] { return launch_q8_read(a, as_stream(stream)); });
+}
+
+int attnres_q8_weight(const void* W, int32_t m, int32_t d, int32_t dtype, void* W8, void* stream) {
+  const int64_t bytes = attnres_q8_weight_bytes(m, d);
+  if (bytes < 0 || !valid_dtype(dtype) || !W || !W8 || !aligned16(W8) || off_element(W, elem_size(dtype)))
+    return ATTNRES_ERR_INVALID_ARG;
+  if (overlap(range_of(W, static_cast<int64_t>(m) * d * elem_size(dtype)), range_of(W8, bytes))) return ATTNRES_ERR_INVALID_ARG;
+  return launched([&] { return launch_q8_weight(W, m, d, dtype == ATTNRES_BF16, W8, as_stream(stream)); });
+}
+
+int attnres_query_projection_q8(const void* rows, int64_t T, int32_t d, const void* W8, int32_t m, float* Q,
+                                void* stream) {
+  Range rr;
+  const int64_t bytes = attnres_q8_weight_bytes(m, d);
+  if (bytes < 0) return ATTNRES_ERR_INVALID_ARG;
+  const int st = check_q8_span(rows, 0, 1, T, d, &rr);
+  if (st != ATTNRES_OK || T == 0) return st;
+  if (T > kMaxElements / m || !W8 || !aligned16(W8) || !Q || off_element(Q, 4)) return ATTNRES_ERR_INVALID_ARG;
+  const Range rq = range_of(Q, T * m * 4);
+  if (overlap(rq, rr) || overlap(rq, range_of(W8, bytes))) return ATTNRES_ERR_INVALID_ARG;
+  return launched([&] { return launch_q8_proj(rows, T, d, W8, m, Q, as_stream(stream)); });
 }
 
 int attnres_rmsnorm(const void* x, int64_t T, int32_t d, int32_t dtype, const float* gamma, float eps, void* out,
@@ -1178,16 +1271,17 @@ int attnres_device_status(void* stream) {
     cudaGetLastError();
     return ATTNRES_ERR_CUDA;
   }
-  unsigned int f1 = 0, f2 = 0, f3 = 0, f4 = 0, f5 = 0, f6 = 0, f7 = 0, f8 = 0, f9 = 0, f10 = 0;
+  unsigned int f1 = 0, f2 = 0, f3 = 0, f4 = 0, f5 = 0, f6 = 0, f7 = 0, f8 = 0, f9 = 0, f10 = 0, f11 = 0, f12 = 0;
   if (take_timeout_full(&f1) != cudaSuccess || take_timeout_stage1(&f2) != cudaSuccess ||
       take_timeout_merge(&f3) != cudaSuccess || take_timeout_stage1tc(&f4) != cudaSuccess ||
       take_timeout_bwd(&f5) != cudaSuccess || take_timeout_proj(&f6) != cudaSuccess ||
       take_timeout_dsplit(&f7) != cudaSuccess || take_timeout_blockbwd(&f8) != cudaSuccess ||
-      take_timeout_residual_fwd(&f9) != cudaSuccess || take_timeout_residual_bwd(&f10) != cudaSuccess) {
+      take_timeout_residual_fwd(&f9) != cudaSuccess || take_timeout_residual_bwd(&f10) != cudaSuccess ||
+      take_timeout_q8_read(&f11) != cudaSuccess || take_timeout_q8_proj(&f12) != cudaSuccess) {
     cudaGetLastError();
     return ATTNRES_ERR_CUDA;
   }
-  if (f1 || f2 || f3 || f4 || f5 || f6 || f7 || f8 || f9 || f10) return ATTNRES_ERR_TIMEOUT;
+  if (f1 || f2 || f3 || f4 || f5 || f6 || f7 || f8 || f9 || f10 || f11 || f12) return ATTNRES_ERR_TIMEOUT;
   e = cudaGetLastError();
   return e == cudaSuccess ? ATTNRES_OK : ATTNRES_ERR_CUDA;
 }
@@ -1197,7 +1291,7 @@ int64_t attnres_test_fail_launch(int64_t after) {
 }
 
 int attnres_test_withhold_stage(int32_t kernel, int64_t index) {
-  if (kernel < kWithholdNone || kernel > kWithholdResidual || (kernel != kWithholdNone && index < 0))
+  if (kernel < kWithholdNone || kernel > kWithholdLast || (kernel != kWithholdNone && index < 0))
     return ATTNRES_ERR_INVALID_ARG;
   g_withhold_index.store(kernel == kWithholdNone ? -1 : index);
   g_withhold_kernel.store(kernel);

@@ -290,9 +290,49 @@ struct GradArgs {
 int run_grads(const GradArgs& a, cudaStream_t s);
 int64_t grads_scratch(int n);
 
+// 8-bit rows (attnres.h): groups and record layout.
+constexpr int kQ8MaxWidth = 1 << 24;
+constexpr int q8_groups(int d) { return (d + ATTNRES_Q8_GROUP - 1) / ATTNRES_Q8_GROUP; }
+constexpr int q8_mean_offset(int G) { return ATTNRES_Q8_GROUP * G + (G + 3) / 4 * 4; }
+constexpr int64_t q8_row_bytes(int d) { return (q8_mean_offset(q8_groups(d)) + 4 + 15) / 16 * 16; }
+constexpr int q8_block_row(int G) { return (G + 15) / 16 * 16; }  // bytes of a weight's row of block exponents
+struct Q8Rows {
+  const void* x;        // the [T, d] side: x when writing, out when reading back
+  int64_t x_stride;     // elements
+  void* rows;
+  int64_t row_stride;   // bytes
+  int n;
+  int64_t T;
+  int d;
+  int bf16;
+};
+struct Q8ReadArgs {
+  const void* rows;
+  int64_t row_stride;   // bytes
+  int n_src;
+  int64_t T;
+  int d;
+  const float* w;       // [d], or nullptr with Q
+  const float* Q;       // [T, d]
+  const float* gamma;
+  float eps;
+  PreNorm pre;
+  void* out;            // may be nullptr when pre.gamma is set
+  int out_bf16;
+  int64_t withhold = -1;  // test hook of the streaming kernel (as FullArgs; per warp)
+};
+cudaError_t launch_q8_write(const Q8Rows& a, cudaStream_t s);
+cudaError_t launch_q8_back(const Q8Rows& a, cudaStream_t s);
+cudaError_t launch_q8_weight(const void* W, int m, int d, int is_bf16, void* W8, cudaStream_t s);
+cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
+cudaError_t launch_q8_proj(const void* rows, int64_t T, int d, const void* W8, int m, float* Q, cudaStream_t s);
+cudaError_t take_timeout_q8_read(unsigned int* flag);
+cudaError_t take_timeout_q8_proj(unsigned int* flag);
+
 // Failure-path test hooks (api.cu), off by default. Which producer, if any,
 // withholds a copy: the tile index to leave unissued, or -1.
-enum WithholdKernel { kWithholdNone = 0, kWithholdFull = 1, kWithholdStage1Tc = 2, kWithholdMerge = 3, kWithholdResidual = 4 };
+enum WithholdKernel { kWithholdNone = 0, kWithholdFull = 1, kWithholdStage1Tc = 2, kWithholdMerge = 3, kWithholdResidual = 4,
+                      kWithholdQ8Read = 5, kWithholdLast = kWithholdQ8Read };
 int64_t withhold_for(WithholdKernel k);
 
 // Device-side timeout records of each kernel file: read and clear (blocking).

@@ -160,6 +160,121 @@ int attnres_full_fwd_dynq(const void* V, int64_t src_stride, int32_t n_src, int6
                           int32_t out_dtype, void* stream);
 
 /*
+ * 8-bit rows. The history of a Full read, and the hidden states its queries are
+ * projected from, may be held in 8 bits: half the bytes of bf16, and the read
+ * is bound by the history's bytes. The pages have no counterpart; they name the
+ * history's memory as the cost of Full AttnRes (DepthBench reading notes,
+ * section 4.7 and Fig. 11).
+ *
+ * A row of d features is cut into groups of ATTNRES_Q8_GROUP = 128 (the last
+ * may be short). With a_g the largest finite magnitude of group g, its scale is
+ * 2^e_g with e_g the smallest integer >= -126 such that a_g <= 448 * 2^e_g (448
+ * is the largest e4m3 number), and feature k is held as
+ *   c_k = x_k * 2^-e_g rounded to e4m3 (to nearest, ties to even),
+ * so it stands for v_k = c_k * 2^e_g. A power of two scales exactly: the codes
+ * follow from x alone, and writing what was read back gives the same values. A
+ * magnitude below 2^-117 keeps fewer than four bits. Where e_g = 120 codes stop
+ * at 240, so that v_k stays finite. An element that is not finite becomes NaN.
+ * With the row goes mean_k v_k^2 (fp32), the mean square its key RMSNorm needs
+ * in every read.
+ *
+ * A row is one record of attnres_q8_row_bytes(d) bytes, on a 16-byte boundary:
+ *   [0, 128 G)           codes, G = ceil(d / 128), zero from d on;
+ *   [128 G, 129 G)       e_g + 127 of each group, one byte each;
+ *   then, on the next 4-byte boundary, the mean square (fp32), and zeros up
+ *   to a multiple of 16 bytes.
+ * Rows of one source are consecutive. Pointers to rows must be 16-byte aligned,
+ * and strides between sources multiples of 16 bytes: else INVALID_ARG.
+ */
+#define ATTNRES_Q8_GROUP 128
+
+/* Bytes of one row: 16 ceil((128 G + 4 ceil(G / 4) + 4) / 16); -1 for d < 1 or d > 2^24. */
+int64_t attnres_q8_row_bytes(int32_t d);
+
+/*
+ * attnres_q8_write - n sources of T rows each into 8-bit rows (a history, one
+ * source at a time as sublayers finish, or as a whole).
+ *
+ *   x           device, n slices [T, d] of dtype, x_stride elements apart
+ *               (>= T*d; not looked at when n == 1).
+ *   rows        device, n slices of T rows, row_stride bytes apart (>= T *
+ *               attnres_q8_row_bytes(d); not looked at when n == 1). Every byte
+ *               of the T rows is written, none behind them. Must not overlap x.
+ * Any d; d a multiple of 8 (bf16) or 4 (fp32) in 16-byte aligned storage
+ * streams fastest.
+ */
+int attnres_q8_write(const void* x, int64_t x_stride, int32_t n, int64_t T, int32_t d,
+                     int32_t dtype, void* rows, int64_t row_stride, void* stream);
+
+/*
+ * attnres_q8_read - the values 8-bit rows stand for: out = c * 2^e. In bf16
+ * they are exact (codes have four significant bits) down to bf16's smallest
+ * number, so attnres_full_bwd over them is the backward of attnres_full_fwd_q8.
+ *
+ *   rows, row_stride, n, T, d   as attnres_q8_write.
+ *   out         device, n slices [T, d] of out_dtype, out_stride elements
+ *               apart (>= T*d; not looked at when n == 1). Must not overlap rows.
+ */
+int attnres_q8_read(const void* rows, int64_t row_stride, int32_t n, int64_t T, int32_t d,
+                    void* out, int64_t out_stride, int32_t out_dtype, void* stream);
+
+/*
+ * attnres_full_fwd_q8 - the Full read (attnres_full_fwd) over 8-bit rows: the
+ * sources are the values the rows stand for, and rms(v_i) comes from the
+ * rows' mean squares.
+ *
+ *   rows        device, n_src sources of T rows, row_stride bytes apart (>= T *
+ *               attnres_q8_row_bytes(d); not looked at when n_src == 1).
+ *   w           device, fp32 [d], the shared query, or NULL with Q.
+ *   Q           device, fp32 [T, d], a query for each token
+ *               (attnres_full_fwd_dynq), or NULL with w. One of the two.
+ *   gamma, eps  as attnres_full_fwd.
+ *   gamma_pre, eps_pre, out_normed   the consuming sublayer's pre-norm, as
+ *               attnres_full_fwd_prenorm; gamma_pre and out_normed both given
+ *               or both NULL.
+ *   out         device, [T, d] of out_dtype; NULL (z not stored) only with
+ *               out_normed.
+ * Outputs overlap nothing. d up to 2048 takes the streaming kernel, which
+ * shares a token's sources over several warps when tokens are few; wider rows take a general
+ * one, for which ATTNRES_ERR_UNSUPPORTED means 4 (n_src + 128 G) bytes are over
+ * 200 KB.
+ */
+int attnres_full_fwd_q8(const void* rows, int64_t row_stride, int32_t n_src, int64_t T, int32_t d,
+                        const float* w, const float* Q, const float* gamma, float eps,
+                        const float* gamma_pre, float eps_pre, void* out, void* out_normed,
+                        int32_t out_dtype, void* stream);
+
+/*
+ * attnres_q8_weight - a weight matrix in 8 bits with one scale for each block
+ * of 128 x 128 weights (the last ones of a row or column may be short), by the
+ * rule of the rows: a power of two from the block's largest finite magnitude.
+ *
+ *   W           device, [m, d] of dtype, row-major (m output features).
+ *   W8          device, attnres_q8_weight_bytes(m, d) bytes, 16-byte aligned:
+ *               m rows of 128 G codes (zero from d on), then, for each 128
+ *               output features, 16 ceil(G / 16) bytes: e + 127 of its G
+ *               blocks, then zeros. Must not overlap W.
+ */
+int attnres_q8_weight(const void* W, int32_t m, int32_t d, int32_t dtype, void* W8, void* stream);
+/* -1 for sizes below 1 or above 2^24. */
+int64_t attnres_q8_weight_bytes(int32_t m, int32_t d);
+
+/*
+ * attnres_query_projection_q8 - the input-dependent query's projection
+ * (attnres_query_projection) of 8-bit rows by an 8-bit weight matrix:
+ * Q[t, j] = sum_k v[t, k] W[j, k], with products of codes summed in fp32 over
+ * each block of 128 features and the blocks' sums scaled and added in fp32.
+ *
+ *   rows        device, T rows of d features.
+ *   W8          device, [m, d] as attnres_q8_weight laid it out, 16-byte aligned. m need not be
+ *               d: the queries of several reads may be projected at once.
+ *   Q           device, fp32 [T, m]; must not overlap rows or W8.
+ * The mean squares of the rows are not looked at.
+ */
+int attnres_query_projection_q8(const void* rows, int64_t T, int32_t d, const void* W8, int32_t m,
+                                float* Q, void* stream);
+
+/*
  * attnres_rmsnorm - RMSNorm of each row, out = gamma * x / sqrt(mean(x^2) + eps)
  * in fp32, stored in dtype: the sublayer pre-norm for a row no aggregation
  * call produces with it (the first sublayer of a block, whose output is
