@@ -9,6 +9,7 @@ the library has not been built the first call raises ``RuntimeError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -68,13 +69,13 @@ _SIGNATURES = {
     "attnres_grad_norm": [_VP, _VP, _VP, _I32, _VP, _VP, _I64, _VP],
     "attnres_grad_clip": [_VP, _VP, _VP, _VP, _VP, _I32, _F, _VP, _VP, _I64, _VP],
     "attnres_grad_norm_scratch_floats": [_I32],
-    "attnres_q8_row_bytes": [_I32],
+    "attnres_q8_source_bytes": [_I64, _I32],
     "attnres_q8_write": [_VP, _I64, _I32, _I64, _I32, _I32, _VP, _I64, _VP],
     "attnres_q8_read": [_VP, _I64, _I32, _I64, _I32, _VP, _I64, _I32, _VP],
     "attnres_full_fwd_q8": [_VP, _I64, _I32, _I64, _I32, _VP, _VP, _VP, _F, _VP, _F, _VP, _VP, _I32, _VP],
     "attnres_q8_weight": [_VP, _I32, _I32, _I32, _VP, _VP],
     "attnres_q8_weight_bytes": [_I32, _I32],
-    "attnres_query_projection_q8": [_VP, _I64, _I32, _VP, _I32, _VP, _VP],
+    "attnres_query_projection_q8": [_VP, _I64, _I64, _I32, _VP, _I32, _VP, _VP],
     "attnres_device_status": [_VP],
     "attnres_selftest_wait_timeout": [_VP],
     "attnres_test_fail_launch": [_I64],
@@ -585,9 +586,9 @@ def attnres_grad_clip(grads, max_norm: float, norm: torch.Tensor, outs=None, scr
 Q8_GROUP = 128
 
 
-def attnres_q8_row_bytes(d: int) -> int:
-    """Bytes of one 8-bit row of d features (-1 for a width that has none)."""
-    return int(lib().attnres_q8_row_bytes(d))
+def attnres_q8_source_bytes(cap: int, d: int) -> int:
+    """Bytes of a source of `cap` 8-bit rows of d features (-1 for sizes that have none)."""
+    return int(lib().attnres_q8_source_bytes(cap, d))
 
 
 def attnres_q8_weight_bytes(m: int, d: int) -> int:
@@ -598,45 +599,43 @@ def attnres_q8_weight_bytes(m: int, d: int) -> int:
 class Q8Rows:
     """n sources of T rows of d features in 8 bits: an AttnRes history, or (n = 1) hidden states.
 
-    Owns its storage (`buffer`, uint8 [n, T, attnres_q8_row_bytes(d)], zero at
-    first) or takes a given one; its pointer is kept, so the buffer must not be
-    given other storage (set_, resize_). `codes` (float8_e4m3fn [n, T, d]),
-    `exponents` (uint8 [n, T, ceil(d / 128)]: the scale of a group is
-    2^(exponent - 127)) and `mean_square` (fp32 [n, T]) are views of it.
-    tokens(t) is the same rows' first t tokens, for a batch smaller than T."""
+    Owns its storage (`buffer`, uint8 [n, attnres_q8_source_bytes(T, d)], zero
+    at first); its pointer is kept, so the buffer must not be given other
+    storage (set_, resize_). `codes` (float8_e4m3fn [n, T, d]), `exponents`
+    (uint8 [n, T, ceil(d / 128)]: the scale of a group is 2^(exponent - 127))
+    and `mean_square` (fp32 [n, T]) are views of it. Calls use the first rows,
+    as many as their [T, d] argument has."""
 
-    def __init__(self, n: int, T: int, d: int, device=None, buffer: torch.Tensor | None = None):
-        row = attnres_q8_row_bytes(d)
-        if n < 1 or T < 0 or row < 0:
+    def __init__(self, n: int, T: int, d: int, device=None):
+        source = attnres_q8_source_bytes(T, d)
+        if n < 1 or source < 0:
             raise ValueError("n and d must be at least 1, T at least 0")
-        if buffer is None:
-            buffer = torch.zeros(n, T, row, dtype=torch.uint8, device="cuda" if device is None else device)
-        if buffer.dtype is not torch.uint8 or tuple(buffer.shape) != (n, T, row) or not buffer.is_cuda or T > 0 and (
-                buffer.stride(2) != 1 or T > 1 and buffer.stride(1) != row or n > 1 and buffer.stride(0) < T * row):
-            raise ValueError(f"buffer must be uint8 [{n}, {T}, {row}] on a CUDA device, with consecutive rows")
-        self.n, self.T, self.d, self.buffer = n, T, d, buffer
-        self.row, self.stride = row, buffer.stride(0) if n > 1 else T * row
-        self.pointer, self.device = buffer.data_ptr(), buffer.get_device()
+        self.n, self.T, self.d, self.source = n, T, d, source
+        self.buffer = torch.zeros(n, source, dtype=torch.uint8, device="cuda" if device is None else device)
+        if not self.buffer.is_cuda:
+            raise ValueError("rows must be on a CUDA device")
+        self.pointer, self.device = self.buffer.data_ptr(), self.buffer.get_device()
 
-    def tokens(self, T: int) -> "Q8Rows":
-        if not 0 <= T <= self.T:
-            raise ValueError(f"0 to {self.T} tokens")
-        return Q8Rows(self.n, T, self.d, buffer=self.buffer[:, :T])
-
-    @property
+    @functools.cached_property
     def codes(self) -> torch.Tensor:
-        return self.buffer[..., :self.d].view(torch.float8_e4m3fn)
+        width = -(-self.d // Q8_GROUP) * Q8_GROUP
+        return self.buffer[:, :self.T * width].unflatten(1, (self.T, width))[..., :self.d].view(torch.float8_e4m3fn)
 
-    @property
+    @functools.cached_property
+    def tails(self) -> torch.Tensor:
+        """What goes with each row's codes (uint8 [n, T, bytes])."""
+        groups = -(-self.d // Q8_GROUP)
+        at, size = self.T * groups * Q8_GROUP, (-(-groups // 4) * 4 + 4 + 15) // 16 * 16
+        return self.buffer[:, at:at + self.T * size].unflatten(1, (self.T, size))
+
+    @functools.cached_property
     def exponents(self) -> torch.Tensor:
-        groups = -(-self.d // Q8_GROUP)
-        return self.buffer[..., Q8_GROUP * groups:(Q8_GROUP + 1) * groups]
+        return self.tails[..., :-(-self.d // Q8_GROUP)]
 
-    @property
+    @functools.cached_property
     def mean_square(self) -> torch.Tensor:
-        groups = -(-self.d // Q8_GROUP)
-        at = Q8_GROUP * groups + (groups + 3) // 4 * 4
-        return self.buffer[..., at:at + 4].view(torch.float32)[..., 0]
+        at = -(-(-(-self.d // Q8_GROUP)) // 4) * 4
+        return self.tails[..., at:at + 4].view(torch.float32)[..., 0]
 
 
 class Q8Weight:
@@ -653,12 +652,12 @@ class Q8Weight:
         self.buffer = torch.zeros(size, dtype=torch.uint8, device="cuda" if device is None else device)
         self.pointer, self.device = self.buffer.data_ptr(), self.buffer.get_device()
 
-    @property
+    @functools.cached_property
     def codes(self) -> torch.Tensor:
         width = -(-self.d // Q8_GROUP) * Q8_GROUP
         return self.buffer[:self.m * width].view(self.m, width)[:, :self.d].view(torch.float8_e4m3fn)
 
-    @property
+    @functools.cached_property
     def exponents(self) -> torch.Tensor:
         groups = -(-self.d // Q8_GROUP)
         return self.buffer[self.m * groups * Q8_GROUP:].view(-1, -(-groups // 16) * 16)[:, :groups]
@@ -687,7 +686,7 @@ def attnres_q8_write(x: torch.Tensor, rows: Q8Rows, src: int = 0, stream=None) -
     first T tokens."""
     n, T, stride = _q8_side("x", x, rows, src)
     _check("attnres_q8_write", (_lib or lib()).attnres_q8_write(
-        x.data_ptr(), stride, n, T, rows.d, _dtype(x), rows.pointer + src * rows.stride, rows.stride,
+        x.data_ptr(), stride, n, T, rows.d, _dtype(x), rows.pointer + src * rows.source, rows.T,
         _stream(stream, rows.device)))
     return rows
 
@@ -696,7 +695,7 @@ def attnres_q8_read(rows: Q8Rows, out: torch.Tensor, src: int = 0, stream=None) 
     """The values of the sources src, src + 1, .. of `rows` into out ([T, d], or [n, T, d]; fp32 or bf16)."""
     n, T, stride = _q8_side("out", out, rows, src)
     _check("attnres_q8_read", (_lib or lib()).attnres_q8_read(
-        rows.pointer + src * rows.stride, rows.stride, n, T, rows.d, out.data_ptr(), stride, _dtype(out),
+        rows.pointer + src * rows.source, rows.T, n, T, rows.d, out.data_ptr(), stride, _dtype(out),
         _stream(stream, rows.device)))
     return out
 
@@ -717,7 +716,7 @@ def attnres_full_fwd_q8(rows: Q8Rows, n_src: int, w: torch.Tensor | None, gamma:
     if rows.device != device:
         raise ValueError("rows must be on the current CUDA device")
     _check("attnres_full_fwd_q8", (_lib or lib()).attnres_full_fwd_q8(
-        rows.pointer, rows.stride, n_src, T, d, _opt("w", w, (d,), f32, device), _opt("Q", Q, shape, f32, device),
+        rows.pointer, rows.T, n_src, T, d, _opt("w", w, (d,), f32, device), _opt("Q", Q, shape, f32, device),
         _like("gamma", gamma, (d,), f32, device), eps, _opt("gamma_pre", gamma_pre, (d,), f32, device), eps_pre,
         _opt("out", out, shape, main.dtype, device), _opt("out_normed", out_normed, shape, main.dtype, device),
         _dtype(main), _stream(stream, device)))
@@ -744,7 +743,7 @@ def attnres_query_projection_q8(rows: Q8Rows, src: int, W8: Q8Weight, Q: torch.T
     if rows.device != device or W8.device != device:
         raise ValueError("rows and W8 must be on the current CUDA device")
     _check("attnres_query_projection_q8", (_lib or lib()).attnres_query_projection_q8(
-        rows.pointer + src * rows.stride, T, rows.d, W8.pointer, m, _like("Q", Q, (T, m), torch.float32, device),
+        rows.pointer + src * rows.source, rows.T, T, rows.d, W8.pointer, m, _like("Q", Q, (T, m), torch.float32, device),
         _stream(stream, device)))
     return Q
 

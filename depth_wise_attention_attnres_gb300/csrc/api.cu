@@ -316,22 +316,20 @@ int check_grads(const GradArgs& a, int64_t scratch_floats) {
   return ATTNRES_OK;
 }
 
-// n sources of T 8-bit rows, row_stride bytes apart, and the memory they span.
-int check_q8_span(const void* rows, int64_t row_stride, int32_t n, int64_t T, int32_t d, Range* span) {
-  const int64_t row = attnres_q8_row_bytes(d);
-  if (row < 0 || n < 1 || T < 0 || T > kMaxElements / row) return ATTNRES_ERR_INVALID_ARG;
+// n sources of `cap` 8-bit rows of which T are used, and the memory they span.
+int check_q8_span(const void* rows, int64_t cap, int32_t n, int64_t T, int32_t d, Range* span) {
+  const int64_t source = attnres_q8_source_bytes(cap, d);
+  if (source < 0 || n < 1 || T < 0 || T > cap || source > 2 * kMaxElements / n) return ATTNRES_ERR_INVALID_ARG;
   if (T == 0) return ATTNRES_OK;
   if (!rows || !aligned16(rows)) return ATTNRES_ERR_INVALID_ARG;
-  if (n > 1 && (row_stride < T * row || row_stride % 16 != 0 || row_stride > 2 * kMaxElements / n))
-    return ATTNRES_ERR_INVALID_ARG;
-  *span = range_of(rows, (n - 1) * (n > 1 ? row_stride : 0) + T * row);
+  *span = range_of(rows, n * source);
   return ATTNRES_OK;
 }
 
 // The same with the [T, d] slices that are written from or read back into.
 int check_q8_rows(const Q8Rows& a, int32_t dtype, Range* other, Range* span) {
   if (!valid_dtype(dtype)) return ATTNRES_ERR_INVALID_ARG;
-  const int st = check_q8_span(a.rows, a.row_stride, a.n, a.T, a.d, span);
+  const int st = check_q8_span(a.rows, a.cap, a.n, a.T, a.d, span);
   if (st != ATTNRES_OK || a.T == 0) return st;
   const int64_t E = a.T * a.d;
   if (!a.x || off_element(a.x, elem_size(dtype))) return ATTNRES_ERR_INVALID_ARG;
@@ -724,7 +722,11 @@ int attnres_full_fwd_dynq(const void* V, int64_t src_stride, int32_t n_src, int6
   return run_full(a, as_stream(stream));
 }
 
-int64_t attnres_q8_row_bytes(int32_t d) { return d < 1 || d > kQ8MaxWidth ? -1 : q8_row_bytes(d); }
+int64_t attnres_q8_source_bytes(int64_t cap, int32_t d) {
+  return d < 1 || d > kQ8MaxWidth || cap < 0 || cap > kMaxElements / (256 * static_cast<int64_t>(q8_groups(d)))
+             ? -1
+             : q8_source_bytes(cap, d);
+}
 
 int64_t attnres_q8_weight_bytes(int32_t m, int32_t d) {
   if (m < 1 || d < 1 || m > kQ8MaxWidth || d > kQ8MaxWidth) return -1;
@@ -733,8 +735,8 @@ int64_t attnres_q8_weight_bytes(int32_t m, int32_t d) {
 }
 
 int attnres_q8_write(const void* x, int64_t x_stride, int32_t n, int64_t T, int32_t d, int32_t dtype, void* rows,
-                     int64_t row_stride, void* stream) {
-  Q8Rows a{x, x_stride, rows, row_stride, n, T, d, dtype == ATTNRES_BF16};
+                     int64_t cap, void* stream) {
+  Q8Rows a{x, x_stride, rows, cap, n, T, d, dtype == ATTNRES_BF16};
   Range rx, rr;
   const int st = check_q8_rows(a, dtype, &rx, &rr);
   if (st != ATTNRES_OK || T == 0) return st;
@@ -742,9 +744,9 @@ int attnres_q8_write(const void* x, int64_t x_stride, int32_t n, int64_t T, int3
   return launched([&] { return launch_q8_write(a, as_stream(stream)); });
 }
 
-int attnres_q8_read(const void* rows, int64_t row_stride, int32_t n, int64_t T, int32_t d, void* out,
+int attnres_q8_read(const void* rows, int64_t cap, int32_t n, int64_t T, int32_t d, void* out,
                     int64_t out_stride, int32_t out_dtype, void* stream) {
-  Q8Rows a{out, out_stride, const_cast<void*>(rows), row_stride, n, T, d, out_dtype == ATTNRES_BF16};
+  Q8Rows a{out, out_stride, const_cast<void*>(rows), cap, n, T, d, out_dtype == ATTNRES_BF16};
   Range ro, rr;
   const int st = check_q8_rows(a, out_dtype, &ro, &rr);
   if (st != ATTNRES_OK || T == 0) return st;
@@ -752,12 +754,12 @@ int attnres_q8_read(const void* rows, int64_t row_stride, int32_t n, int64_t T, 
   return launched([&] { return launch_q8_back(a, as_stream(stream)); });
 }
 
-int attnres_full_fwd_q8(const void* rows, int64_t row_stride, int32_t n_src, int64_t T, int32_t d, const float* w,
+int attnres_full_fwd_q8(const void* rows, int64_t cap, int32_t n_src, int64_t T, int32_t d, const float* w,
                         const float* Q, const float* gamma, float eps, const float* gamma_pre, float eps_pre, void* out,
                         void* out_normed, int32_t out_dtype, void* stream) {
   if (!valid_dtype(out_dtype) || !valid_eps(eps) || (gamma_pre && !valid_eps(eps_pre))) return ATTNRES_ERR_INVALID_ARG;
   Range rr;
-  const int st = check_q8_span(rows, row_stride, n_src, T, d, &rr);
+  const int st = check_q8_span(rows, cap, n_src, T, d, &rr);
   if (st != ATTNRES_OK || T == 0) return st;
   const int64_t os = elem_size(out_dtype), E = T * d;
   if (!gamma || !w == !Q || !gamma_pre != !out_normed || (!out && !out_normed)) return ATTNRES_ERR_INVALID_ARG;
@@ -767,7 +769,7 @@ int attnres_full_fwd_q8(const void* rows, int64_t row_stride, int32_t n_src, int
   const Range in[] = {rr, range_if(w, d * 4ll), range_if(Q, E * 4), range_of(gamma, d * 4ll), range_if(gamma_pre, d * 4ll)};
   const Range outs[] = {range_if(out, E * os), range_if(out_normed, E * os)};
   if (any_overlap(outs, in)) return ATTNRES_ERR_INVALID_ARG;
-  Q8ReadArgs a{rows, row_stride, n_src, T, d, w, Q, gamma, eps, {gamma_pre, eps_pre, out_normed}, out,
+  Q8ReadArgs a{rows, cap, n_src, T, d, w, Q, gamma, eps, {gamma_pre, eps_pre, out_normed}, out,
                out_dtype == ATTNRES_BF16, withhold_for(kWithholdQ8Read)};
   return launched([&] { return launch_q8_read(a, as_stream(stream)); });
 }
@@ -780,17 +782,17 @@ int attnres_q8_weight(const void* W, int32_t m, int32_t d, int32_t dtype, void* 
   return launched([&] { return launch_q8_weight(W, m, d, dtype == ATTNRES_BF16, W8, as_stream(stream)); });
 }
 
-int attnres_query_projection_q8(const void* rows, int64_t T, int32_t d, const void* W8, int32_t m, float* Q,
+int attnres_query_projection_q8(const void* rows, int64_t cap, int64_t T, int32_t d, const void* W8, int32_t m, float* Q,
                                 void* stream) {
   Range rr;
   const int64_t bytes = attnres_q8_weight_bytes(m, d);
   if (bytes < 0) return ATTNRES_ERR_INVALID_ARG;
-  const int st = check_q8_span(rows, 0, 1, T, d, &rr);
+  const int st = check_q8_span(rows, cap, 1, T, d, &rr);
   if (st != ATTNRES_OK || T == 0) return st;
   if (T > kMaxElements / m || !W8 || !aligned16(W8) || !Q || off_element(Q, 4)) return ATTNRES_ERR_INVALID_ARG;
   const Range rq = range_of(Q, T * m * 4);
   if (overlap(rq, rr) || overlap(rq, range_of(W8, bytes))) return ATTNRES_ERR_INVALID_ARG;
-  return launched([&] { return launch_q8_proj(rows, T, d, W8, m, Q, as_stream(stream)); });
+  return launched([&] { return launch_q8_proj(rows, cap, T, d, W8, m, Q, as_stream(stream)); });
 }
 
 int attnres_rmsnorm(const void* x, int64_t T, int32_t d, int32_t dtype, const float* gamma, float eps, void* out,

@@ -293,14 +293,18 @@ int64_t grads_scratch(int n);
 // 8-bit rows (attnres.h): groups and record layout.
 constexpr int kQ8MaxWidth = 1 << 24;
 constexpr int q8_groups(int d) { return (d + ATTNRES_Q8_GROUP - 1) / ATTNRES_Q8_GROUP; }
-constexpr int q8_mean_offset(int G) { return ATTNRES_Q8_GROUP * G + (G + 3) / 4 * 4; }
-constexpr int64_t q8_row_bytes(int d) { return (q8_mean_offset(q8_groups(d)) + 4 + 15) / 16 * 16; }
+constexpr int q8_mean_offset(int G) { return (G + 3) / 4 * 4; }                    // in a tail
+constexpr int q8_tail_bytes(int G) { return (q8_mean_offset(G) + 4 + 15) / 16 * 16; }
+// Bytes of a source of `cap` rows: codes, then tails, up to a 128-byte boundary.
+constexpr int64_t q8_source_bytes(int64_t cap, int d) {
+  return cap * 128 * q8_groups(d) + (cap * q8_tail_bytes(q8_groups(d)) + 127) / 128 * 128;
+}
 constexpr int q8_block_row(int G) { return (G + 15) / 16 * 16; }  // bytes of a weight's row of block exponents
 struct Q8Rows {
   const void* x;        // the [T, d] side: x when writing, out when reading back
   int64_t x_stride;     // elements
   void* rows;
-  int64_t row_stride;   // bytes
+  int64_t cap;          // rows of each source
   int n;
   int64_t T;
   int d;
@@ -308,7 +312,7 @@ struct Q8Rows {
 };
 struct Q8ReadArgs {
   const void* rows;
-  int64_t row_stride;   // bytes
+  int64_t cap;          // rows of each source
   int n_src;
   int64_t T;
   int d;
@@ -325,7 +329,7 @@ cudaError_t launch_q8_write(const Q8Rows& a, cudaStream_t s);
 cudaError_t launch_q8_back(const Q8Rows& a, cudaStream_t s);
 cudaError_t launch_q8_weight(const void* W, int m, int d, int is_bf16, void* W8, cudaStream_t s);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
-cudaError_t launch_q8_proj(const void* rows, int64_t T, int d, const void* W8, int m, float* Q, cudaStream_t s);
+cudaError_t launch_q8_proj(const void* rows, int64_t cap, int64_t T, int d, const void* W8, int m, float* Q, cudaStream_t s);
 cudaError_t take_timeout_q8_read(unsigned int* flag);
 cudaError_t take_timeout_q8_proj(unsigned int* flag);
 

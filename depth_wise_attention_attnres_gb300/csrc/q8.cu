@@ -97,12 +97,13 @@ __device__ __forceinline__ uint4 encode16(const float (&x)[16], uint32_t e) {
 // L lanes a row (8: 4 rows a warp, each lane a chunk of every group; 32: a row
 // a warp, 4 groups at a time). kBatch chunks a lane are loaded at once.
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) q8_write_kernel(Q8Rows a, int G, int rec, int vec) {
+__global__ void __launch_bounds__(kThreads) q8_write_kernel(Q8Rows a, int G, int vec) {
   constexpr int kRows = 32 / L;
   constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
   const int lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
   const int chunks = 8 * G, steps = (chunks + L - 1) / L;
-  const int mean_at = q8_mean_offset(G);
+  const int mean_at = q8_mean_offset(G), tail_bytes = q8_tail_bytes(G);
+  const int64_t source = q8_source_bytes(a.cap, a.d);
   const int64_t total = static_cast<int64_t>(a.n) * a.T;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
   pdl_trigger();
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(kThreads) q8_write_kernel(Q8Rows a, int G, int
     const bool valid = r < total;
     const int64_t i = valid ? r / a.T : 0, t = valid ? r - i * a.T : 0;
     const T* x = static_cast<const T*>(a.x) + i * a.x_stride + t * a.d;
-    unsigned char* out = static_cast<unsigned char*>(a.rows) + i * a.row_stride + t * rec;
+    unsigned char* out = static_cast<unsigned char*>(a.rows) + i * source + t * (128 * G);
+    unsigned char* tail = static_cast<unsigned char*>(a.rows) + i * source + a.cap * (128 * G) + t * tail_bytes;
     const int d = valid ? a.d : 0;  // lanes behind the last row read nothing
     float ms = 0.f;
     for (int c0 = 0; c0 < steps; c0 += kBatch) {
@@ -136,16 +138,16 @@ __global__ void __launch_bounds__(kThreads) q8_write_kernel(Q8Rows a, int G, int
         ms += (q.x + q.y) * s * s;
         if (valid && chunk < chunks) {
           *reinterpret_cast<uint4*>(out + chunk * 16) = code;
-          if ((j & 7) == 0) out[128 * G + (chunk >> 3)] = static_cast<unsigned char>(e);
+          if ((j & 7) == 0) tail[chunk >> 3] = static_cast<unsigned char>(e);
         }
       }
     }
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
     if (valid && j == 0) {
-      for (int k = 129 * G; k < mean_at; ++k) out[k] = 0;
-      *reinterpret_cast<float*>(out + mean_at) = ms / static_cast<float>(a.d);
-      for (int k = mean_at + 4; k < rec; k += 4) *reinterpret_cast<uint32_t*>(out + k) = 0;
+      for (int k = G; k < mean_at; ++k) tail[k] = 0;
+      *reinterpret_cast<float*>(tail + mean_at) = ms / static_cast<float>(a.d);
+      for (int k = mean_at + 4; k < tail_bytes; k += 4) *reinterpret_cast<uint32_t*>(tail + k) = 0;
     }
   }
 }
@@ -179,10 +181,11 @@ __device__ __forceinline__ void store_row16(float* row, int k0, int d, bool vec,
 }
 
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) q8_back_kernel(Q8Rows a, int G, int rec, int vec) {
+__global__ void __launch_bounds__(kThreads) q8_back_kernel(Q8Rows a, int G, int vec) {
   constexpr int kRows = 32 / L, kBatch = 4;
   const int lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
   const int chunks = 8 * G, steps = (chunks + L - 1) / L;
+  const int64_t source = q8_source_bytes(a.cap, a.d);
   const int64_t total = static_cast<int64_t>(a.n) * a.T;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
   pdl_trigger();
@@ -191,7 +194,9 @@ __global__ void __launch_bounds__(kThreads) q8_back_kernel(Q8Rows a, int G, int 
        r += warps * kRows) {
     const int64_t i = r / a.T, t = r - i * a.T;
     T* out = static_cast<T*>(const_cast<void*>(a.x)) + i * a.x_stride + t * a.d;
-    const unsigned char* row = static_cast<const unsigned char*>(a.rows) + i * a.row_stride + t * rec;
+    const unsigned char* row = static_cast<const unsigned char*>(a.rows) + i * source + t * (128 * G);
+    const unsigned char* tail =
+        static_cast<const unsigned char*>(a.rows) + i * source + a.cap * (128 * G) + t * q8_tail_bytes(G);
     for (int c0 = 0; c0 < steps; c0 += kBatch) {
       uint4 code[kBatch];
       uint32_t e[kBatch];
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) q8_back_kernel(Q8Rows a, int G, int 
         const int chunk = (c0 + b) * L + j;
         const bool in = chunk < chunks;
         code[b] = in ? __ldcs(reinterpret_cast<const uint4*>(row) + chunk) : make_uint4(0, 0, 0, 0);
-        e[b] = in ? row[128 * G + (chunk >> 3)] : 1u;
+        e[b] = in ? tail[chunk >> 3] : 1u;
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
@@ -276,18 +281,18 @@ unsigned row_grid(int64_t rows, int per_warp) {
 
 template <typename T>
 cudaError_t write_as(const Q8Rows& a, cudaStream_t s) {
-  const int G = q8_groups(a.d), rec = static_cast<int>(q8_row_bytes(a.d)), vec = rows_vec(a);
+  const int G = q8_groups(a.d), vec = rows_vec(a);
   const int64_t rows = a.n * a.T;
-  if (G <= 8) return launch_pdl(q8_write_kernel<T, 8>, row_grid(rows, 4), kThreads, 0, s, a, G, rec, vec);
-  return launch_pdl(q8_write_kernel<T, 32>, row_grid(rows, 1), kThreads, 0, s, a, G, rec, vec);
+  if (G <= 8) return launch_pdl(q8_write_kernel<T, 8>, row_grid(rows, 4), kThreads, 0, s, a, G, vec);
+  return launch_pdl(q8_write_kernel<T, 32>, row_grid(rows, 1), kThreads, 0, s, a, G, vec);
 }
 
 template <typename T>
 cudaError_t back_as(const Q8Rows& a, cudaStream_t s) {
-  const int G = q8_groups(a.d), rec = static_cast<int>(q8_row_bytes(a.d)), vec = rows_vec(a);
+  const int G = q8_groups(a.d), vec = rows_vec(a);
   const int64_t rows = a.n * a.T;
-  if (G <= 8) return launch_pdl(q8_back_kernel<T, 8>, row_grid(rows, 4), kThreads, 0, s, a, G, rec, vec);
-  return launch_pdl(q8_back_kernel<T, 32>, row_grid(rows, 1), kThreads, 0, s, a, G, rec, vec);
+  if (G <= 8) return launch_pdl(q8_back_kernel<T, 8>, row_grid(rows, 4), kThreads, 0, s, a, G, vec);
+  return launch_pdl(q8_back_kernel<T, 32>, row_grid(rows, 1), kThreads, 0, s, a, G, vec);
 }
 
 }  // namespace

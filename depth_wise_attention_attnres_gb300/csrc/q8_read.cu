@@ -2,15 +2,14 @@
 // z = sum_i softmax_i(e) v_i) in one pass over the rows, with a running maximum and sum.
 //
 // Streaming kernel (rows of up to 2048 features). A row is held by L lanes, 16
-// features in each of C steps, so a warp works on 32 / L tokens at once; a
-// token's 8 lanes of a group share its scale. Each warp streams its own rows:
-// per source, the records of its tokens are consecutive, and one bulk copy
-// brings them into a ring of the warp's own in shared memory. No warp waits
-// for another, and lane 0 refills a stage as soon as its codes are in
-// registers. Per source a lane decodes its 16 C codes once and keeps the values,
-// multiplies them with u (in registers for as long as the token lasts), adds over the
-// L lanes, and adds the weighted values onto its accumulators. rms needs no
-// sum: the mean square comes with the row.
+// features in each of C steps, so a warp works on 32 / L tokens at once; the
+// 8 lanes of a group share its scale. A producer warp brings, source by source,
+// the rows of the CTA's tokens into a ring of shared-memory stages (one bulk copy of codes,
+// one of tails). Per source a lane decodes its 16 C codes once and keeps the
+// values, multiplies them with u, adds over the L lanes, and adds the
+// weighted values onto its accumulators. rms needs no sum: the mean square
+// comes with the row. u lies in shared memory, where rows of a warp share
+// what they read; with a query for each token it lies in registers.
 //
 // When there are fewer groups of tokens than warps, `split` warps of a CTA
 // share one: each takes every split-th source, and the maxima, sums and
@@ -66,157 +65,228 @@ __device__ __forceinline__ void put16(void* out, int out_bf16, int64_t row, int 
   }
 }
 
-template <int C, int L>
+template <int C, int L, bool kToken>
 struct Q8Read {
-  static constexpr int kRows = 32 / L;               // tokens a warp works on
-  static constexpr int kWarps = C <= 2 ? 16 : 8;     // warps of a CTA, one CTA an SM
+  static constexpr int kRows = 32 / L;  // tokens a warp works on
+  // Consumer warps; one CTA an SM, whose registers they share with the producer.
+  static constexpr int kWarps = kToken ? (C <= 2 ? 11 : 7) : (C <= 2 ? 15 : 11);
+  static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kTile = kWarps * kRows;
+  static constexpr int kBox = (16 * C + 2) * 32;  // floats of a warp's share in a join
 };
 
-template <int C, int L>
-__global__ void __launch_bounds__(Q8Read<C, L>::kWarps * 32, 1) q8_read_kernel(Q8ReadArgs a, int rec, int nstage, int split,
-                                                                              int vec) {
-  constexpr int kRows = Q8Read<C, L>::kRows, kWarps = Q8Read<C, L>::kWarps;
+template <int C, int L, bool kToken>
+__global__ void __launch_bounds__(Q8Read<C, L, kToken>::kThreads, 1)
+    q8_read_kernel(Q8ReadArgs a, int nstage, int split, int vec) {
+  using R = Q8Read<C, L, kToken>;
+  constexpr int kRows = R::kRows, kWarps = R::kWarps;
   extern __shared__ __align__(128) unsigned char smem[];
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty_bar = full_bar + kMaxStages;
+  float* us = reinterpret_cast<float*>(smem + 2 * kMaxStages * 8);  // u, [128 G] (not with a query for each token)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
-  const int G = (a.d + 127) / 128, d = a.d;
-  const int stage_bytes = kRows * rec;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem) + warp * kMaxStages;
-  unsigned char* ring = smem + kWarps * kMaxStages * 8 + static_cast<size_t>(warp) * nstage * stage_bytes;
-  const int teams = kWarps / split, team = warp / split, part = warp - team * split;
+  const int G = (a.d + 127) / 128, d = a.d, n = a.n_src, Dp = 128 * G;
+  const int tail_bytes = q8_tail_bytes(G), slot_bytes = kRows * (Dp + tail_bytes), stage_bytes = kWarps * slot_bytes;
+  unsigned char* ring = smem + 2 * kMaxStages * 8 + (kToken ? 0 : Dp * 4);
+  // Tiles of `teams` groups of kRows tokens; a team of `split` warps has a group.
+  const int teams = kWarps / split, steps = (n + split - 1) / split;
   const int64_t T = a.T, groups = (T + kRows - 1) / kRows;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * teams + team, step = static_cast<int64_t>(gridDim.x) * teams;
-  const int64_t mine = first < groups ? (groups - 1 - first) / step + 1 : 0;
-  const int ni = (a.n_src - part + split - 1) / split;  // sources part, part + split, ..: at least one (split <= n_src)
-  const int64_t total = mine * ni;
-  const bool last_in = (C - 1) * L + j < 8 * G;  // whether the lane's last step holds codes
+  // Contiguous groups [g0, g1) of this CTA, in tiles whose sizes differ by one at most.
+  const int64_t g0 = static_cast<int64_t>(blockIdx.x) * groups / gridDim.x;
+  const int64_t g1 = static_cast<int64_t>(blockIdx.x + 1) * groups / gridDim.x;
+  const int64_t ntiles = (g1 - g0 + teams - 1) / teams;
+  auto tile_first = [&](int64_t t) { return g0 + t * (g1 - g0) / ntiles; };
 
   pdl_trigger();
-  if (lane == 0) {
-    for (int s = 0; s < nstage; ++s) mbar_init(smem_u32(&bars[s]), 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < nstage; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), kWarps);
+    }
     mbar_fence_init();
   }
-  __syncwarp();
+  __syncthreads();
   pdl_wait();
 
-  // Lane 0's position among the warp's copies: token group pg, source pi.
-  int64_t issued = 0, pg = first;
-  int pi = part, pstage = 0;
-  const char* rows = static_cast<const char*>(a.rows);
-  auto issue = [&] {
-    const int64_t left = T - pg * kRows;
-    const uint32_t bytes = static_cast<uint32_t>(left < kRows ? static_cast<int>(left) : kRows) * static_cast<uint32_t>(rec);
-    if (issued != a.withhold) {  // the test hook leaves this stage unfilled
-      const uint32_t bar = smem_u32(&bars[pstage]);
-      mbar_arrive_expect_tx(bar, bytes);
-      bulk_g2s(smem_u32(ring + pstage * stage_bytes), rows + static_cast<int64_t>(pi) * a.row_stride + pg * kRows * rec, bytes,
-               bar);
-    }
-    ++issued;
-    if (++pstage == nstage) pstage = 0;
-    pi += split;
-    if (pi >= a.n_src) {
-      pi = part;
-      pg += step;
-    }
-  };
-  if (lane == 0)
-    for (int s = 0; s < nstage && issued < total; ++s) issue();
-
-  const float inv_d = 1.0f / static_cast<float>(d);
-  float2 u[8 * C];
-  auto load_u = [&](const float* q) {
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = (c * L + j) * 16 + 2 * i;
-        u[c * 8 + i] = make_float2(k < d ? q[k] * kQueryDown * a.gamma[k] : 0.f,
-                                   k + 1 < d ? q[k + 1] * kQueryDown * a.gamma[k + 1] : 0.f);
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    // A stage holds, for split == 1, the tile's rows of one source (codes,
+    // then tails, as one copy each); otherwise a slot for each warp, copied by a lane each.
+    const int64_t source = q8_source_bytes(a.cap, d);
+    const char* rows = static_cast<const char*>(a.rows);
+    const char* tails = rows + a.cap * Dp;
+    int s = 0;
+    uint32_t phase = 0;
+    int64_t it = 0;
+    bool ok = true;
+    for (int64_t t = 0; t < ntiles && ok; ++t) {
+      const int64_t r0 = tile_first(t) * kRows, r1 = tile_first(t + 1) * kRows < T ? tile_first(t + 1) * kRows : T;
+      const int64_t nr = r1 - r0;
+      for (int step = 0; step < steps; ++step) {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[s]), phase ^ 1u));
+        if (!ok) break;
+        const uint32_t fb = smem_u32(&full_bar[s]), dst = smem_u32(ring + s * stage_bytes);
+        if (it != a.withhold) {  // the test hook leaves this stage unfilled
+          if (split == 1) {
+            if (lane == 0) {
+              const uint32_t cb = static_cast<uint32_t>(nr) * static_cast<uint32_t>(Dp);
+              const uint32_t tb = static_cast<uint32_t>(nr) * static_cast<uint32_t>(tail_bytes);
+              mbar_arrive_expect_tx(fb, cb + tb);
+              bulk_g2s(dst, rows + step * source + r0 * Dp, cb, fb);
+              bulk_g2s(dst + R::kTile * Dp, tails + step * source + r0 * tail_bytes, tb, fb);
+            }
+          } else {
+            const int here = n - step * split < split ? n - step * split : split;  // sources of this step
+            if (lane == 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(nr * here) * static_cast<uint32_t>(Dp + tail_bytes));
+            __syncwarp();
+            const int team = lane / split, part = lane - team * split;
+            const int64_t left = nr - team * kRows;
+            if (team < teams && part < here && left > 0) {
+              const uint32_t k = left < kRows ? static_cast<uint32_t>(left) : static_cast<uint32_t>(kRows);
+              const int64_t src = static_cast<int64_t>(step * split + part) * source, row = r0 + team * kRows;
+              bulk_g2s(dst + lane * kRows * Dp, rows + src + row * Dp, k * static_cast<uint32_t>(Dp), fb);
+              bulk_g2s(dst + R::kTile * Dp + lane * kRows * tail_bytes, tails + src + row * tail_bytes,
+                       k * static_cast<uint32_t>(tail_bytes), fb);
+            }
+          }
+        }
+        ++it;
+        if (++s == nstage) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
-  };
-  if (a.w) load_u(a.w);
+    }
+    // Every copy has landed before this CTA's memory goes (a withheld one was
+    // never issued); without a timeout the consumers have seen to that.
+    if (lane == 0) {
+      for (int64_t k = it > nstage ? it - nstage : 0; k < it; ++k)
+        if (k != a.withhold) ok &= mbar_wait(smem_u32(&full_bar[k % nstage]), static_cast<uint32_t>((k / nstage) & 1));
+      if (!ok) atomicOr(&g_q8_read_timeout, 1u);
+    }
+    return;
+  }
 
-  int stage = 0;
+  // -------------------------------------------------------------- consumers
+  float2 ur[kToken ? 8 * C : 1];
+  if constexpr (!kToken) {
+    for (int k = threadIdx.x; k < Dp; k += kWarps * 32) us[k] = k < d ? a.w[k] * kQueryDown * a.gamma[k] : 0.f;
+    named_sync(1, kWarps * 32);
+  }
+  const int team = warp / split, part = warp - team * split;
+  const bool last_in = (C - 1) * L + j < 8 * G;  // whether the lane's last step holds codes
+  const int lane_at = j * 16, tail_at = R::kTile * Dp + (warp * kRows + sub) * tail_bytes, ms_at = q8_mean_offset(G);
+  const int codes_at = (warp * kRows + sub) * Dp;
+
+  int s = 0;
   uint32_t phase = 0;
   bool ok = true;
-  int64_t it = 0;
-  for (int64_t g = first; g < groups && ok; g += step) {
-    const int64_t row = g * kRows + sub;
-    const bool valid = row < T;
-    if (!a.w) load_u(a.Q + (valid ? row : T - 1) * d);
+  for (int64_t t = 0; t < ntiles; ++t) {
+    const int64_t group = tile_first(t) + team, row = group * kRows + sub;
+    const bool busy = team < teams && group < tile_first(t + 1), valid = busy && row < T;
+    if constexpr (kToken) {
+      const float* q = a.Q + (valid ? row : 0) * d;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = (c * L + j) * 16 + 2 * i;
+          ur[c * 8 + i] = make_float2(k < d ? q[k] * kQueryDown * a.gamma[k] : 0.f,
+                                      k + 1 < d ? q[k + 1] * kQueryDown * a.gamma[k + 1] : 0.f);
+        }
+    }
     float2 acc[8 * C];
 #pragma unroll
     for (int i = 0; i < 8 * C; ++i) acc[i] = make_float2(0.f, 0.f);
     // A finite start, so that a score of -inf has weight 0 whatever came before.
     float m = -3.402823466e38f, l = 0.f;
-    for (int i = 0; i < ni; ++i, ++it) {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[stage]), phase))) {
-        ok = false;
-        break;
-      }
-      const unsigned char* r = ring + stage * stage_bytes + sub * rec;
-      float2 v[8 * C];
-      float sc[C];
-      float2 dot = make_float2(0.f, 0.f);
-      const float ms = *reinterpret_cast<const float*>(r + q8_mean_offset(G));
+    for (int step = 0; step < steps; ++step) {
+      // After a wait that ran out the warp goes on without waiting (barriers
+      // stay matched, nothing is stored) and the failure is on record.
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[s]), phase));
+      if (busy && step * split + part < n) {
+        const unsigned char* stage = ring + s * stage_bytes;
+        const unsigned char* r = stage + codes_at + lane_at;
+        const unsigned char* tail = stage + tail_at;
+        float2 v[8 * C];
+        float sc[C];
+        float2 dot = make_float2(0.f, 0.f);
+        const float ms = *reinterpret_cast<const float*>(tail + ms_at);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const bool in = c + 1 < C || last_in;
-        const uint4 code = in ? *reinterpret_cast<const uint4*>(r + (c * L + j) * 16) : make_uint4(0, 0, 0, 0);
-        sc[c] = q8_scale(in ? r[128 * G + ((c * L + j) >> 3)] : 1u);
-        float2 w[8], p = make_float2(0.f, 0.f);
-        decode16(code, w);
+        for (int c = 0; c < C; ++c) {
+          const bool in = c + 1 < C || last_in;
+          const uint4 code = in ? *reinterpret_cast<const uint4*>(r + c * L * 16) : make_uint4(0, 0, 0, 0);
+          sc[c] = q8_scale(in ? tail[(c * L + j) >> 3] : 1u);
+          float2 w[8], p = make_float2(0.f, 0.f);
+          decode16(code, w);
+          const float4* uq = reinterpret_cast<const float4*>(us + (in ? c * L * 16 + lane_at : 0));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[c * 8 + k] = w[k];
-          p = ffma2(w[k], u[c * 8 + k], p);
+          for (int k = 0; k < 4; ++k) {
+            float2 u0, u1;
+            if constexpr (kToken) {
+              u0 = ur[c * 8 + 2 * k];
+              u1 = ur[c * 8 + 2 * k + 1];
+            } else {
+              const float4 u4 = uq[k];
+              u0 = make_float2(u4.x, u4.y);
+              u1 = make_float2(u4.z, u4.w);
+            }
+            v[c * 8 + 2 * k] = w[2 * k];
+            v[c * 8 + 2 * k + 1] = w[2 * k + 1];
+            p = ffma2(w[2 * k], u0, p);
+            p = ffma2(w[2 * k + 1], u1, p);
+          }
+          dot = ffma2(p, make_float2(sc[c], sc[c]), dot);
         }
-        dot = ffma2(p, make_float2(sc[c], sc[c]), dot);
+        __syncwarp();  // the stage's codes are in registers
+        if (lane == 0) mbar_arrive(smem_u32(&empty_bar[s]));
+        float x = dot.x + dot.y;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        x *= rsqrtf(ms + a.eps) * kScoreUp;
+        // The accumulators are rescaled only when a score passes the maximum they
+        // are scaled by by more than 8: weights up to e^8 lose nothing in fp32.
+        const bool up = x > m + 8.f;
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = up ? __expf(m - x) : 1.f;
+          l *= f;
+          const float2 f2 = make_float2(f, f);
+#pragma unroll
+          for (int k = 0; k < 8 * C; ++k) acc[k] = fmul2(acc[k], f2);
+          if (up) m = x;
+        }
+        const float p = __expf(x - m);
+        l += p;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const float ps = p * sc[c];
+          const float2 p2 = make_float2(ps, ps);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[c * 8 + k] = ffma2(p2, v[c * 8 + k], acc[c * 8 + k]);
+        }
+      } else if (lane == 0) {
+        mbar_arrive(smem_u32(&empty_bar[s]));
       }
-      __syncwarp();  // the stage's codes are in registers
-      if (lane == 0 && issued < total) issue();
-      if (++stage == nstage) {
-        stage = 0;
+      if (++s == nstage) {
+        s = 0;
         phase ^= 1u;
-      }
-      float s = dot.x + dot.y;
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      s *= rsqrtf(ms + a.eps) * kScoreUp;
-      // The accumulators are rescaled only when a score passes the maximum they
-      // are scaled by by more than 8: weights up to e^8 lose nothing in fp32.
-      const bool up = s > m + 8.f;
-      if (__any_sync(0xffffffffu, up)) {
-        const float c = up ? __expf(m - s) : 1.f;
-        l *= c;
-        const float2 c2 = make_float2(c, c);
-#pragma unroll
-        for (int k = 0; k < 8 * C; ++k) acc[k] = fmul2(acc[k], c2);
-        if (up) m = s;
-      }
-      const float p = __expf(s - m);
-      l += p;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float ps = p * sc[c];
-        const float2 p2 = make_float2(ps, ps);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[c * 8 + k] = ffma2(p2, v[c * 8 + k], acc[c * 8 + k]);
       }
     }
     if (split > 1) {
-      // Join the team's shares. Each warp's ring is idle: its copies have all
-      // been used (a team with split > 1 has one token group).
-      float* box = reinterpret_cast<float*>(ring);
+      // Join the teams' shares. All warps are through with the ring, whose
+      // copies have all been used (with split > 1 a CTA has one tile).
+      named_sync(1, kWarps * 32);
+      float* box = reinterpret_cast<float*>(ring) + warp * R::kBox;
+      if (part > 0 && team < teams) {
 #pragma unroll
-      for (int k = 0; k < 8 * C; ++k) *reinterpret_cast<float2*>(box + k * 64 + lane * 2) = acc[k];
-      box[64 * 8 * C + lane] = m;
-      box[64 * 8 * C + 32 + lane] = l;
-      named_sync(1 + team, split * 32);
-      if (part == 0) {
-        const size_t next = static_cast<size_t>(nstage) * stage_bytes / 4;
+        for (int k = 0; k < 8 * C; ++k) *reinterpret_cast<float2*>(box + k * 64 + lane * 2) = acc[k];
+        box[64 * 8 * C + lane] = m;
+        box[64 * 8 * C + 32 + lane] = l;
+      }
+      named_sync(1, kWarps * 32);
+      if (part == 0 && team < teams) {
         for (int q = 1; q < split; ++q) {
-          const float* other = box + q * next;
+          const float* other = box + q * R::kBox;
           const float mo = other[64 * 8 * C + lane], lo = other[64 * 8 * C + 32 + lane];
           const float top = fmaxf(m, mo);  // a NaN score is in l and the accumulators
           const float ca = __expf(m - top), cb = __expf(mo - top);
@@ -229,7 +299,7 @@ __global__ void __launch_bounds__(Q8Read<C, L>::kWarps * 32, 1) q8_read_kernel(Q
         }
       }
     }
-    if (part != 0 || !ok) continue;
+    if (part != 0 || !ok || !busy) continue;
     const float inv = 1.0f / l;
 #pragma unroll
     for (int k = 0; k < 8 * C; ++k) acc[k] = fmul2(acc[k], make_float2(inv, inv));
@@ -250,7 +320,7 @@ __global__ void __launch_bounds__(Q8Read<C, L>::kWarps * 32, 1) q8_read_kernel(Q
       float q = q2.x + q2.y;
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-      const float rr = rsqrtf(q * inv_d + a.pre.eps);
+      const float rr = rsqrtf(q / static_cast<float>(d) + a.pre.eps);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
 #pragma unroll
@@ -263,23 +333,15 @@ __global__ void __launch_bounds__(Q8Read<C, L>::kWarps * 32, 1) q8_read_kernel(Q
       }
     }
   }
-  if (!ok) {
-    if (lane == 0) {
-      atomicOr(&g_q8_read_timeout, 1u);
-      // Copies still in flight land before this CTA's memory goes (a withheld one was never issued).
-      for (int64_t k = issued > nstage ? issued - nstage : 0; k < issued; ++k)
-        if (k != a.withhold && k >= it)
-          (void)mbar_wait(smem_u32(&bars[k % nstage]), static_cast<uint32_t>((k / nstage) & 1));
-    }
-    __syncwarp();
-  }
+  if (!ok && lane == 0) atomicOr(&g_q8_read_timeout, 1u);
 }
 
 constexpr int kGenThreads = 256;
 
-__global__ void __launch_bounds__(kGenThreads) q8_read_general_kernel(Q8ReadArgs a, int rec) {
+__global__ void __launch_bounds__(kGenThreads) q8_read_general_kernel(Q8ReadArgs a) {
   extern __shared__ __align__(16) float sm[];
   const int G = (a.d + 127) / 128, Dp = 128 * G, n = a.n_src, d = a.d;
+  const int64_t source = q8_source_bytes(a.cap, d);
   float* z = sm;          // [Dp]
   float* p = sm + Dp;     // [n] scores, then weights
   __shared__ float part[kGenThreads / 32];
@@ -297,15 +359,16 @@ __global__ void __launch_bounds__(kGenThreads) q8_read_general_kernel(Q8ReadArgs
     return t;
   };
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const unsigned char* rows = static_cast<const unsigned char*>(a.rows) + t * rec;
+    const unsigned char* rows = static_cast<const unsigned char*>(a.rows) + t * Dp;
+    const unsigned char* tails = static_cast<const unsigned char*>(a.rows) + a.cap * Dp + t * q8_tail_bytes(G);
     const float* q = a.w ? a.w : a.Q + t * d;
     for (int i = warp; i < n; i += kGenThreads / 32) {
-      const unsigned char* r = rows + i * a.row_stride;
+      const unsigned char *r = rows + i * source, *tail = tails + i * source;
       float dot = 0.f;
       for (int w = lane; w < Dp / 4; w += 32) {
         float2 v0, v1;
         decode4(*reinterpret_cast<const uint32_t*>(r + 4 * w), v0, v1);
-        const float s = q8_scale(r[Dp + (w >> 5)]);
+        const float s = q8_scale(tail[w >> 5]);
         float x = 0.f;
         if (4 * w < d) x += v0.x * (q[4 * w] * kQueryDown * a.gamma[4 * w]);
         if (4 * w + 1 < d) x += v0.y * (q[4 * w + 1] * kQueryDown * a.gamma[4 * w + 1]);
@@ -314,7 +377,7 @@ __global__ void __launch_bounds__(kGenThreads) q8_read_general_kernel(Q8ReadArgs
         dot = fmaf(x, s, dot);
       }
       dot = warp_sum(dot);
-      if (lane == 0) p[i] = dot * (rsqrtf(*reinterpret_cast<const float*>(r + q8_mean_offset(G)) + a.eps) * kScoreUp);
+      if (lane == 0) p[i] = dot * (rsqrtf(*reinterpret_cast<const float*>(tail + q8_mean_offset(G)) + a.eps) * kScoreUp);
     }
     __syncthreads();
     float m = -3.402823466e38f;
@@ -327,10 +390,10 @@ __global__ void __launch_bounds__(kGenThreads) q8_read_general_kernel(Q8ReadArgs
     for (int w = threadIdx.x; w < Dp / 4; w += kGenThreads) {
       float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
       for (int i = 0; i < n; ++i) {
-        const unsigned char* r = rows + i * a.row_stride;
+        const unsigned char *r = rows + i * source, *tail = tails + i * source;
         float2 v0, v1;
         decode4(*reinterpret_cast<const uint32_t*>(r + 4 * w), v0, v1);
-        const float ps = p[i] * q8_scale(r[Dp + (w >> 5)]);
+        const float ps = p[i] * q8_scale(tail[w >> 5]);
         acc0 = ffma2(v0, make_float2(ps, ps), acc0);
         acc1 = ffma2(v1, make_float2(ps, ps), acc1);
       }
@@ -362,34 +425,40 @@ __global__ void __launch_bounds__(kGenThreads) q8_read_general_kernel(Q8ReadArgs
   }
 }
 
-template <int C, int L>
-cudaError_t launch_cl(const Q8ReadArgs& a, int rec, cudaStream_t s) {
-  using R = Q8Read<C, L>;
-  const int stage_bytes = R::kRows * rec, fixed = R::kWarps * kMaxStages * 8;
-  // The join's boxes take (16 C + 2) * 128 bytes of each ring.
-  int nstage = (kSmemMax - fixed) / (R::kWarps * stage_bytes);
+template <int C, int L, bool kToken>
+cudaError_t launch_clt(const Q8ReadArgs& a, cudaStream_t s) {
+  using R = Q8Read<C, L, kToken>;
+  const int G = q8_groups(a.d), stage_bytes = R::kTile * (128 * G + q8_tail_bytes(G));
+  const int fixed = 2 * kMaxStages * 8 + (kToken ? 0 : 512 * G);
+  int nstage = (kSmemMax - fixed) / stage_bytes;
   nstage = nstage > kMaxStages ? kMaxStages : nstage;
   const int64_t groups = (a.T + R::kRows - 1) / R::kRows;
   const int sms = sm_count();
+  // As many warps to a group of tokens as there are to spare, so that each CTA still has one tile.
   int split = 1;
-  while (split < R::kWarps && 2 * split <= a.n_src && groups * 2 * split <= static_cast<int64_t>(sms) * R::kWarps) split *= 2;
+  while (2 * split <= R::kWarps && 2 * split <= a.n_src && groups <= static_cast<int64_t>(sms) * (R::kWarps / (2 * split)))
+    split *= 2;
   int ring = nstage * stage_bytes;
-  const int box = (16 * C + 2) * 128;
-  if (split > 1 && ring < box) return cudaErrorInvalidValue;
-  const int smem = fixed + R::kWarps * ring;
-  const void* fn = reinterpret_cast<const void*>(&q8_read_kernel<C, L>);
-  cudaError_t e = allow_dynamic_smem(fn, smem);
+  const int boxes = R::kWarps * R::kBox * 4;
+  if (split > 1 && ring < boxes) ring = boxes;
+  const int smem = fixed + ring;
+  const void* fn = reinterpret_cast<const void*>(&q8_read_kernel<C, L, kToken>);
+  cudaError_t e = allow_dynamic_smem(fn, kSmemMax);
   if (e != cudaSuccess) return e;
   // Rows of both outputs that start on 16-byte boundaries and hold whole 16-byte vectors.
   const int vec = a.d % (a.out_bf16 ? 8 : 4) == 0 && aligned16(a.out) && aligned16(a.pre.out);
   const int teams = R::kWarps / split;
   int64_t grid = (groups + teams - 1) / teams;
   if (grid > sms) grid = sms;
-  return launch_pdl(q8_read_kernel<C, L>, static_cast<unsigned>(grid), R::kWarps * 32, smem, s, a, rec, nstage, split,
-                    vec);
+  return launch_pdl(q8_read_kernel<C, L, kToken>, static_cast<unsigned>(grid), R::kThreads, smem, s, a, nstage, split, vec);
 }
 
-cudaError_t launch_general(const Q8ReadArgs& a, int rec, cudaStream_t s) {
+template <int C, int L>
+cudaError_t launch_cl(const Q8ReadArgs& a, cudaStream_t s) {
+  return a.w ? launch_clt<C, L, false>(a, s) : launch_clt<C, L, true>(a, s);
+}
+
+cudaError_t launch_general(const Q8ReadArgs& a, cudaStream_t s) {
   const int64_t smem = (static_cast<int64_t>(a.n_src) + 128 * q8_groups(a.d)) * 4;
   if (smem > 200 * 1024) return cudaErrorInvalidValue;
   const void* fn = reinterpret_cast<const void*>(&q8_read_general_kernel);
@@ -397,23 +466,23 @@ cudaError_t launch_general(const Q8ReadArgs& a, int rec, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
   return launch_pdl(q8_read_general_kernel, static_cast<unsigned>(a.T < cap ? a.T : cap), kGenThreads, static_cast<int>(smem), s,
-                    a, rec);
+                    a);
 }
 
 }  // namespace
 
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
-  const int G = q8_groups(a.d), rec = static_cast<int>(q8_row_bytes(a.d));
+  const int G = q8_groups(a.d);
   switch (G) {
-    case 1: return launch_cl<1, 8>(a, rec, s);
-    case 2: return launch_cl<2, 8>(a, rec, s);
-    case 3: return launch_cl<3, 8>(a, rec, s);
-    case 4: return launch_cl<4, 8>(a, rec, s);
-    case 5: case 6: return launch_cl<3, 16>(a, rec, s);
-    case 7: case 8: return launch_cl<4, 16>(a, rec, s);
-    case 9: case 10: case 11: case 12: return launch_cl<3, 32>(a, rec, s);
-    case 13: case 14: case 15: case 16: return launch_cl<4, 32>(a, rec, s);
-    default: return launch_general(a, rec, s);
+    case 1: return launch_cl<1, 8>(a, s);
+    case 2: return launch_cl<2, 8>(a, s);
+    case 3: return launch_cl<3, 8>(a, s);
+    case 4: return launch_cl<4, 8>(a, s);
+    case 5: case 6: return launch_cl<3, 16>(a, s);
+    case 7: case 8: return launch_cl<4, 16>(a, s);
+    case 9: case 10: case 11: case 12: return launch_cl<3, 32>(a, s);
+    case 13: case 14: case 15: case 16: return launch_cl<4, 32>(a, s);
+    default: return launch_general(a, s);
   }
 }
 

@@ -178,18 +178,20 @@ int attnres_full_fwd_dynq(const void* V, int64_t src_stride, int32_t n_src, int6
  * With the row goes mean_k v_k^2 (fp32), the mean square its key RMSNorm needs
  * in every read.
  *
- * A row is one record of attnres_q8_row_bytes(d) bytes, on a 16-byte boundary:
- *   [0, 128 G)           codes, G = ceil(d / 128), zero from d on;
- *   [128 G, 129 G)       e_g + 127 of each group, one byte each;
- *   then, on the next 4-byte boundary, the mean square (fp32), and zeros up
- *   to a multiple of 16 bytes.
- * Rows of one source are consecutive. Pointers to rows must be 16-byte aligned,
- * and strides between sources multiples of 16 bytes: else INVALID_ARG.
+ * A source is `cap` rows in attnres_q8_source_bytes(cap, d) bytes, with G = ceil(d / 128):
+ *   cap rows of 128 G bytes: the codes, zero from feature d on;
+ *   cap tails of 16 ceil((4 ceil(G / 4) + 4) / 16) bytes: e_g + 127 of each
+ *   group, one byte each; on the next 4-byte boundary the mean square (fp32);
+ *   zeros;
+ *   what is left up to a multiple of 128 bytes is not looked at.
+ * Sources follow each other. Calls take `cap` and the number T <= cap of rows in use (a batch may be
+ * smaller than the history was made for). Pointers to sources must be 16-byte
+ * aligned (128-byte aligned ones stream fastest): else INVALID_ARG.
  */
 #define ATTNRES_Q8_GROUP 128
 
-/* Bytes of one row: 16 ceil((128 G + 4 ceil(G / 4) + 4) / 16); -1 for d < 1 or d > 2^24. */
-int64_t attnres_q8_row_bytes(int32_t d);
+/* Bytes of a source of cap rows; -1 for cap < 0, d < 1 or d > 2^24. */
+int64_t attnres_q8_source_bytes(int64_t cap, int32_t d);
 
 /*
  * attnres_q8_write - n sources of T rows each into 8-bit rows (a history, one
@@ -197,34 +199,32 @@ int64_t attnres_q8_row_bytes(int32_t d);
  *
  *   x           device, n slices [T, d] of dtype, x_stride elements apart
  *               (>= T*d; not looked at when n == 1).
- *   rows        device, n slices of T rows, row_stride bytes apart (>= T *
- *               attnres_q8_row_bytes(d); not looked at when n == 1). Every byte
- *               of the T rows is written, none behind them. Must not overlap x.
+ *   rows, cap   device, n sources of cap >= T rows. The codes and tails of the
+ *               first T rows are written whole, nothing else. Must not overlap x.
  * Any d; d a multiple of 8 (bf16) or 4 (fp32) in 16-byte aligned storage
  * streams fastest.
  */
 int attnres_q8_write(const void* x, int64_t x_stride, int32_t n, int64_t T, int32_t d,
-                     int32_t dtype, void* rows, int64_t row_stride, void* stream);
+                     int32_t dtype, void* rows, int64_t cap, void* stream);
 
 /*
  * attnres_q8_read - the values 8-bit rows stand for: out = c * 2^e. In bf16
  * they are exact (codes have four significant bits) down to bf16's smallest
  * number, so attnres_full_bwd over them is the backward of attnres_full_fwd_q8.
  *
- *   rows, row_stride, n, T, d   as attnres_q8_write.
+ *   rows, cap, n, T, d   as attnres_q8_write.
  *   out         device, n slices [T, d] of out_dtype, out_stride elements
  *               apart (>= T*d; not looked at when n == 1). Must not overlap rows.
  */
-int attnres_q8_read(const void* rows, int64_t row_stride, int32_t n, int64_t T, int32_t d,
-                    void* out, int64_t out_stride, int32_t out_dtype, void* stream);
+int attnres_q8_read(const void* rows, int64_t cap, int32_t n, int64_t T, int32_t d, void* out,
+                    int64_t out_stride, int32_t out_dtype, void* stream);
 
 /*
  * attnres_full_fwd_q8 - the Full read (attnres_full_fwd) over 8-bit rows: the
  * sources are the values the rows stand for, and rms(v_i) comes from the
  * rows' mean squares.
  *
- *   rows        device, n_src sources of T rows, row_stride bytes apart (>= T *
- *               attnres_q8_row_bytes(d); not looked at when n_src == 1).
+ *   rows, cap   device, n_src sources of cap >= T rows.
  *   w           device, fp32 [d], the shared query, or NULL with Q.
  *   Q           device, fp32 [T, d], a query for each token
  *               (attnres_full_fwd_dynq), or NULL with w. One of the two.
@@ -234,12 +234,11 @@ int attnres_q8_read(const void* rows, int64_t row_stride, int32_t n, int64_t T, 
  *               or both NULL.
  *   out         device, [T, d] of out_dtype; NULL (z not stored) only with
  *               out_normed.
- * Outputs overlap nothing. d up to 2048 takes the streaming kernel, which
- * shares a token's sources over several warps when tokens are few; wider rows take a general
- * one, for which ATTNRES_ERR_UNSUPPORTED means 4 (n_src + 128 G) bytes are over
- * 200 KB.
+ * Outputs overlap nothing. d up to 2048 takes streaming kernels; wider rows
+ * take a general one, for which ATTNRES_ERR_UNSUPPORTED means that
+ * 4 (n_src + 128 G) bytes are over 200 KB.
  */
-int attnres_full_fwd_q8(const void* rows, int64_t row_stride, int32_t n_src, int64_t T, int32_t d,
+int attnres_full_fwd_q8(const void* rows, int64_t cap, int32_t n_src, int64_t T, int32_t d,
                         const float* w, const float* Q, const float* gamma, float eps,
                         const float* gamma_pre, float eps_pre, void* out, void* out_normed,
                         int32_t out_dtype, void* stream);
@@ -265,14 +264,14 @@ int64_t attnres_q8_weight_bytes(int32_t m, int32_t d);
  * Q[t, j] = sum_k v[t, k] W[j, k], with products of codes summed in fp32 over
  * each block of 128 features and the blocks' sums scaled and added in fp32.
  *
- *   rows        device, T rows of d features.
+ *   rows, cap   device, one source of cap >= T rows of d features.
  *   W8          device, [m, d] as attnres_q8_weight laid it out, 16-byte aligned. m need not be
  *               d: the queries of several reads may be projected at once.
  *   Q           device, fp32 [T, m]; must not overlap rows or W8.
  * The mean squares of the rows are not looked at.
  */
-int attnres_query_projection_q8(const void* rows, int64_t T, int32_t d, const void* W8, int32_t m,
-                                float* Q, void* stream);
+int attnres_query_projection_q8(const void* rows, int64_t cap, int64_t T, int32_t d, const void* W8,
+                                int32_t m, float* Q, void* stream);
 
 /*
  * attnres_rmsnorm - RMSNorm of each row, out = gamma * x / sqrt(mean(x^2) + eps)
