@@ -1,11 +1,12 @@
 // 8-bit rows: writing them, reading them back, and laying out a weight matrix
 // (the format and its rounding are described in attnres.h).
 //
-// Writing takes one pass: L lanes hold 16 consecutive features of a row each,
-// so 8 lanes share a group of 128; its largest magnitude is three shuffles
-// away, the scale follows from its bits, and the codes, the exponents and the
-// row's mean square (of the values the codes stand for) leave together. Both
-// kernels are bound by the bytes they stream; several 16-byte loads a thread
+// Writing takes one pass: 8 lanes hold a group of 128 features, 16 each, so its
+// largest magnitude is three shuffles away; the scale follows from its bits,
+// and the codes, the exponents and the row's mean square (of the values the
+// codes stand for) leave together. Both directions are bound by the bytes they
+// stream: every load and store of a warp covers whole 128-byte lines (a lane's 16
+// features are two or four pieces, 8 lanes apart), and several loads a thread
 // are issued before the first is used.
 #include "q8.cuh"
 
@@ -20,20 +21,36 @@ template <typename T> struct Raw16 {
   uint4 v[kVecs];
 };
 
-// Features [k0, k0 + 16) of a row, zero from d on. `vec`: rows start on
+// A lane's 16 features of group g: piece i holds the 16 bytes from feature
+// 128 g + (8 i + j) kPer on (lane j of 8), zero from d on. `vec`: rows start on
 // 16-byte boundaries and d is a whole number of 16-byte vectors.
 template <typename T>
-__device__ __forceinline__ void load_raw(const T* row, int k0, int d, bool vec, Raw16<T>& r) {
+__device__ __forceinline__ void load_raw(const T* row, int g, int j, int d, bool vec, Raw16<T>& r) {
   constexpr int kPer = 16 / sizeof(T);
-  if (vec) {
 #pragma unroll
-    for (int i = 0; i < Raw16<T>::kVecs; ++i)
-      r.v[i] = k0 + i * kPer < d ? __ldcs(reinterpret_cast<const uint4*>(row + k0) + i) : make_uint4(0, 0, 0, 0);
-  } else {
-    T* e = reinterpret_cast<T*>(r.v);
+  for (int i = 0; i < Raw16<T>::kVecs; ++i) {
+    const int k = g * 128 + (i * 8 + j) * kPer;
+    if (vec) {
+      r.v[i] = k < d ? __ldcs(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0, 0, 0, 0);
+    } else {
+      T* e = reinterpret_cast<T*>(&r.v[i]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) e[i] = k0 + i < d ? row[k0 + i] : from_f32<T>(0.f);
+      for (int q = 0; q < kPer; ++q) e[q] = k + q < d ? row[k + q] : from_f32<T>(0.f);
+    }
   }
+}
+
+// The codes of such features, in the same places.
+__device__ __forceinline__ void store_codes(unsigned char* group, int j, const uint4& c, bf16) {
+  reinterpret_cast<uint2*>(group)[j] = make_uint2(c.x, c.y);
+  reinterpret_cast<uint2*>(group)[8 + j] = make_uint2(c.z, c.w);
+}
+__device__ __forceinline__ void store_codes(unsigned char* group, int j, const uint4& c, float) {
+  uint32_t* at = reinterpret_cast<uint32_t*>(group) + j;
+  at[0] = c.x;
+  at[8] = c.y;
+  at[16] = c.z;
+  at[24] = c.w;
 }
 
 __device__ __forceinline__ void widen(const Raw16<bf16>& r, float (&x)[16]) {
@@ -94,14 +111,14 @@ __device__ __forceinline__ uint4 encode16(const float (&x)[16], uint32_t e) {
                     encode4(y[8], y[9], y[10], y[11]), encode4(y[12], y[13], y[14], y[15]));
 }
 
-// L lanes a row (8: 4 rows a warp, each lane a chunk of every group; 32: a row
-// a warp, 4 groups at a time). kBatch chunks a lane are loaded at once.
+// L lanes a row (8: 4 rows a warp, one group of each at a time; 32: a row a
+// warp, 4 groups at a time). kBatch groups a lane are loaded at once.
 template <typename T, int L>
 __global__ void __launch_bounds__(kThreads) q8_write_kernel(Q8Rows a, int G, int vec) {
   constexpr int kRows = 32 / L;
   constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
   const int lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
-  const int chunks = 8 * G, steps = (chunks + L - 1) / L;
+  const int steps = (8 * G + L - 1) / L, gj = j >> 3, j8 = j & 7;
   const int mean_at = q8_mean_offset(G), tail_bytes = q8_tail_bytes(G);
   const int64_t source = q8_source_bytes(a.cap, a.d);
   const int64_t total = static_cast<int64_t>(a.n) * a.T;
@@ -121,11 +138,11 @@ __global__ void __launch_bounds__(kThreads) q8_write_kernel(Q8Rows a, int G, int
     for (int c0 = 0; c0 < steps; c0 += kBatch) {
       Raw16<T> raw[kBatch];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) load_raw(x, ((c0 + b) * L + j) * 16, d, vec, raw[b]);
+      for (int b = 0; b < kBatch; ++b) load_raw(x, (c0 + b) * (L / 8) + gj, j8, d, vec, raw[b]);
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         if (c0 + b >= steps) break;  // the same for every lane
-        const int chunk = (c0 + b) * L + j;
+        const int g = (c0 + b) * (L / 8) + gj;
         float v[16];
         widen(raw[b], v);
         const uint32_t e = group_exponent(v);
@@ -136,9 +153,9 @@ __global__ void __launch_bounds__(kThreads) q8_write_kernel(Q8Rows a, int G, int
         for (int k = 0; k < 8; ++k) q = ffma2(w[k], w[k], q);
         const float s = q8_scale(e);
         ms += (q.x + q.y) * s * s;
-        if (valid && chunk < chunks) {
-          *reinterpret_cast<uint4*>(out + chunk * 16) = code;
-          if ((j & 7) == 0) tail[chunk >> 3] = static_cast<unsigned char>(e);
+        if (valid && g < G) {
+          store_codes(out + g * 128, j8, code, T());
+          if (j8 == 0) tail[g] = static_cast<unsigned char>(e);
         }
       }
     }
@@ -152,71 +169,96 @@ __global__ void __launch_bounds__(kThreads) q8_write_kernel(Q8Rows a, int G, int
   }
 }
 
-// 16 values into features [k0, k0 + 16) of a row; none from d on.
-__device__ __forceinline__ void store_row16(bf16* row, int k0, int d, bool vec, const float2 (&v)[8]) {
-  if (vec) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (k0 + 8 * h < d)
-        __stcs(reinterpret_cast<uint4*>(row + k0) + h,
-               make_uint4(pack_bf16x2(v[4 * h].x, v[4 * h].y), pack_bf16x2(v[4 * h + 1].x, v[4 * h + 1].y),
-                          pack_bf16x2(v[4 * h + 2].x, v[4 * h + 2].y), pack_bf16x2(v[4 * h + 3].x, v[4 * h + 3].y)));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k0 + i < d) row[k0 + i] = __float2bfloat16_rn(i & 1 ? v[i >> 1].y : v[i >> 1].x);
-  }
-}
-__device__ __forceinline__ void store_row16(float* row, int k0, int d, bool vec, const float2 (&v)[8]) {
-  if (vec) {
-#pragma unroll
-    for (int h = 0; h < 4; ++h)
-      if (k0 + 4 * h < d)
-        __stcs(reinterpret_cast<float4*>(row + k0) + h, make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k0 + i < d) row[k0 + i] = i & 1 ? v[i >> 1].y : v[i >> 1].x;
-  }
-}
-
+// Reading back: a lane's piece is the codes of 16 bytes of output (8 of bf16, 4
+// of fp32), so L lanes (16 or 32, all of a warp where the row is long enough)
+// read and write whole lines. kBatch pieces a lane are loaded at once.
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) q8_back_kernel(Q8Rows a, int G, int vec) {
-  constexpr int kRows = 32 / L, kBatch = 4;
-  const int lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
-  const int chunks = 8 * G, steps = (chunks + L - 1) / L;
+__global__ void __launch_bounds__(kThreads) q8_back_kernel(Q8Rows a, int G) {
+  constexpr int kPer = 16 / sizeof(T), kRows = 32 / L, kBatch = 8;
+  const int lane = threadIdx.x & 31, j = lane % L;
   const int64_t source = q8_source_bytes(a.cap, a.d);
   const int64_t total = static_cast<int64_t>(a.n) * a.T;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  const int pieces = (a.d + kPer - 1) / kPer;
   pdl_trigger();
   pdl_wait();
-  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kRows + sub; r < total;
+  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kRows + lane / L; r < total;
        r += warps * kRows) {
     const int64_t i = r / a.T, t = r - i * a.T;
     T* out = static_cast<T*>(const_cast<void*>(a.x)) + i * a.x_stride + t * a.d;
     const unsigned char* row = static_cast<const unsigned char*>(a.rows) + i * source + t * (128 * G);
     const unsigned char* tail =
         static_cast<const unsigned char*>(a.rows) + i * source + a.cap * (128 * G) + t * q8_tail_bytes(G);
-    for (int c0 = 0; c0 < steps; c0 += kBatch) {
-      uint4 code[kBatch];
+    for (int p0 = j; p0 < pieces; p0 += kBatch * L) {
+      uint2 code[kBatch];
       uint32_t e[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int chunk = (c0 + b) * L + j;
-        const bool in = chunk < chunks;
-        code[b] = in ? __ldcs(reinterpret_cast<const uint4*>(row) + chunk) : make_uint4(0, 0, 0, 0);
-        e[b] = in ? tail[chunk >> 3] : 1u;
+        const int k = (p0 + b * L) * kPer;
+        code[b] = make_uint2(0, 0);
+        e[b] = 1;
+        if (k < a.d) {
+          if (kPer == 8)
+            code[b] = __ldcs(reinterpret_cast<const uint2*>(row + k));
+          else
+            code[b].x = __ldcs(reinterpret_cast<const uint32_t*>(row + k));
+          e[b] = tail[k >> 7];
+        }
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int chunk = (c0 + b) * L + j;
-        if (chunk >= chunks) break;
-        float2 v[8];
-        decode16(code[b], v);
+        const int k = (p0 + b * L) * kPer;
+        if (k >= a.d) break;
         const float s = q8_scale(e[b]);
+        const float2 s2 = make_float2(s, s);
+        float2 v[4];
+        decode4(code[b].x, v[0], v[1]);
+        v[0] = fmul2(v[0], s2);
+        v[1] = fmul2(v[1], s2);
+        if constexpr (kPer == 8) {
+          decode4(code[b].y, v[2], v[3]);
+          v[2] = fmul2(v[2], s2);
+          v[3] = fmul2(v[3], s2);
+          __stcs(reinterpret_cast<uint4*>(out + k), make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                               pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y)));
+        } else {
+          __stcs(reinterpret_cast<float4*>(out + k), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+        }
+      }
+    }
+  }
+}
+
+// The same into rows that do not start on 16-byte boundaries: an element a lane,
+// so that a warp still writes consecutive elements (16384 rows of 1001 to bf16, four
+// sources: TIME us; with 16 elements a lane 348).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) q8_back_element_kernel(Q8Rows a, int G) {
+  constexpr int kBatch = 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t source = q8_source_bytes(a.cap, a.d);
+  const int64_t total = static_cast<int64_t>(a.n) * a.T;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); r < total; r += warps) {
+    const int64_t i = r / a.T, t = r - i * a.T;
+    T* out = static_cast<T*>(const_cast<void*>(a.x)) + i * a.x_stride + t * a.d;
+    const unsigned char* row = static_cast<const unsigned char*>(a.rows) + i * source + t * (128 * G);
+    const unsigned char* tail =
+        static_cast<const unsigned char*>(a.rows) + i * source + a.cap * (128 * G) + t * q8_tail_bytes(G);
+    for (int k0 = lane; k0 < a.d; k0 += kBatch * 32) {
+      uint32_t code[kBatch], e[kBatch];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = fmul2(v[k], make_float2(s, s));
-        store_row16(out, chunk * 16, a.d, vec, v);
+      for (int b = 0; b < kBatch; ++b) {
+        const int k = k0 + b * 32;
+        code[b] = k < a.d ? row[k] : 0u;
+        e[b] = k < a.d ? tail[k >> 7] : 1u;
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int k = k0 + b * 32;
+        if (k < a.d) out[k] = from_f32<T>(f16x2_f32(e4m3x2_f16x2(static_cast<uint16_t>(code[b]))).x * q8_scale(e[b]));
       }
     }
   }
@@ -289,10 +331,11 @@ cudaError_t write_as(const Q8Rows& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t back_as(const Q8Rows& a, cudaStream_t s) {
-  const int G = q8_groups(a.d), vec = rows_vec(a);
+  const int G = q8_groups(a.d);
   const int64_t rows = a.n * a.T;
-  if (G <= 8) return launch_pdl(q8_back_kernel<T, 8>, row_grid(rows, 4), kThreads, 0, s, a, G, vec);
-  return launch_pdl(q8_back_kernel<T, 32>, row_grid(rows, 1), kThreads, 0, s, a, G, vec);
+  if (!rows_vec(a)) return launch_pdl(q8_back_element_kernel<T>, row_grid(rows, 1), kThreads, 0, s, a, G);
+  if (a.d * static_cast<int>(sizeof(T)) <= 256) return launch_pdl(q8_back_kernel<T, 16>, row_grid(rows, 2), kThreads, 0, s, a, G);
+  return launch_pdl(q8_back_kernel<T, 32>, row_grid(rows, 1), kThreads, 0, s, a, G);
 }
 
 }  // namespace

@@ -6,10 +6,9 @@
 // 8 lanes of a group share its scale. A producer warp brings, source by source,
 // the rows of the CTA's tokens into a ring of shared-memory stages (one bulk copy of codes,
 // one of tails). Per source a lane decodes its 16 C codes once and keeps the
-// values, multiplies them with u, adds over the L lanes, and adds the
-// weighted values onto its accumulators. rms needs no sum: the mean square
-// comes with the row. u lies in shared memory, where rows of a warp share
-// what they read; with a query for each token it lies in registers.
+// values, multiplies them with u (in registers; from shared memory it took
+// half as long again), adds over the L lanes, and adds the weighted values onto
+// its accumulators. rms needs no sum: the mean square comes with the row.
 //
 // When there are fewer groups of tokens than warps, `split` warps of a CTA
 // share one: each takes every split-th source, and the maxima, sums and
@@ -20,6 +19,7 @@
 #include <math.h>
 
 #include "q8.cuh"
+#include "tcgen05.cuh"
 
 namespace attnres {
 namespace {
@@ -27,7 +27,7 @@ namespace {
 __device__ unsigned int g_q8_read_timeout = 0;
 
 constexpr int kMaxStages = 8;
-constexpr int kSmemMax = 200 * 1024;
+constexpr int kSmemMax = 226 * 1024;
 // A query is multiplied with codes of up to 448 before their scale, so it is taken
 // 2^-16 times as large and the score 2^16: no finite product of a value and a
 // query overflows.
@@ -65,35 +65,47 @@ __device__ __forceinline__ void put16(void* out, int out_bf16, int64_t row, int 
   }
 }
 
-template <int C, int L, bool kToken>
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int K, int S, int C, int L, int NW>
 struct Q8Read {
   static constexpr int kRows = 32 / L;  // tokens a warp works on
-  // Consumer warps; one CTA an SM, whose registers they share with the producer.
-  static constexpr int kWarps = kToken ? (C <= 2 ? 11 : 7) : (C <= 2 ? 15 : 11);
+  static constexpr int kWarps = NW;     // consumer warps; one CTA an SM, whose registers they share with the producer
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kTile = kWarps * kRows;
   static constexpr int kBox = (16 * C + 2) * 32;  // floats of a warp's share in a join
 };
 
-template <int C, int L, bool kToken>
-__global__ void __launch_bounds__(Q8Read<C, L, kToken>::kThreads, 1)
-    q8_read_kernel(Q8ReadArgs a, int nstage, int split, int vec) {
-  using R = Q8Read<C, L, kToken>;
+template <int K, int S, int C, int L, int NW, bool kCluster>
+__global__ void __launch_bounds__(Q8Read<K, S, C, L, NW>::kThreads, 1)
+    q8_read_kernel(Q8ReadArgs a, int nstage, int split, int cluster, int vec) {
+  using R = Q8Read<K, S, C, L, NW>;
   constexpr int kRows = R::kRows, kWarps = R::kWarps;
+  const int cl = kCluster ? cluster : 1;
   extern __shared__ __align__(128) unsigned char smem[];
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty_bar = full_bar + kMaxStages;
-  float* us = reinterpret_cast<float*>(smem + 2 * kMaxStages * 8);  // u, [128 G] (not with a query for each token)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
   const int G = (a.d + 127) / 128, d = a.d, n = a.n_src, Dp = 128 * G;
-  const int tail_bytes = q8_tail_bytes(G), slot_bytes = kRows * (Dp + tail_bytes), stage_bytes = kWarps * slot_bytes;
-  unsigned char* ring = smem + 2 * kMaxStages * 8 + (kToken ? 0 : Dp * 4);
+  const int tail_bytes = q8_tail_bytes(G), stage_bytes = K * R::kTile * (Dp + tail_bytes);
+  unsigned char* ring = smem + 2 * kMaxStages * 8;
   // Tiles of `teams` groups of kRows tokens; a team of `split` warps has a group.
-  const int teams = kWarps / split, steps = (n + split - 1) / split;
+  const int teams = kWarps / split, steps = (n + K * split * cl - 1) / (K * split * cl);
   const int64_t T = a.T, groups = (T + kRows - 1) / kRows;
-  // Contiguous groups [g0, g1) of this CTA, in tiles whose sizes differ by one at most.
-  const int64_t g0 = static_cast<int64_t>(blockIdx.x) * groups / gridDim.x;
-  const int64_t g1 = static_cast<int64_t>(blockIdx.x + 1) * groups / gridDim.x;
+  // Contiguous groups [g0, g1) of this CTA (of this cluster of cl CTAs, which
+  // share their sources), in tiles whose sizes differ by one at most.
+  const int rank = cl > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int64_t unit = blockIdx.x / cl, units = gridDim.x / cl;
+  const int64_t g0 = unit * groups / units, g1 = (unit + 1) * groups / units;
   const int64_t ntiles = (g1 - g0 + teams - 1) / teams;
   auto tile_first = [&](int64_t t) { return g0 + t * (g1 - g0) / ntiles; };
 
@@ -110,8 +122,9 @@ __global__ void __launch_bounds__(Q8Read<C, L, kToken>::kThreads, 1)
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
-    // A stage holds, for split == 1, the tile's rows of one source (codes,
-    // then tails, as one copy each); otherwise a slot for each warp, copied by a lane each.
+    // A stage holds the codes of K sources, then their tails: for split == 1 the
+    // tile's rows of each (a lane copies a source); otherwise K sources for each
+    // warp, its team's rows (a lane copies for a warp).
     const int64_t source = q8_source_bytes(a.cap, d);
     const char* rows = static_cast<const char*>(a.rows);
     const char* tails = rows + a.cap * Dp;
@@ -127,26 +140,30 @@ __global__ void __launch_bounds__(Q8Read<C, L, kToken>::kThreads, 1)
         if (!ok) break;
         const uint32_t fb = smem_u32(&full_bar[s]), dst = smem_u32(ring + s * stage_bytes);
         if (it != a.withhold) {  // the test hook leaves this stage unfilled
+          const int i0 = (step * cl + rank) * K * split;  // sources of this step, if any
+          const int here = n - i0 < K * split ? (n > i0 ? n - i0 : 0) : K * split;
+          if (lane == 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(nr * here) * static_cast<uint32_t>(Dp + tail_bytes));
+          __syncwarp();
+          const uint32_t tdst = dst + K * R::kTile * Dp;
           if (split == 1) {
-            if (lane == 0) {
-              const uint32_t cb = static_cast<uint32_t>(nr) * static_cast<uint32_t>(Dp);
-              const uint32_t tb = static_cast<uint32_t>(nr) * static_cast<uint32_t>(tail_bytes);
-              mbar_arrive_expect_tx(fb, cb + tb);
-              bulk_g2s(dst, rows + step * source + r0 * Dp, cb, fb);
-              bulk_g2s(dst + R::kTile * Dp, tails + step * source + r0 * tail_bytes, tb, fb);
+            if (lane < here) {
+              const int64_t src = static_cast<int64_t>(i0 + lane) * source;
+              bulk_g2s(dst + lane * R::kTile * Dp, rows + src + r0 * Dp, static_cast<uint32_t>(nr) * static_cast<uint32_t>(Dp), fb);
+              bulk_g2s(tdst + lane * R::kTile * tail_bytes, tails + src + r0 * tail_bytes,
+                       static_cast<uint32_t>(nr) * static_cast<uint32_t>(tail_bytes), fb);
             }
           } else {
-            const int here = n - step * split < split ? n - step * split : split;  // sources of this step
-            if (lane == 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(nr * here) * static_cast<uint32_t>(Dp + tail_bytes));
-            __syncwarp();
             const int team = lane / split, part = lane - team * split;
             const int64_t left = nr - team * kRows;
-            if (team < teams && part < here && left > 0) {
-              const uint32_t k = left < kRows ? static_cast<uint32_t>(left) : static_cast<uint32_t>(kRows);
-              const int64_t src = static_cast<int64_t>(step * split + part) * source, row = r0 + team * kRows;
-              bulk_g2s(dst + lane * kRows * Dp, rows + src + row * Dp, k * static_cast<uint32_t>(Dp), fb);
-              bulk_g2s(dst + R::kTile * Dp + lane * kRows * tail_bytes, tails + src + row * tail_bytes,
-                       k * static_cast<uint32_t>(tail_bytes), fb);
+            if (team < teams && left > 0) {
+              const uint32_t few = left < kRows ? static_cast<uint32_t>(left) : static_cast<uint32_t>(kRows);
+              for (int q = 0; q < K; ++q) {
+                if (part * K + q >= here) break;
+                const int64_t src = static_cast<int64_t>(i0 + part * K + q) * source, row = r0 + team * kRows;
+                bulk_g2s(dst + (q * R::kTile + lane * kRows) * Dp, rows + src + row * Dp, few * static_cast<uint32_t>(Dp), fb);
+                bulk_g2s(tdst + (q * R::kTile + lane * kRows) * tail_bytes, tails + src + row * tail_bytes,
+                         few * static_cast<uint32_t>(tail_bytes), fb);
+              }
             }
           }
         }
@@ -168,15 +185,23 @@ __global__ void __launch_bounds__(Q8Read<C, L, kToken>::kThreads, 1)
   }
 
   // -------------------------------------------------------------- consumers
-  float2 ur[kToken ? 8 * C : 1];
-  if constexpr (!kToken) {
-    for (int k = threadIdx.x; k < Dp; k += kWarps * 32) us[k] = k < d ? a.w[k] * kQueryDown * a.gamma[k] : 0.f;
-    named_sync(1, kWarps * 32);
-  }
   const int team = warp / split, part = warp - team * split;
   const bool last_in = (C - 1) * L + j < 8 * G;  // whether the lane's last step holds codes
-  const int lane_at = j * 16, tail_at = R::kTile * Dp + (warp * kRows + sub) * tail_bytes, ms_at = q8_mean_offset(G);
+  const int lane_at = j * 16, tail_at = K * R::kTile * Dp + (warp * kRows + sub) * tail_bytes, ms_at = q8_mean_offset(G);
   const int codes_at = (warp * kRows + sub) * Dp;
+
+  float2 u[8 * C];
+  auto load_query = [&](const float* q) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = (c * L + j) * 16 + 2 * i;
+        u[c * 8 + i] = make_float2(k < d ? q[k] * kQueryDown * a.gamma[k] : 0.f,
+                                   k + 1 < d ? q[k + 1] * kQueryDown * a.gamma[k + 1] : 0.f);
+      }
+  };
+  if (a.w) load_query(a.w);
 
   int s = 0;
   uint32_t phase = 0;
@@ -184,17 +209,7 @@ __global__ void __launch_bounds__(Q8Read<C, L, kToken>::kThreads, 1)
   for (int64_t t = 0; t < ntiles; ++t) {
     const int64_t group = tile_first(t) + team, row = group * kRows + sub;
     const bool busy = team < teams && group < tile_first(t + 1), valid = busy && row < T;
-    if constexpr (kToken) {
-      const float* q = a.Q + (valid ? row : 0) * d;
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = (c * L + j) * 16 + 2 * i;
-          ur[c * 8 + i] = make_float2(k < d ? q[k] * kQueryDown * a.gamma[k] : 0.f,
-                                      k + 1 < d ? q[k + 1] * kQueryDown * a.gamma[k + 1] : 0.f);
-        }
-    }
+    if (!a.w) load_query(a.Q + (valid ? row : 0) * d);
     float2 acc[8 * C];
 #pragma unroll
     for (int i = 0; i < 8 * C; ++i) acc[i] = make_float2(0.f, 0.f);
@@ -204,69 +219,72 @@ __global__ void __launch_bounds__(Q8Read<C, L, kToken>::kThreads, 1)
       // After a wait that ran out the warp goes on without waiting (barriers
       // stay matched, nothing is stored) and the failure is on record.
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[s]), phase));
-      if (busy && step * split + part < n) {
-        const unsigned char* stage = ring + s * stage_bytes;
-        const unsigned char* r = stage + codes_at + lane_at;
-        const unsigned char* tail = stage + tail_at;
-        float2 v[8 * C];
-        float sc[C];
-        float2 dot = make_float2(0.f, 0.f);
-        const float ms = *reinterpret_cast<const float*>(tail + ms_at);
+      const int first = ((step * cl + rank) * split + part) * K;
+      const unsigned char* r = ring + s * stage_bytes + codes_at + lane_at;
+      const unsigned char* tail = ring + s * stage_bytes + tail_at;
+      const int todo = !busy ? 0 : (n - first < K ? n - first : K);
+#pragma unroll 1
+      for (int q0 = 0; q0 < todo; q0 += S, r += S * R::kTile * Dp, tail += S * R::kTile * tail_bytes) {
+        float2 v[S][8 * C];
+        float sc[S][C], x[S], ms[S];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const bool in = c + 1 < C || last_in;
-          const uint4 code = in ? *reinterpret_cast<const uint4*>(r + c * L * 16) : make_uint4(0, 0, 0, 0);
-          sc[c] = q8_scale(in ? tail[(c * L + j) >> 3] : 1u);
-          float2 w[8], p = make_float2(0.f, 0.f);
-          decode16(code, w);
-          const float4* uq = reinterpret_cast<const float4*>(us + (in ? c * L * 16 + lane_at : 0));
+        for (int q = 0; q < S; ++q) {
+          const bool there = q == 0 || q0 + q < todo;  // the same for the whole warp
+          float2 dot = make_float2(0.f, 0.f);
+          ms[q] = there ? *reinterpret_cast<const float*>(tail + q * R::kTile * tail_bytes + ms_at) : 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float2 u0, u1;
-            if constexpr (kToken) {
-              u0 = ur[c * 8 + 2 * k];
-              u1 = ur[c * 8 + 2 * k + 1];
-            } else {
-              const float4 u4 = uq[k];
-              u0 = make_float2(u4.x, u4.y);
-              u1 = make_float2(u4.z, u4.w);
+          for (int c = 0; c < C; ++c) {
+            const bool in = there && (c + 1 < C || last_in);
+            const uint4 code =
+                in ? *reinterpret_cast<const uint4*>(r + q * R::kTile * Dp + c * L * 16) : make_uint4(0, 0, 0, 0);
+            sc[q][c] = q8_scale(in ? tail[q * R::kTile * tail_bytes + ((c * L + j) >> 3)] : 1u);
+            float2 w[8], p = make_float2(0.f, 0.f);
+            decode16(code, w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              v[q][c * 8 + k] = w[k];
+              p = ffma2(w[k], u[c * 8 + k], p);
             }
-            v[c * 8 + 2 * k] = w[2 * k];
-            v[c * 8 + 2 * k + 1] = w[2 * k + 1];
-            p = ffma2(w[2 * k], u0, p);
-            p = ffma2(w[2 * k + 1], u1, p);
+            dot = ffma2(p, make_float2(sc[q][c], sc[q][c]), dot);
           }
-          dot = ffma2(p, make_float2(sc[c], sc[c]), dot);
+          x[q] = dot.x + dot.y;
         }
-        __syncwarp();  // the stage's codes are in registers
-        if (lane == 0) mbar_arrive(smem_u32(&empty_bar[s]));
-        float x = dot.x + dot.y;
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        x *= rsqrtf(ms + a.eps) * kScoreUp;
+        for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int q = 0; q < S; ++q) x[q] += __shfl_xor_sync(0xffffffffu, x[q], o);
+        float top = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < S; ++q) {
+          x[q] = q == 0 || q0 + q < todo ? x[q] * (rsqrtf(ms[q] + a.eps) * kScoreUp) : -INFINITY;
+          top = fmaxf(top, x[q]);
+        }
         // The accumulators are rescaled only when a score passes the maximum they
         // are scaled by by more than 8: weights up to e^8 lose nothing in fp32.
-        const bool up = x > m + 8.f;
+        const bool up = top > m + 8.f;
         if (__any_sync(0xffffffffu, up)) {
-          const float f = up ? __expf(m - x) : 1.f;
+          const float f = up ? __expf(m - top) : 1.f;
           l *= f;
           const float2 f2 = make_float2(f, f);
 #pragma unroll
           for (int k = 0; k < 8 * C; ++k) acc[k] = fmul2(acc[k], f2);
-          if (up) m = x;
+          if (up) m = top;
         }
-        const float p = __expf(x - m);
-        l += p;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float ps = p * sc[c];
-          const float2 p2 = make_float2(ps, ps);
+        for (int q = 0; q < S; ++q) {
+          const float p = __expf(x[q] - m);
+          l += p;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) acc[c * 8 + k] = ffma2(p2, v[c * 8 + k], acc[c * 8 + k]);
+          for (int c = 0; c < C; ++c) {
+            const float ps = p * sc[q][c];
+            const float2 p2 = make_float2(ps, ps);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[c * 8 + k] = ffma2(p2, v[q][c * 8 + k], acc[c * 8 + k]);
+          }
         }
-      } else if (lane == 0) {
-        mbar_arrive(smem_u32(&empty_bar[s]));
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&empty_bar[s]));
       if (++s == nstage) {
         s = 0;
         phase ^= 1u;
@@ -299,7 +317,34 @@ __global__ void __launch_bounds__(Q8Read<C, L, kToken>::kThreads, 1)
         }
       }
     }
-    if (part != 0 || !ok || !busy) continue;
+    if (kCluster && cl > 1) {
+      // The same over the cluster, whose CTAs have one tile too: each leaves
+      // its share in its own memory, the first reads them.
+      float* box = reinterpret_cast<float*>(ring) + warp * R::kBox;
+      if (split == 1) named_sync(1, kWarps * 32);  // all warps are through with the ring
+      if (part == 0 && team < teams && rank > 0) {
+#pragma unroll
+        for (int k = 0; k < 8 * C; ++k) *reinterpret_cast<float2*>(box + k * 64 + lane * 2) = acc[k];
+        box[64 * 8 * C + lane] = m;
+        box[64 * 8 * C + 32 + lane] = l;
+      }
+      cluster_sync();
+      if (part == 0 && team < teams && rank == 0) {
+        for (int q = 1; q < cl; ++q) {
+          const uint32_t other = cluster_addr(smem_u32(box), static_cast<uint32_t>(q));
+          const float mo = ld_cluster(other + (64 * 8 * C + lane) * 4), lo = ld_cluster(other + (64 * 8 * C + 32 + lane) * 4);
+          const float top = fmaxf(m, mo);
+          const float ca = __expf(m - top), cb = __expf(mo - top);
+          l = l * ca + lo * cb;
+#pragma unroll
+          for (int k = 0; k < 8 * C; ++k)
+            acc[k] = ffma2(ld_cluster2(other + (k * 64 + lane * 2) * 4), make_float2(cb, cb), fmul2(acc[k], make_float2(ca, ca)));
+          m = top;
+        }
+      }
+      cluster_sync();  // the shares have been read: their owners may leave
+    }
+    if (part != 0 || rank != 0 || !ok || !busy) continue;
     const float inv = 1.0f / l;
 #pragma unroll
     for (int k = 0; k < 8 * C; ++k) acc[k] = fmul2(acc[k], make_float2(inv, inv));
@@ -425,37 +470,49 @@ __global__ void __launch_bounds__(kGenThreads) q8_read_general_kernel(Q8ReadArgs
   }
 }
 
-template <int C, int L, bool kToken>
-cudaError_t launch_clt(const Q8ReadArgs& a, cudaStream_t s) {
-  using R = Q8Read<C, L, kToken>;
-  const int G = q8_groups(a.d), stage_bytes = R::kTile * (128 * G + q8_tail_bytes(G));
-  const int fixed = 2 * kMaxStages * 8 + (kToken ? 0 : 512 * G);
+template <int K, int S, int C, int L, int NW, bool kCluster = false>
+cudaError_t launch_cl(const Q8ReadArgs& a, cudaStream_t s) {
+  using R = Q8Read<K, S, C, L, NW>;
+  const int G = q8_groups(a.d), stage_bytes = K * R::kTile * (128 * G + q8_tail_bytes(G));
+  const int fixed = 2 * kMaxStages * 8;
   int nstage = (kSmemMax - fixed) / stage_bytes;
   nstage = nstage > kMaxStages ? kMaxStages : nstage;
   const int64_t groups = (a.T + R::kRows - 1) / R::kRows;
   const int sms = sm_count();
   // As many warps to a group of tokens as there are to spare, so that each CTA still has one tile.
   int split = 1;
-  while (2 * split <= R::kWarps && 2 * split <= a.n_src && groups <= static_cast<int64_t>(sms) * (R::kWarps / (2 * split)))
+  while (2 * split <= R::kWarps && 2 * split * K <= a.n_src + K - 1 && groups <= static_cast<int64_t>(sms) * (R::kWarps / (2 * split)))
     split *= 2;
+  // And as many CTAs (a cluster), as long as every warp of them still has sources.
+  const int teams = R::kWarps / split;
+  const int64_t tiles = (groups + teams - 1) / teams;
+  int cl = 1;
+  while (kCluster && 2 * cl <= 8 && tiles * 2 * cl <= sms && 2 * cl * split * K <= a.n_src + K - 1) cl *= 2;
   int ring = nstage * stage_bytes;
   const int boxes = R::kWarps * R::kBox * 4;
-  if (split > 1 && ring < boxes) ring = boxes;
+  if (split * cl > 1 && ring < boxes) ring = boxes;
   const int smem = fixed + ring;
-  const void* fn = reinterpret_cast<const void*>(&q8_read_kernel<C, L, kToken>);
+  const void* fn = reinterpret_cast<const void*>(&q8_read_kernel<K, S, C, L, NW, kCluster>);
   cudaError_t e = allow_dynamic_smem(fn, kSmemMax);
   if (e != cudaSuccess) return e;
   // Rows of both outputs that start on 16-byte boundaries and hold whole 16-byte vectors.
   const int vec = a.d % (a.out_bf16 ? 8 : 4) == 0 && aligned16(a.out) && aligned16(a.pre.out);
-  const int teams = R::kWarps / split;
-  int64_t grid = (groups + teams - 1) / teams;
-  if (grid > sms) grid = sms;
-  return launch_pdl(q8_read_kernel<C, L, kToken>, static_cast<unsigned>(grid), R::kThreads, smem, s, a, nstage, split, vec);
-}
-
-template <int C, int L>
-cudaError_t launch_cl(const Q8ReadArgs& a, cudaStream_t s) {
-  return a.w ? launch_clt<C, L, false>(a, s) : launch_clt<C, L, true>(a, s);
+  const int64_t grid = tiles < sms ? tiles * cl : sms;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(R::kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cl);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cl > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, q8_read_kernel<K, S, C, L, NW, kCluster>, a, nstage, split, cl, vec);
 }
 
 cudaError_t launch_general(const Q8ReadArgs& a, cudaStream_t s) {
@@ -473,15 +530,29 @@ cudaError_t launch_general(const Q8ReadArgs& a, cudaStream_t s) {
 
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
   const int G = q8_groups(a.d);
+  // In each line the last C step holds codes: 8 G > (C - 1) L. Few tokens: a
+  // token's sources spread over many warps and CTAs, so few to a stage.
+  const int sms = sm_count();
+  if (a.T <= 2 * sms) {
+    if (G <= 4) return launch_cl<2, 2, 1, 32, 15, true>(a, s);
+    if (G <= 8) return launch_cl<2, 2, 2, 32, 11, true>(a, s);
+    if (G <= 12) return launch_cl<1, 1, 3, 32, 7, true>(a, s);
+    if (G <= 16) return launch_cl<1, 1, 4, 32, 7, true>(a, s);
+  }
+  auto rounds = [&](int tile) { return (a.T + static_cast<int64_t>(sms) * tile - 1) / (static_cast<int64_t>(sms) * tile) * tile; };
   switch (G) {
-    case 1: return launch_cl<1, 8>(a, s);
-    case 2: return launch_cl<2, 8>(a, s);
-    case 3: return launch_cl<3, 8>(a, s);
-    case 4: return launch_cl<4, 8>(a, s);
-    case 5: case 6: return launch_cl<3, 16>(a, s);
-    case 7: case 8: return launch_cl<4, 16>(a, s);
-    case 9: case 10: case 11: case 12: return launch_cl<3, 32>(a, s);
-    case 13: case 14: case 15: case 16: return launch_cl<4, 32>(a, s);
+    case 1: return launch_cl<6, 1, 2, 4, 11>(a, s);
+    case 2: return launch_cl<6, 1, 4, 4, 7>(a, s);
+    case 3: return launch_cl<4, 1, 3, 8, 7>(a, s);
+    case 4: return launch_cl<4, 1, 4, 8, 7>(a, s);
+    case 5: case 6: return launch_cl<8, 1, 3, 16, 7>(a, s);
+    case 7:
+    case 8:
+      // Tiles of 14 tokens, or of 11 where their last round leaves fewer SMs
+      // idle: 8192 x 896, 33 sources, a query for each token: 105 us and 110; 4999 x 1000, 17 sources: 53 and 47.
+      return rounds(14) * 20 <= rounds(11) * 21 ? launch_cl<6, 1, 4, 16, 7>(a, s) : launch_cl<4, 2, 2, 32, 11>(a, s);
+    case 9: case 10: case 11: case 12: return launch_cl<6, 1, 3, 32, 7>(a, s);
+    case 13: case 14: case 15: case 16: return launch_cl<6, 1, 4, 32, 7>(a, s);
     default: return launch_general(a, s);
   }
 }
