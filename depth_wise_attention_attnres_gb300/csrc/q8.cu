@@ -5,9 +5,7 @@
 // largest magnitude is three shuffles away; the scale follows from its bits,
 // and the codes, the exponents and the row's mean square (of the values the
 // codes stand for) leave together. Both directions are bound by the bytes they
-// stream: every load and store of a warp covers whole 128-byte lines (a lane's 16
-// features are two or four pieces, 8 lanes apart), and several loads a thread
-// are issued before the first is used.
+// stream, and several loads a thread are issued before the first is used.
 #include "q8.cuh"
 
 namespace attnres {
@@ -21,36 +19,20 @@ template <typename T> struct Raw16 {
   uint4 v[kVecs];
 };
 
-// A lane's 16 features of group g: piece i holds the 16 bytes from feature
-// 128 g + (8 i + j) kPer on (lane j of 8), zero from d on. `vec`: rows start on
+// Features [k0, k0 + 16) of a row, zero from d on. `vec`: rows start on
 // 16-byte boundaries and d is a whole number of 16-byte vectors.
 template <typename T>
-__device__ __forceinline__ void load_raw(const T* row, int g, int j, int d, bool vec, Raw16<T>& r) {
+__device__ __forceinline__ void load_raw(const T* row, int k0, int d, bool vec, Raw16<T>& r) {
   constexpr int kPer = 16 / sizeof(T);
+  if (vec) {
 #pragma unroll
-  for (int i = 0; i < Raw16<T>::kVecs; ++i) {
-    const int k = g * 128 + (i * 8 + j) * kPer;
-    if (vec) {
-      r.v[i] = k < d ? __ldcs(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0, 0, 0, 0);
-    } else {
-      T* e = reinterpret_cast<T*>(&r.v[i]);
+    for (int i = 0; i < Raw16<T>::kVecs; ++i)
+      r.v[i] = k0 + i * kPer < d ? __ldcs(reinterpret_cast<const uint4*>(row + k0) + i) : make_uint4(0, 0, 0, 0);
+  } else {
+    T* e = reinterpret_cast<T*>(r.v);
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) e[q] = k + q < d ? row[k + q] : from_f32<T>(0.f);
-    }
+    for (int i = 0; i < 16; ++i) e[i] = k0 + i < d ? row[k0 + i] : from_f32<T>(0.f);
   }
-}
-
-// The codes of such features, in the same places.
-__device__ __forceinline__ void store_codes(unsigned char* group, int j, const uint4& c, bf16) {
-  reinterpret_cast<uint2*>(group)[j] = make_uint2(c.x, c.y);
-  reinterpret_cast<uint2*>(group)[8 + j] = make_uint2(c.z, c.w);
-}
-__device__ __forceinline__ void store_codes(unsigned char* group, int j, const uint4& c, float) {
-  uint32_t* at = reinterpret_cast<uint32_t*>(group) + j;
-  at[0] = c.x;
-  at[8] = c.y;
-  at[16] = c.z;
-  at[24] = c.w;
 }
 
 __device__ __forceinline__ void widen(const Raw16<bf16>& r, float (&x)[16]) {
@@ -111,119 +93,158 @@ __device__ __forceinline__ uint4 encode16(const float (&x)[16], uint32_t e) {
                     encode4(y[8], y[9], y[10], y[11]), encode4(y[12], y[13], y[14], y[15]));
 }
 
-// L lanes a row (8: 4 rows a warp, one group of each at a time; 32: a row a
-// warp, 4 groups at a time). kBatch groups a lane are loaded at once.
+// a / b of values that are not negative: 32-bit where both fit (the 64-bit division is a long subroutine).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((a | b) >> 32) ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
+// Row number r of n sources of T rows: its source and token, and the row `step` further on.
+struct RowAt {
+  int64_t i, t;
+  __device__ __forceinline__ RowAt(int64_t r, int64_t T) : i(r < T ? 0 : divide(r, T)), t(r < T ? r : r - i * T) {}
+  __device__ __forceinline__ void advance(int64_t step, int64_t T) {
+    t += step;
+    if (t >= T) {
+      const int64_t q = t < 2 * T ? 1 : divide(t, T);
+      i += q;
+      t -= q * T;
+    }
+  }
+};
+
+// L lanes a row: 8 up to 8 groups (4 rows a warp, each lane 16 features of every
+// group), 32 beyond (a row a warp, 4 groups at a time). A warp writes a row's
+// tail with one 16-byte store (L = 8) or a word a step: with a byte a group,
+// narrow rows took 51 us where they now take 32 (262144 rows of 128, bf16).
 template <typename T, int L>
 __global__ void __launch_bounds__(kThreads) q8_write_kernel(Q8Rows a, int G, int vec) {
   constexpr int kRows = 32 / L;
-  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
-  const int lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
-  const int steps = (8 * G + L - 1) / L, gj = j >> 3, j8 = j & 7;
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // steps of a row loaded at once
+  const int lane = threadIdx.x & 31, j = lane % L;
+  const int chunks = 8 * G, steps = (chunks + L - 1) / L;
   const int mean_at = q8_mean_offset(G), tail_bytes = q8_tail_bytes(G);
   const int64_t source = q8_source_bytes(a.cap, a.d);
   const int64_t total = static_cast<int64_t>(a.n) * a.T;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kRows;  // rows between a warp's
   pdl_trigger();
   pdl_wait();
-  for (int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kRows; r0 < total;
-       r0 += warps * kRows) {
-    const int64_t r = r0 + sub;
+  int64_t r = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kRows + lane / L;
+  RowAt at(r, a.T);
+  for (; r - lane / L < total; r += step, at.advance(step, a.T)) {  // the same for every lane of the warp
     const bool valid = r < total;
-    const int64_t i = valid ? r / a.T : 0, t = valid ? r - i * a.T : 0;
+    const int64_t i = valid ? at.i : 0, t = valid ? at.t : 0;
     const T* x = static_cast<const T*>(a.x) + i * a.x_stride + t * a.d;
     unsigned char* out = static_cast<unsigned char*>(a.rows) + i * source + t * (128 * G);
     unsigned char* tail = static_cast<unsigned char*>(a.rows) + i * source + a.cap * (128 * G) + t * tail_bytes;
-    const int d = valid ? a.d : 0;  // lanes behind the last row read nothing
+    const int d = valid ? a.d : 0;  // lanes behind the last row read and write nothing
     float ms = 0.f;
+    uint32_t words[2] = {0, 0};  // L = 8: the row's exponents, two words at most
     for (int c0 = 0; c0 < steps; c0 += kBatch) {
       Raw16<T> raw[kBatch];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) load_raw(x, (c0 + b) * (L / 8) + gj, j8, d, vec, raw[b]);
+      for (int b = 0; b < kBatch; ++b) load_raw(x, ((c0 + b) * L + j) * 16, d, vec, raw[b]);
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         if (c0 + b >= steps) break;  // the same for every lane
-        const int g = (c0 + b) * (L / 8) + gj;
+        const int chunk = (c0 + b) * L + j;
         float v[16];
         widen(raw[b], v);
         const uint32_t e = group_exponent(v);
         const uint4 code = encode16(v, e);
-        float2 w[8], q = make_float2(0.f, 0.f);
+        float2 w[8], m2 = make_float2(0.f, 0.f);
         decode16(code, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q = ffma2(w[k], w[k], q);
+        for (int k = 0; k < 8; ++k) m2 = ffma2(w[k], w[k], m2);
         const float s = q8_scale(e);
-        ms += (q.x + q.y) * s * s;
-        if (valid && g < G) {
-          store_codes(out + g * 128, j8, code, T());
-          if (j8 == 0) tail[g] = static_cast<unsigned char>(e);
+        ms += (m2.x + m2.y) * s * s;
+        if (valid && chunk < chunks) *reinterpret_cast<uint4*>(out + chunk * 16) = code;
+        if constexpr (L == 8) {
+          words[0] |= c0 + b < 4 ? e << (8 * (c0 + b)) : 0;
+          words[1] |= c0 + b < 4 ? 0 : e << (8 * (c0 + b - 4));
+        } else {  // four groups' exponents a step: one word of the tail
+          uint32_t word = chunk < chunks ? e << (8 * (j >> 3)) : 0;
+          word |= __shfl_xor_sync(0xffffffffu, word, 8);
+          word |= __shfl_xor_sync(0xffffffffu, word, 16);
+          if (valid && j == 0) reinterpret_cast<uint32_t*>(tail)[c0 + b] = word;
         }
       }
     }
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
     if (valid && j == 0) {
-      for (int k = G; k < mean_at; ++k) tail[k] = 0;
-      *reinterpret_cast<float*>(tail + mean_at) = ms / static_cast<float>(a.d);
-      for (int k = mean_at + 4; k < tail_bytes; k += 4) *reinterpret_cast<uint32_t*>(tail + k) = 0;
+      const float mean = ms / static_cast<float>(a.d);
+      if constexpr (L == 8) {
+        const uint32_t m = __float_as_uint(mean);
+        *reinterpret_cast<uint4*>(tail) = make_uint4(words[0], G <= 4 ? m : words[1], G <= 4 ? 0 : m, 0);
+      } else {
+        *reinterpret_cast<float*>(tail + mean_at) = mean;
+        for (int k = mean_at + 4; k < tail_bytes; k += 4) *reinterpret_cast<uint32_t*>(tail + k) = 0;
+      }
     }
   }
 }
 
 // Reading back: a lane's piece is the codes of 16 bytes of output (8 of bf16, 4
 // of fp32), so L lanes (16 or 32, all of a warp where the row is long enough)
-// read and write whole lines. kBatch pieces a lane are loaded at once.
+// read and write whole lines. kBatch pieces a lane are loaded at once, of one row or of several.
 template <typename T, int L>
 __global__ void __launch_bounds__(kThreads) q8_back_kernel(Q8Rows a, int G) {
   constexpr int kPer = 16 / sizeof(T), kRows = 32 / L, kBatch = 8;
   const int lane = threadIdx.x & 31, j = lane % L;
   const int64_t source = q8_source_bytes(a.cap, a.d);
   const int64_t total = static_cast<int64_t>(a.n) * a.T;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  const int pieces = (a.d + kPer - 1) / kPer;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kRows;
+  const int tail_bytes = q8_tail_bytes(G);
   pdl_trigger();
   pdl_wait();
-  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kRows + lane / L; r < total;
-       r += warps * kRows) {
-    const int64_t i = r / a.T, t = r - i * a.T;
-    T* out = static_cast<T*>(const_cast<void*>(a.x)) + i * a.x_stride + t * a.d;
-    const unsigned char* row = static_cast<const unsigned char*>(a.rows) + i * source + t * (128 * G);
-    const unsigned char* tail =
-        static_cast<const unsigned char*>(a.rows) + i * source + a.cap * (128 * G) + t * q8_tail_bytes(G);
-    for (int p0 = j; p0 < pieces; p0 += kBatch * L) {
-      uint2 code[kBatch];
-      uint32_t e[kBatch];
+  int64_t r = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kRows + lane / L;
+  RowAt at(r, a.T);
+  int k = j * kPer;  // the lane's next piece, in row r
+  while (r < total) {
+    uint2 code[kBatch];
+    uint32_t e[kBatch];
+    T* to[kBatch];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int k = (p0 + b * L) * kPer;
-        code[b] = make_uint2(0, 0);
-        e[b] = 1;
+    for (int b = 0; b < kBatch; ++b) {
+      to[b] = nullptr;
+      e[b] = 1;
+      code[b] = make_uint2(0, 0);
+      if (r < total) {
         if (k < a.d) {
+          const unsigned char* rows = static_cast<const unsigned char*>(a.rows) + at.i * source;
+          const unsigned char* c = rows + at.t * (128 * G) + k;
           if (kPer == 8)
-            code[b] = __ldcs(reinterpret_cast<const uint2*>(row + k));
+            code[b] = __ldcs(reinterpret_cast<const uint2*>(c));
           else
-            code[b].x = __ldcs(reinterpret_cast<const uint32_t*>(row + k));
-          e[b] = tail[k >> 7];
+            code[b].x = __ldcs(reinterpret_cast<const uint32_t*>(c));
+          e[b] = rows[a.cap * (128 * G) + at.t * tail_bytes + (k >> 7)];
+          to[b] = static_cast<T*>(const_cast<void*>(a.x)) + at.i * a.x_stride + at.t * a.d + k;
+        }
+        k += L * kPer;
+        if (k >= a.d) {
+          k = j * kPer;
+          r += step;
+          at.advance(step, a.T);
         }
       }
+    }
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int k = (p0 + b * L) * kPer;
-        if (k >= a.d) break;
-        const float s = q8_scale(e[b]);
-        const float2 s2 = make_float2(s, s);
-        float2 v[4];
-        decode4(code[b].x, v[0], v[1]);
-        v[0] = fmul2(v[0], s2);
-        v[1] = fmul2(v[1], s2);
-        if constexpr (kPer == 8) {
-          decode4(code[b].y, v[2], v[3]);
-          v[2] = fmul2(v[2], s2);
-          v[3] = fmul2(v[3], s2);
-          __stcs(reinterpret_cast<uint4*>(out + k), make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
-                                                               pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y)));
-        } else {
-          __stcs(reinterpret_cast<float4*>(out + k), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
-        }
+    for (int b = 0; b < kBatch; ++b) {
+      if (!to[b]) continue;
+      const float s = q8_scale(e[b]);
+      const float2 s2 = make_float2(s, s);
+      float2 v[4];
+      decode4(code[b].x, v[0], v[1]);
+      v[0] = fmul2(v[0], s2);
+      v[1] = fmul2(v[1], s2);
+      if constexpr (kPer == 8) {
+        decode4(code[b].y, v[2], v[3]);
+        v[2] = fmul2(v[2], s2);
+        v[3] = fmul2(v[3], s2);
+        __stcs(reinterpret_cast<uint4*>(to[b]), make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                          pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y)));
+      } else {
+        __stcs(reinterpret_cast<float4*>(to[b]), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
       }
     }
   }
@@ -231,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) q8_back_kernel(Q8Rows a, int G) {
 
 // The same into rows that do not start on 16-byte boundaries: an element a lane,
 // so that a warp still writes consecutive elements (16384 rows of 1001 to bf16, four
-// sources: TIME us; with 16 elements a lane 348).
+// sources: 53 us; with 16 elements a lane 348).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) q8_back_element_kernel(Q8Rows a, int G) {
   constexpr int kBatch = 8;
@@ -242,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) q8_back_element_kernel(Q8Rows a, int
   pdl_trigger();
   pdl_wait();
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); r < total; r += warps) {
-    const int64_t i = r / a.T, t = r - i * a.T;
+    const int64_t i = divide(r, a.T), t = r - i * a.T;
     T* out = static_cast<T*>(const_cast<void*>(a.x)) + i * a.x_stride + t * a.d;
     const unsigned char* row = static_cast<const unsigned char*>(a.rows) + i * source + t * (128 * G);
     const unsigned char* tail =
@@ -317,7 +338,7 @@ bool rows_vec(const Q8Rows& a) {
 
 unsigned row_grid(int64_t rows, int per_warp) {
   const int64_t blocks = (rows + per_warp * (kThreads / 32) - 1) / (per_warp * (kThreads / 32));
-  const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * 16;
   return static_cast<unsigned>(blocks < cap ? blocks : cap);
 }
 
