@@ -600,11 +600,10 @@ class Q8Rows:
     """n sources of T rows of d features in 8 bits: an AttnRes history, or (n = 1) hidden states.
 
     Owns its storage (`buffer`, uint8 [n, attnres_q8_source_bytes(T, d)], zero
-    at first); its pointer is kept, so the buffer must not be given other
-    storage (set_, resize_). `codes` (float8_e4m3fn [n, T, d]), `exponents`
-    (uint8 [n, T, ceil(d / 128)]: the scale of a group is 2^(exponent - 127))
-    and `mean_square` (fp32 [n, T]) are views of it. Calls use the first rows,
-    as many as their [T, d] argument has."""
+    at first, which must keep its size). `codes` (float8_e4m3fn [n, T, d]),
+    `exponents` (uint8 [n, T, ceil(d / 128)]: the scale of a group is
+    2^(exponent - 127)) and `mean_square` (fp32 [n, T]) are views of it. Calls
+    use the first rows, as many as their [T, d] argument has."""
 
     def __init__(self, n: int, T: int, d: int, device=None):
         source = attnres_q8_source_bytes(T, d)
@@ -614,7 +613,11 @@ class Q8Rows:
         self.buffer = torch.zeros(n, source, dtype=torch.uint8, device="cuda" if device is None else device)
         if not self.buffer.is_cuda:
             raise ValueError("rows must be on a CUDA device")
-        self.pointer, self.device = self.buffer.data_ptr(), self.buffer.get_device()
+        self.device = self.buffer.get_device()
+
+    @property
+    def pointer(self) -> int:
+        return self.buffer.data_ptr()
 
     @functools.cached_property
     def codes(self) -> torch.Tensor:
@@ -650,7 +653,13 @@ class Q8Weight:
             raise ValueError("m and d must be at least 1")
         self.m, self.d = m, d
         self.buffer = torch.zeros(size, dtype=torch.uint8, device="cuda" if device is None else device)
-        self.pointer, self.device = self.buffer.data_ptr(), self.buffer.get_device()
+        if not self.buffer.is_cuda:
+            raise ValueError("weights must be on a CUDA device")
+        self.device = self.buffer.get_device()
+
+    @property
+    def pointer(self) -> int:
+        return self.buffer.data_ptr()
 
     @functools.cached_property
     def codes(self) -> torch.Tensor:

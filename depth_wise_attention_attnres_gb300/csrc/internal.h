@@ -323,7 +323,7 @@ struct Q8ReadArgs {
   PreNorm pre;
   void* out;            // may be nullptr when pre.gamma is set
   int out_bf16;
-  int64_t withhold = -1;  // test hook of the streaming kernel (as FullArgs; per warp)
+  int64_t withhold = -1;  // test hook of the streaming kernel: the stage of each CTA to leave unfilled
 };
 cudaError_t launch_q8_write(const Q8Rows& a, cudaStream_t s);
 cudaError_t launch_q8_back(const Q8Rows& a, cudaStream_t s);

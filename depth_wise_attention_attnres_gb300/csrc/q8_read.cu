@@ -3,16 +3,25 @@
 //
 // Streaming kernel (rows of up to 2048 features). A row is held by L lanes, 16
 // features in each of C steps, so a warp works on 32 / L tokens at once; the
-// 8 lanes of a group share its scale. A producer warp brings, source by source,
-// the rows of the CTA's tokens into a ring of shared-memory stages (one bulk copy of codes,
-// one of tails). Per source a lane decodes its 16 C codes once and keeps the
-// values, multiplies them with u (in registers; from shared memory it took
+// 8 lanes of a group share its scale. A producer warp brings the rows of the CTA's
+// tokens into a ring of shared-memory stages, K sources a stage (one bulk copy of codes
+// and one of tails for each source). Per source a lane decodes its 16 C codes once and
+// keeps the values, multiplies them with u (in registers; from shared memory it took
 // half as long again), adds over the L lanes, and adds the weighted values onto
 // its accumulators. rms needs no sum: the mean square comes with the row.
 //
+// It is bound by instructions, not bytes: a code takes half a conversion to fp16,
+// one to fp32 and two half multiply-adds (pairs), and u, values and accumulators
+// take most of the registers, so an SM has 7 to 15 warps, which issue in 45 % of the
+// cycles. What helped was less around a source: several sources a stage (64 x 8192 x 896:
+// 178 us with one source a stage, 127 with six) and a rescaling only when the maximum
+// has grown by 8. Scores by the tensor cores, with the values weighted here, took
+// 161 us and more; their operands have to be decoded and laid out anew.
+//
 // When there are fewer groups of tokens than warps, `split` warps of a CTA
-// share one: each takes every split-th source, and the maxima, sums and
-// accumulators are joined through shared memory.
+// share one (each takes every split-th K sources) and, for few tokens, `cluster` CTAs;
+// the maxima, sums and accumulators are joined through shared memory (one token, 141
+// sources of 640: 9.9 us, 15 with the warps of one CTA).
 //
 // General kernel (wider rows): a CTA a token; the scores of all sources, their
 // softmax, then the weighted sum, reading the rows twice.
@@ -217,7 +226,7 @@ __global__ void __launch_bounds__(Q8Read<K, S, C, L, NW>::kThreads, 1)
     float m = -3.402823466e38f, l = 0.f;
     for (int step = 0; step < steps; ++step) {
       // After a wait that ran out the warp goes on without waiting (barriers
-      // stay matched, nothing is stored) and the failure is on record.
+      // stay matched, the warp stores nothing) and the failure is on record.
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[s]), phase));
       const int first = ((step * cl + rank) * split + part) * K;
       const unsigned char* r = ring + s * stage_bytes + codes_at + lane_at;

@@ -176,7 +176,8 @@ int attnres_full_fwd_dynq(const void* V, int64_t src_stride, int32_t n_src, int6
  * magnitude below 2^-117 keeps fewer than four bits. Where e_g = 120 codes stop
  * at 240, so that v_k stays finite. An element that is not finite becomes NaN.
  * With the row goes mean_k v_k^2 (fp32), the mean square its key RMSNorm needs
- * in every read.
+ * in every read (infinite, and the row's score 0, where squares of its values
+ * add up past fp32's range: magnitudes of some 1e19).
  *
  * A source is `cap` rows in attnres_q8_source_bytes(cap, d) bytes, with G = ceil(d / 128):
  *   cap rows of 128 G bytes: the codes, zero from feature d on;
@@ -788,9 +789,11 @@ int64_t attnres_test_fail_launch(int64_t after);
  * 2 = the tensor-core stage 1 (index counts each CTA's tiles), 3 = the tiled
  * merge (index counts each CTA's tiles; tiles fetched before the previous
  * kernel finishes, in a Block pass, are never withheld), 4 = the gated residual
- * and its backward (index counts each team's rows). Every CTA (4: team) with more
- * than `index` copies withholds its copy number `index`; its other copies are
- * issued and waited for before the CTA exits. Stays set until changed.
+ * and its backward (index counts each team's rows), 5 = the streaming read over
+ * 8-bit rows (index counts each CTA's stages, of one or more sources). Every CTA
+ * (4: team) with more than `index` copies withholds its copy number `index`; its
+ * other copies are issued and waited for before the CTA exits. Stays set until
+ * changed.
  * Returns ATTNRES_ERR_INVALID_ARG for an unknown kernel or a negative index.
  */
 int attnres_test_withhold_stage(int32_t kernel, int64_t index);

@@ -1,5 +1,7 @@
 """8-bit rows on the GPU: writing, reading back, the Full read over them, weights and the query projection, each
 against its fp64 definition (tests/_q8.py, whose bounds are those of fp32 evaluation)."""
+import copy
+
 import pytest
 import torch
 
@@ -186,6 +188,96 @@ def test_full_read_around_the_sharing_of_sources(T):
     """Token counts at which the warps a token's sources are shared by change, and the last groups of tokens."""
     for d in (128, 512, 896, 2048):
         read_case(9, T, d, "bf16", "fixed", False, T)
+
+
+@pytest.mark.parametrize("d", [100, 256, 384, 512, 640, 896, 1000, 1152, 2048])
+def test_full_read_stages(d):
+    """Source counts around the number a stage holds, with sources shared between warps and without."""
+    for n in (1, 2, 3, 4, 5, 6, 7, 8, 9, 13):
+        read_case(n, 350 + n, d, "f32", "fixed", False, n)
+        read_case(n, 5003, d, "bf16", "fixed", n % 2 == 1, n + 50)
+
+
+@pytest.mark.parametrize("n,T", [(12, 303), (12, 304), (12, 305), (40, 19), (40, 38), (17, 39), (33, 76), (33, 77), (9, 152),
+                                 (9, 153), (200, 11)])
+def test_full_read_clusters(n, T):
+    """Token counts around those at which CTAs begin to share a token's sources, and at which this ends."""
+    for d in (128, 512, 640, 1024, 1152, 1600, 2048):
+        read_case(n, T, d, "f32", "token" if T % 2 else "fixed", T % 3 == 0, n + T)
+
+
+def test_broken_rows_in_clusters():
+    """NaN in one of many sources, and a token whose other sources have weight 0."""
+    n, T, d = 141, 3, 640
+    x = _q8.history(n, T, d, gen(4), DEV, loud=False)
+    w, gamma = torch.randn(d, generator=gen(5), device=DEV) / d ** 0.5, torch.ones(d, device=DEV)
+    for i in (0, 70, 140):
+        y = x.clone()
+        y[i, 1, 639] = float("inf")
+        rows = ar.Q8Rows(n, T, d, device=DEV)
+        ar.attnres_q8_write(y, rows)
+        out = ar.attnres_full_fwd_q8(rows, n, w, gamma, 1e-6, torch.empty(T, d, device=DEV))
+        assert out[1].isnan().all() and out[[0, 2]].isfinite().all()
+    y = x.clone()
+    y[100, 2] = 50 * w  # the score of one source is above all others
+    rows = ar.Q8Rows(n, T, d, device=DEV)
+    ar.attnres_q8_write(y, rows)
+    out = ar.attnres_full_fwd_q8(rows, n, 90 * w, gamma, 1e-6, torch.empty(T, d, device=DEV))
+    z, dz, _, _ = _q8.read(values_of(rows), 90 * w, gamma, 1e-6)
+    _q8.assert_within(out, z, dz)
+
+
+def test_two_graphs_at_once():
+    """Two captured chains replayed on two streams at the same time: no memory is shared between calls."""
+    n, T, d = 9, 2500, 640
+    w, gamma = torch.randn(d, generator=gen(2), device=DEV) * 0.1, torch.ones(d, device=DEV)
+    W8 = ar.attnres_q8_weight(torch.randn(d, d, generator=gen(3), device=DEV) / d ** 0.5, ar.Q8Weight(d, d, device=DEV))
+    runs = []
+    for k in range(2):
+        x = _q8.history(n, T, d, gen(10 + k), DEV)
+        rows, out, Q = ar.Q8Rows(n, T, d, device=DEV), torch.empty(T, d, device=DEV), torch.empty(T, d, device=DEV)
+        few = torch.empty(2, d, device=DEV)
+
+        def chain(x=x, rows=rows, out=out, Q=Q, few=few):
+            ar.attnres_q8_write(x, rows)
+            ar.attnres_query_projection_q8(rows, n - 1, W8, Q)
+            ar.attnres_full_fwd_q8(rows, n, None, gamma, 1e-6, out, Q=Q)
+            ar.attnres_full_fwd_q8(rows, n, w, gamma, 1e-6, few)
+
+        chain()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (rows.buffer, out, Q, few)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chain()
+        runs.append((graph, [rows.buffer, out, Q, few], want, torch.cuda.Stream(), chain))  # the chain keeps its input
+    for _, got, *_ in runs:
+        for t in got:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, _, _, stream, _ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert ar.attnres_device_status() == 0
+    for _, got, want, *_ in runs:
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_copies_of_rows():
+    """A copied Q8Rows or Q8Weight has storage of its own."""
+    T, d = 20, 256
+    rows, v = made(2, T, d, gen(1))
+    other = copy.deepcopy(rows)
+    ar.attnres_q8_write(torch.ones(T, d, device=DEV), other, 1)
+    assert torch.equal(values_of(rows), v) and (values_of(other)[1] == 1).all() and torch.equal(values_of(other)[0], v[0])
+    W8 = ar.attnres_q8_weight(torch.ones(d, d, device=DEV), ar.Q8Weight(d, d, device=DEV))
+    zero = ar.attnres_q8_weight(torch.zeros(d, d, device=DEV), copy.deepcopy(W8))
+    Q = torch.empty(T, d, device=DEV)
+    assert (ar.attnres_query_projection_q8(other, 1, W8, Q) == d).all()
+    assert not ar.attnres_query_projection_q8(other, 1, zero, Q).any()
 
 
 def test_single_source_is_returned():
@@ -542,22 +634,22 @@ def test_binding_refusals():
     ar.attnres_query_projection_q8(empty, 0, W8, torch.zeros(0, 64, device=DEV))
 
 
-@pytest.mark.parametrize("index", [0, 3])
-@pytest.mark.parametrize("n,T,d", [(9, 80000, 256), (20, 1, 640), (13, 6000, 2048)])
-def test_a_copy_that_never_arrives(n, T, d, index):
+# The stages of a CTA: 2 where the warps (and CTAs) that share a token take 16 sources (and 128) at once.
+@pytest.mark.parametrize("index", [0, 1, 3])
+@pytest.mark.parametrize("n,T,d,stages", [(9, 80000, 256, 4), (20, 1, 640, 2), (13, 6000, 2048, 4), (141, 2, 640, 2)])
+def test_a_copy_that_never_arrives(n, T, d, stages, index):
     """A withheld copy ends the kernel with a timeout on record, and the next call is right again."""
     rows, v = made(n, T, d, gen(1))
     w, gamma = torch.randn(d, generator=gen(2), device=DEV) * 0.1, torch.ones(d, device=DEV)
     want, out = torch.empty(T, d, device=DEV), torch.empty(T, d, device=DEV)
     ar.attnres_full_fwd_q8(rows, n, w, gamma, 1e-6, want)
     assert ar.attnres_device_status() == 0
-    used = binding.WITHHOLD_Q8_READ
-    binding.attnres_test_withhold_stage(used, index)
+    binding.attnres_test_withhold_stage(binding.WITHHOLD_Q8_READ, index)
     try:
         ar.attnres_full_fwd_q8(rows, n, w, gamma, 1e-6, out)
         status = ar.attnres_device_status()
     finally:
         binding.attnres_test_withhold_stage(binding.WITHHOLD_NONE)
-    assert status == (4 if index == 0 or T > 1 else status)
+    assert status == (4 if index < stages else 0)
     ar.attnres_full_fwd_q8(rows, n, w, gamma, 1e-6, out)
     assert ar.attnres_device_status() == 0 and torch.equal(out, want)
