@@ -92,11 +92,12 @@ struct Q8Read {
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kTile = kWarps * kRows;
   static constexpr int kBox = (16 * C + 2) * 32;  // floats of a warp's share in a join
+  static constexpr int kGains = 16 * C * L;       // floats of a row of gains
 };
 
 template <int K, int S, int C, int L, int NW, bool kCluster>
 __global__ void __launch_bounds__(Q8Read<K, S, C, L, NW>::kThreads, 1)
-    q8_read_kernel(Q8ReadArgs a, int nstage, int split, int cluster, int vec) {
+    q8_read_kernel(Q8ReadArgs a, int nstage, int split, int cluster, int vec, int qvec) {
   using R = Q8Read<K, S, C, L, NW>;
   constexpr int kRows = R::kRows, kWarps = R::kWarps;
   const int cl = kCluster ? cluster : 1;
@@ -106,7 +107,10 @@ __global__ void __launch_bounds__(Q8Read<K, S, C, L, NW>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
   const int G = (a.d + 127) / 128, d = a.d, n = a.n_src, Dp = 128 * G;
   const int tail_bytes = q8_tail_bytes(G), stage_bytes = K * R::kTile * (Dp + tail_bytes);
-  unsigned char* ring = smem + 2 * kMaxStages * 8;
+  // Gains by feature, a lane's 16 of a step as four vectors that are L vectors
+  // apart: w gamma (or gamma, for Q's rows), then gamma_pre. Zero from d on.
+  float* gains = reinterpret_cast<float*>(smem + 2 * kMaxStages * 8);
+  unsigned char* ring = reinterpret_cast<unsigned char*>(gains + (a.pre.gamma ? 2 : 1) * R::kGains);
   // Tiles of `teams` groups of kRows tokens; a team of `split` warps has a group.
   const int teams = kWarps / split, steps = (n + K * split * cl - 1) / (K * split * cl);
   const int64_t T = a.T, groups = (T + kRows - 1) / kRows;
@@ -126,8 +130,14 @@ __global__ void __launch_bounds__(Q8Read<K, S, C, L, NW>::kThreads, 1)
     }
     mbar_fence_init();
   }
-  __syncthreads();
   pdl_wait();
+  for (int k = threadIdx.x; k < R::kGains; k += R::kThreads) {
+    const int chunk = k >> 4, at = ((chunk / L * 4 + (k >> 2 & 3)) * L + chunk % L) * 4 + (k & 3);
+    const float g = k < d ? a.gamma[k] : 0.f;
+    gains[at] = (a.w && k < d ? a.w[k] * kQueryDown : kQueryDown) * g;
+    if (a.pre.gamma) gains[R::kGains + at] = k < d ? a.pre.gamma[k] : 0.f;
+  }
+  __syncthreads();
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
@@ -199,18 +209,41 @@ __global__ void __launch_bounds__(Q8Read<K, S, C, L, NW>::kThreads, 1)
   const int lane_at = j * 16, tail_at = K * R::kTile * Dp + (warp * kRows + sub) * tail_bytes, ms_at = q8_mean_offset(G);
   const int codes_at = (warp * kRows + sub) * Dp;
 
+  auto gain = [&](int which, int c, int i) {
+    return *reinterpret_cast<const float4*>(gains + which * R::kGains + ((c * 4 + i) * L + j) * 4);
+  };
   float2 u[8 * C];
+  if (a.w) {
+#pragma unroll
+    for (int i = 0; i < 4 * C; ++i) {
+      const float4 g = gain(0, i >> 2, i & 3);
+      u[2 * i] = make_float2(g.x, g.y);
+      u[2 * i + 1] = make_float2(g.z, g.w);
+    }
+  }
   auto load_query = [&](const float* q) {
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = (c * L + j) * 16 + 2 * i;
-        u[c * 8 + i] = make_float2(k < d ? q[k] * kQueryDown * a.gamma[k] : 0.f,
-                                   k + 1 < d ? q[k + 1] * kQueryDown * a.gamma[k + 1] : 0.f);
+    for (int i = 0; i < 4 * C; ++i) {
+      const int k = ((i >> 2) * L + j) * 16 + (i & 3) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (qvec) {
+        if (k < d) x = __ldg(reinterpret_cast<const float4*>(q + k));
+      } else {
+        if (k < d) x.x = q[k];
+        if (k + 1 < d) x.y = q[k + 1];
+        if (k + 2 < d) x.z = q[k + 2];
+        if (k + 3 < d) x.w = q[k + 3];
       }
+      u[2 * i] = make_float2(x.x, x.y);
+      u[2 * i + 1] = make_float2(x.z, x.w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * C; ++i) {
+      const float4 g = gain(0, i >> 2, i & 3);
+      u[2 * i] = fmul2(u[2 * i], make_float2(g.x, g.y));
+      u[2 * i + 1] = fmul2(u[2 * i + 1], make_float2(g.z, g.w));
+    }
   };
-  if (a.w) load_query(a.w);
 
   int s = 0;
   uint32_t phase = 0;
@@ -378,10 +411,10 @@ __global__ void __launch_bounds__(Q8Read<K, S, C, L, NW>::kThreads, 1)
 #pragma unroll
       for (int c = 0; c < C; ++c) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = (c * L + j) * 16 + 2 * i;
-          acc[c * 8 + i].x *= rr * (k < d ? a.pre.gamma[k] : 0.f);
-          acc[c * 8 + i].y *= rr * (k + 1 < d ? a.pre.gamma[k + 1] : 0.f);
+        for (int i = 0; i < 4; ++i) {
+          const float4 g = gain(1, c, i);
+          acc[c * 8 + 2 * i] = fmul2(acc[c * 8 + 2 * i], make_float2(rr * g.x, rr * g.y));
+          acc[c * 8 + 2 * i + 1] = fmul2(acc[c * 8 + 2 * i + 1], make_float2(rr * g.z, rr * g.w));
         }
         put(a.pre.out, c);
       }
@@ -483,7 +516,7 @@ template <int K, int S, int C, int L, int NW, bool kCluster = false>
 cudaError_t launch_cl(const Q8ReadArgs& a, cudaStream_t s) {
   using R = Q8Read<K, S, C, L, NW>;
   const int G = q8_groups(a.d), stage_bytes = K * R::kTile * (128 * G + q8_tail_bytes(G));
-  const int fixed = 2 * kMaxStages * 8;
+  const int fixed = 2 * kMaxStages * 8 + (a.pre.gamma ? 2 : 1) * R::kGains * 4;
   int nstage = (kSmemMax - fixed) / stage_bytes;
   nstage = nstage > kMaxStages ? kMaxStages : nstage;
   const int64_t groups = (a.T + R::kRows - 1) / R::kRows;
@@ -506,6 +539,7 @@ cudaError_t launch_cl(const Q8ReadArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // Rows of both outputs that start on 16-byte boundaries and hold whole 16-byte vectors.
   const int vec = a.d % (a.out_bf16 ? 8 : 4) == 0 && aligned16(a.out) && aligned16(a.pre.out);
+  const int qvec = a.Q && a.d % 4 == 0 && aligned16(a.Q);
   const int64_t grid = tiles < sms ? tiles * cl : sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -521,7 +555,7 @@ cudaError_t launch_cl(const Q8ReadArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cl > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, q8_read_kernel<K, S, C, L, NW, kCluster>, a, nstage, split, cl, vec);
+  return cudaLaunchKernelEx(&cfg, q8_read_kernel<K, S, C, L, NW, kCluster>, a, nstage, split, cl, vec, qvec);
 }
 
 cudaError_t launch_general(const Q8ReadArgs& a, cudaStream_t s) {
