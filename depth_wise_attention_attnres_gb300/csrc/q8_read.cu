@@ -12,16 +12,18 @@
 //
 // It is bound by instructions, not bytes: a code takes half a conversion to fp16,
 // one to fp32 and two half multiply-adds (pairs), and u, values and accumulators
-// take most of the registers, so an SM has 7 to 15 warps, which issue in 45 % of the
+// take most of the registers, so an SM has 7 to 15 warps, which issue in 40 % of the
 // cycles. What helped was less around a source: several sources a stage (64 x 8192 x 896:
-// 178 us with one source a stage, 127 with six) and a rescaling only when the maximum
-// has grown by 8. Scores by the tensor cores, with the values weighted here, took
-// 161 us and more; their operands have to be decoded and laid out anew.
+// 178 us with one source a stage, 123 with six), a rescaling only when the maximum
+// has grown by 8, and gains from shared memory (8192 x 896, 33 sources, a query for
+// each token: 105 us with scalar loads of gamma and query, 83 now). Scores by the tensor cores, with
+// the values weighted here, took 161 us and more; their operands have to be decoded
+// and laid out anew.
 //
 // When there are fewer groups of tokens than warps, `split` warps of a CTA
 // share one (each takes every split-th K sources) and, for few tokens, `cluster` CTAs;
 // the maxima, sums and accumulators are joined through shared memory (one token, 141
-// sources of 640: 9.9 us, 15 with the warps of one CTA).
+// sources of 640: 8.2 us, 17.7 with the warps of one CTA).
 //
 // General kernel (wider rows): a CTA a token; the scores of all sources, their
 // softmax, then the weighted sum, reading the rows twice.
@@ -574,9 +576,11 @@ cudaError_t launch_general(const Q8ReadArgs& a, cudaStream_t s) {
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
   const int G = q8_groups(a.d);
   // In each line the last C step holds codes: 8 G > (C - 1) L. Few tokens: a
-  // token's sources spread over many warps and CTAs, so few to a stage.
+  // token's sources spread over many warps and CTAs, so few to a stage (9 sources:
+  // 228 x 640 in 6.0 us, 7.7 by the kernels below; 33: 228 x 2048 in 12.5 and 14.8, 228 x 640
+  // in 9.9 and 8.0, 300 x 640 in 10.1 and 8.2).
   const int sms = sm_count();
-  if (a.T <= 2 * sms) {
+  if (a.T <= 3 * sms / 2) {
     if (G <= 4) return launch_cl<2, 2, 1, 32, 15, true>(a, s);
     if (G <= 8) return launch_cl<2, 2, 2, 32, 11, true>(a, s);
     if (G <= 12) return launch_cl<1, 1, 3, 32, 7, true>(a, s);
@@ -586,15 +590,17 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
   switch (G) {
     case 1: return launch_cl<6, 1, 2, 4, 11>(a, s);
     case 2: return launch_cl<6, 1, 4, 4, 7>(a, s);
-    case 3: return launch_cl<4, 1, 3, 8, 7>(a, s);
+    case 3: return launch_cl<5, 1, 3, 8, 11>(a, s);
     case 4: return launch_cl<4, 1, 4, 8, 7>(a, s);
     case 5: case 6: return launch_cl<8, 1, 3, 16, 7>(a, s);
     case 7:
     case 8:
       // Tiles of 14 tokens, or of 11 where their last round leaves fewer SMs
-      // idle: 8192 x 896, 33 sources, a query for each token: 105 us and 110; 4999 x 1000, 17 sources: 53 and 47.
-      return rounds(14) * 20 <= rounds(11) * 21 ? launch_cl<6, 1, 4, 16, 7>(a, s) : launch_cl<4, 2, 2, 32, 11>(a, s);
-    case 9: case 10: case 11: case 12: return launch_cl<6, 1, 3, 32, 7>(a, s);
+      // idle and no tokens are shared by warps of the first (64 sources of 896: 1200 tokens
+      // 34.4 us and 29.6, 2000 tokens 35.7 and 47.1, 850 tokens 23.3 and 28.9).
+      return a.T <= 6 * sms || rounds(14) * 20 <= rounds(11) * 21 ? launch_cl<6, 1, 4, 16, 7>(a, s)
+                                                                  : launch_cl<4, 2, 2, 32, 11>(a, s);
+    case 9: case 10: case 11: case 12: return launch_cl<5, 1, 3, 32, 11>(a, s);
     case 13: case 14: case 15: case 16: return launch_cl<6, 1, 4, 32, 7>(a, s);
     default: return launch_general(a, s);
   }
