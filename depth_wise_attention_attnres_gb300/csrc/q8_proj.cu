@@ -135,6 +135,7 @@ __device__ unsigned int g_q8_proj_timeout = 0;
 
 constexpr int kBM = 128, kBK = 128;  // rows of a CTA's tile; features of a block
 constexpr int kATile = kBM * kBK;    // bytes
+constexpr uint32_t kNextScale = (1u << 4) | (1u << 29);  // the next scale byte of A and of B, in the instruction descriptor
 constexpr int kScaleWarps = 4, kProducer = 4, kIssuer = 5, kEpi = 8;
 constexpr int kThreads = (kScaleWarps + 2 + kEpi) * 32;
 constexpr int kScaleCols = 12, kSlots = 3;
@@ -143,10 +144,12 @@ constexpr int kSmemMax = 227 * 1024;
 
 template <int BN, int CG> struct Tile {
   static constexpr int kBRows = BN / CG;                               // weight rows a CTA holds
-  static constexpr int kStageBytes = kATile + kBRows * kBK;
+  static constexpr int kBlockBytes = kATile + kBRows * kBK;            // a block's operands
   static constexpr int kFixed = 1024 + 256 + kEpi * kStageFloats * 4;  // alignment slack, barriers, staging
-  static constexpr int kFit = (kSmemMax - kFixed) / kStageBytes;
-  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kFit = (kSmemMax - kFixed) / kBlockBytes;       // blocks
+  static constexpr int kBlocks = kFit >= 6 ? 2 : 1;                    // of a stage
+  static constexpr int kStageBytes = kBlocks * kBlockBytes;
+  static constexpr int kStages = kFit / kBlocks;
   static constexpr int kSmem = kFixed + kStages * kStageBytes;
   static constexpr int kUsed = 2 * BN + kSlots * kScaleCols;
   static constexpr uint32_t kTmemCols = kUsed <= 128 ? 128u : (kUsed <= 256 ? 256u : 512u);
@@ -154,7 +157,7 @@ template <int BN, int CG> struct Tile {
   // scales of powers of two (23 = 1), M / 16 (24-28); which scale byte of B (4-5) and A (29-30) is added to it.
   static constexpr uint32_t kIdesc =
       (static_cast<uint32_t>(BN >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(CG * kBM >> 4) << 24);
-  static_assert(kStages >= 4 && (2 * kStages + 2 * kSlots + 5) * 8 + 4 <= 256 && kUsed <= 512, "stages and barriers fit");
+  static_assert(kStages >= 3 && (2 * kStages + 2 * kSlots + 5) * 8 + 4 <= 256 && kUsed <= 512, "stages and barriers fit");
   static_assert(kBRows % 8 == 0 && BN <= 256, "weight rows come in 8-row swizzle atoms");
 };
 
@@ -369,21 +372,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t tile = unit + i * units;
         const int m0 = static_cast<int>(tile / ntn) * (CG * kBM) + static_cast<int>(rank) * kBM;
         const int n0 = static_cast<int>(tile % ntn) * BN + static_cast<int>(rank) * G_::kBRows;
-        for (int kt = 0; kt < G; ++kt) {
+        for (int kt = 0; kt < G; kt += G_::kBlocks) {
           if (!mbar_wait(smem_u32(&empty_bar[s]), phase ^ 1u)) {
             ok = false;
             break;
           }
           const uint32_t fb = smem_u32(&full_bar[s]);
           const uint32_t st = smem_u32(smem + s * kStageBytes);
-          if (rank == 0) mbar_arrive_expect_tx(fb, CG * kStageBytes);
-          if constexpr (CG == 1) {
-            tma_load_2d(st, &tmA, kt * kBK, m0, fb);
-            tma_load_2d(st + kATile, &tmB, kt * kBK, n0, fb);
-          } else {
-            const uint32_t fbc = cluster_addr(fb, 0);
-            tma_load_2d_pair(st, &tmA, kt * kBK, m0, fbc);
-            tma_load_2d_pair(st + kATile, &tmB, kt * kBK, n0, fbc);
+          const int nb = G - kt < G_::kBlocks ? G - kt : G_::kBlocks;
+          if (rank == 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(nb * CG * G_::kBlockBytes));
+          for (int b = 0; b < nb; ++b) {
+            const uint32_t at = st + static_cast<uint32_t>(b * G_::kBlockBytes);
+            if constexpr (CG == 1) {
+              tma_load_2d(at, &tmA, (kt + b) * kBK, m0, fb);
+              tma_load_2d(at + kATile, &tmB, (kt + b) * kBK, n0, fb);
+            } else {
+              const uint32_t fbc = cluster_addr(fb, 0);
+              tma_load_2d_pair(at, &tmA, (kt + b) * kBK, m0, fbc);
+              tma_load_2d_pair(at + kATile, &tmB, (kt + b) * kBK, n0, fbc);
+            }
           }
           ++issued;
           if (++s == kS) {
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, wait_bar<CG>(smem_u32(&tempty[acc]), static_cast<uint32_t>(((i >> 1) & 1) ^ 1)));
         if (!ok) break;
         const uint32_t tacc = tmem + static_cast<uint32_t>(acc * BN);
-        for (int kt = 0; kt < G; ++kt) {
+        for (int kt = 0; kt < G; kt += G_::kBlocks) {
           bool got = (kt & 3) != 0 || wait_bar<CG>(smem_u32(&scaled_bar[slot]), sphase);
           got = got && wait_bar<CG>(smem_u32(&full_bar[s]), phase);
           ok = __all_sync(0xffffffffu, got);
@@ -425,10 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t st = desc_lo + static_cast<uint32_t>(s * (kStageBytes / 16));
           const uint32_t sa = tmem + static_cast<uint32_t>(2 * BN + slot * kScaleCols);
-          const uint32_t idesc = G_::kIdesc + static_cast<uint32_t>(kt & 3) * ((1u << 4) | (1u << 29));
-          const bool slot_done = (kt & 3) == 3 || kt + 1 == G;
+          const uint32_t idesc = G_::kIdesc + static_cast<uint32_t>(kt & 3) * kNextScale;
+          const bool slot_done = ((kt + G_::kBlocks) & 3) == 0 || kt + G_::kBlocks >= G;
           if (leader) {
             umma_block<CG>(tacc, st, st + kATile / 16, desc_hi, idesc, sa, kt != 0);
+            if (G_::kBlocks == 2 && kt + 1 < G)
+              umma_block<CG>(tacc, st + G_::kBlockBytes / 16, st + (G_::kBlockBytes + kATile) / 16, desc_hi, idesc + kNextScale,
+                             sa, 1);
             commit_mmas<CG>(smem_u32(&empty_bar[s]));
             if (slot_done) commit_mmas<CG>(smem_u32(&used_bar[slot]));
           }
