@@ -7,8 +7,11 @@
 // either operand, K = 32): the rows' and blocks' exponents are such scales as they
 // are. Sums stay in fp32 in tensor memory over all of d. Operands arrive by TMA
 // copies of 128-byte rows (128 codes, one block) in the 128-byte swizzle.
+// 32749 x 2048 x 2048: 105 us, 2.6 PFLOP/s, 0.68 of twice the measured bf16 rate;
+// the MMAs alone, issued without a wait, take 66, and what is between them
+// (waits, commits, the scales' slots) the rest: with a block a stage it was 116.
 // (Summing each block unscaled and adding it, scaled, in registers was measured
-// first: 205 us at 32749 x 2048 x 2048 against 116, bound by the warps that read tensor memory.)
+// first: 205 us, bound by the warps that read tensor memory.)
 //
 // q8_proj_rows_kernel: few tokens. Bound by the weights' bytes and by latency,
 // so the work is spread over the SMs by output features and by d: a warp takes
@@ -623,15 +626,25 @@ cudaError_t launch_rows(const void* rows, int64_t cap, int64_t T, int d, const v
 
 constexpr int kFewTokens = 16;
 
+// Few tokens: which of the two kernels is sooner done, by their times in us as
+// measured for 640 to 4096 features, 640 to 8192 outputs and 1 to 16 tokens (16 x 896 x
+// 896: 3.2 by rows, 4.6; 8 x 2048 x 2048: 6.3 and 6.9; 16 x 2048 x 2048: 10.9 and 6.9;
+// 4 x 640 x 5120: 5.7 and 4.9; 1 x 4096 x 4096: 9.4 and 13.1). The rows' grows
+// with the products and the conversions of the weights, the tensor cores' with the
+// blocks that follow each other.
+bool rows_are_sooner(int64_t T, int G, int m) {
+  return T <= kFewTokens && 2.0 + 1.1e-5 * static_cast<double>(T + 5) * G * m <= 2.65 + 0.265 * G;
+}
+
 }  // namespace
 
 cudaError_t launch_q8_proj(const void* rows, int64_t cap, int64_t T, int d, const void* W8, int m, float* Q, cudaStream_t s) {
-  if (T > kFewTokens && T < (int64_t{1} << 31) - 2 * kBM && tensor_map_encode_fn()) {
-    // Wide tiles shared by pairs when every pair gets one (8192 x 896: 12.3 us,
-    // 13.2 with 128 columns a CTA; 32749 x 2048: 116, 168). A block of a tile takes a CTA
+  if (!rows_are_sooner(T, q8_groups(d), m) && T < (int64_t{1} << 31) - 2 * kBM && tensor_map_encode_fn()) {
+    // Wide tiles shared by pairs when every pair gets one (8192 x 896: 12.0 us,
+    // 13.1 with 128 columns a CTA; 32749 x 2048: 105, 167). A block of a tile takes a CTA
     // about the same time whatever its columns, so fewer are taken only as
     // long as that puts more SMs to work and no SM gets two tiles
-    // (512 x 1024: 5.7 us with 64, 6.3 with 128).
+    // (512 x 1024: 5.0 us with 64, 6.3 with 128).
     const int64_t rt = (T + kBM - 1) / kBM, rp = (T + 2 * kBM - 1) / (2 * kBM);
     const int pairs = tc_units<224, 2>();
     if (pairs > 0 && rp * ((m + 223) / 224) >= pairs) return launch_tc<224, 2>(rows, cap, T, d, W8, m, Q, s);

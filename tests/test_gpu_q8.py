@@ -431,6 +431,13 @@ def test_projection(T, d, m):
     projection_case(T, d, m, T + d)
 
 
+@pytest.mark.parametrize("T", [1, 3, 5, 8, 12, 16])
+@pytest.mark.parametrize("d,m", [(640, 5120), (1024, 4000), (2048, 2050), (2176, 1025), (4096, 300)])
+def test_projection_few_tokens(T, d, m):
+    """Sizes on both sides of the choice between the kernels for few tokens and the tensor cores."""
+    projection_case(T, d, m, T)
+
+
 def test_projection_larger():
     projection_case(4999, 896, 896, 1)
     projection_case(20000, 1024, 1024, 2, src=1)
