@@ -321,27 +321,49 @@ __global__ void __launch_bounds__(kThreads) q8_back_element_kernel(Q8Rows a, int
   }
 }
 
-// One CTA per block of 128 x 128 weights, 64 of them a thread, held in
-// registers between the search for the largest and the rounding.
+// Weights: a CTA a block of 128 x 128, 64 of them a thread as pieces of 16 bytes, so that a
+// warp reads and writes whole lines; with `vec` rows start on 16-byte boundaries and
+// hold whole pieces. They stay in registers between the search for the largest magnitude
+// and the rounding (2048 x 2048 bf16: 5.2 us, 17.9 with an element a lane; 16384 x 16384 fp32: 242 us,
+// 0.82 of the copy rate).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) q8_weight_kernel(const T* W, int m, int d, int G, unsigned char* W8) {
+__global__ void __launch_bounds__(kThreads) q8_weight_kernel(const T* W, int m, int d, int G, int vec, unsigned char* W8) {
+  constexpr int kPer = 16 / sizeof(T), kAcross = 128 / kPer, kDown = kThreads / kAcross, kPieces = 128 / kDown;
   __shared__ float part[kThreads / 32];
   pdl_trigger();
   pdl_wait();
   const int bm = blockIdx.x / G, bk = blockIdx.x - bm * G;
-  const int col = bk * 128 + (threadIdx.x & 127), row0 = bm * 128 + (threadIdx.x >> 7);
-  float x[64];
+  const int col = bk * 128 + threadIdx.x % kAcross * kPer, row0 = bm * 128 + threadIdx.x / kAcross;
+  float x[kPieces][kPer];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int row = row0 + i * kDown;
+    const T* w = W + static_cast<int64_t>(row) * d + col;
+    uint4 piece = make_uint4(0, 0, 0, 0);
+    T* e = reinterpret_cast<T*>(&piece);
+    if (row < m) {
+      if (vec) {
+        if (col < d) piece = __ldcs(reinterpret_cast<const uint4*>(w));
+      } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (col + k < d) e[k] = w[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) x[i][k] = to_f32(e[k]);
+  }
   float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 64; ++i) {
-    const int row = row0 + 2 * i;
-    x[i] = row < m && col < d ? to_f32(W[static_cast<int64_t>(row) * d + col]) : 0.f;
-    // only finite magnitudes count; what is not finite becomes NaN
-    if ((__float_as_uint(x[i]) & 0x7fffffffu) >= kInfBits)
-      x[i] = __uint_as_float(0x7fffffffu);
-    else
-      a = fmaxf(a, fabsf(x[i]));
-  }
+  for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      // only finite magnitudes count; what is not finite becomes NaN
+      if ((__float_as_uint(x[i][k]) & 0x7fffffffu) >= kInfBits)
+        x[i][k] = __uint_as_float(0x7fffffffu);
+      else
+        a = fmaxf(a, fabsf(x[i][k]));
+    }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
@@ -352,11 +374,25 @@ __global__ void __launch_bounds__(kThreads) q8_weight_kernel(const T* W, int m, 
   const uint32_t e = q8_exponent(__float_as_uint(a));
   const float inv = q8_inverse(e), top = q8_top(e);
 #pragma unroll
-  for (int i = 0; i < 64; ++i) {
-    const int row = row0 + 2 * i;
-    float y = x[i] * inv;
-    if (fabsf(y) > top) y = copysignf(top, y);
-    if (row < m) W8[static_cast<int64_t>(row) * (128 * G) + col] = static_cast<unsigned char>(encode4(y, 0.f, 0.f, 0.f));
+  for (int i = 0; i < kPieces; ++i) {
+    const int row = row0 + i * kDown;
+    if (row >= m) break;
+    uint32_t code[kPer / 4];
+#pragma unroll
+    for (int q = 0; q < kPer / 4; ++q) {
+      float y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        y[k] = x[i][4 * q + k] * inv;
+        if (fabsf(y[k]) > top) y[k] = copysignf(top, y[k]);
+      }
+      code[q] = encode4(y[0], y[1], y[2], y[3]);
+    }
+    unsigned char* to = W8 + static_cast<int64_t>(row) * (128 * G) + col;
+    if constexpr (kPer == 8)
+      *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
+    else
+      *reinterpret_cast<uint32_t*>(to) = code[0];
   }
   // The exponents, and with the row's last block the zeros behind them.
   const int stride = q8_block_row(G);
@@ -408,11 +444,12 @@ cudaError_t launch_q8_weight(const void* W, int m, int d, int is_bf16, void* W8,
   const int64_t blocks = static_cast<int64_t>(q8_groups(m)) * G;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   unsigned char* out = static_cast<unsigned char*>(W8);
+  const int vec = aligned16(W) && d % (is_bf16 ? 8 : 4) == 0;
   if (is_bf16)
     return launch_pdl(q8_weight_kernel<bf16>, static_cast<unsigned>(blocks), kThreads, 0, s, static_cast<const bf16*>(W), m,
-                      d, G, out);
+                      d, G, vec, out);
   return launch_pdl(q8_weight_kernel<float>, static_cast<unsigned>(blocks), kThreads, 0, s, static_cast<const float*>(W), m,
-                    d, G, out);
+                    d, G, vec, out);
 }
 
 }  // namespace attnres

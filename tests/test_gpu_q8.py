@@ -266,6 +266,45 @@ def test_two_graphs_at_once():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("shift", [16, 112])
+def test_rows_off_128_bytes(shift):
+    """Sources and weights on 16-byte boundaries that are not 128-byte ones: the same bits."""
+
+    def moved(holder):
+        store = torch.full((holder.buffer.numel() + 256,), 0x5A, dtype=torch.uint8, device=DEV)
+        other = copy.copy(holder)
+        other.__dict__.pop("codes", None)
+        other.buffer = store[shift:shift + holder.buffer.numel()].view(holder.buffer.shape)
+        assert other.pointer % 128 == shift
+        return other, store
+
+    for n, T, d, m in ((5, 700, 640, 640), (9, 40, 1000, 77), (3, 2, 2048, 300), (4, 60, 2304, 130)):
+        g = gen(n)
+        x = _q8.history(n, T, d, g, DEV)
+        W = torch.randn(m, d, generator=g, device=DEV) / d ** 0.5
+        w, gamma = torch.randn(d, generator=g, device=DEV) * 0.05, torch.ones(d, device=DEV)
+        results = []
+        for off in (False, True):
+            rows, W8 = filled(n, T, d, 0), ar.Q8Weight(m, d, device=DEV)
+            stores = []
+            if off:
+                (rows, a), (W8, b) = moved(rows), moved(W8)
+                rows.buffer.zero_()
+                stores = [(a, rows), (b, W8)]
+            ar.attnres_q8_write(x, rows)
+            ar.attnres_q8_weight(W, W8)
+            out, Q, back = torch.empty(T, d, device=DEV), torch.empty(T, m, device=DEV), torch.empty(n, T, d, device=DEV)
+            ar.attnres_full_fwd_q8(rows, n, w, gamma, 1e-6, out)
+            ar.attnres_query_projection_q8(rows, n - 1, W8, Q)
+            ar.attnres_q8_read(rows, back)
+            for store, holder in stores:
+                assert (store[:shift] == 0x5A).all() and (store[shift + holder.buffer.numel():] == 0x5A).all()
+            results.append((rows.buffer.clone(), W8.buffer.clone(), out, Q, back))
+        assert ar.attnres_device_status() == 0
+        for a, b in zip(*results):
+            assert torch.equal(a, b)
+
+
 def test_copies_of_rows():
     """A copied Q8Rows or Q8Weight has storage of its own."""
     T, d = 20, 256
@@ -404,6 +443,18 @@ def test_weight(m, d, dtype):
     G = _q8.groups(d)
     assert not W8.buffer[:m * G * 128].view(m, G * 128)[:, d:].any()
     assert not W8.buffer[m * G * 128:].view(-1, -(-G // 16) * 16)[:, G:].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_weight_off_16_bytes(dtype):
+    """Weights that start between 16-byte boundaries: the same bits."""
+    W = torch.randn(200 * 256 + 8, generator=gen(1), device=DEV).to(TYPES[dtype])
+    want, got = ar.Q8Weight(200, 256, device=DEV), ar.Q8Weight(200, 256, device=DEV)
+    for off in (1, 3):
+        part = W[off:off + 200 * 256].view(200, 256)
+        ar.attnres_q8_weight(part, got)
+        ar.attnres_q8_weight(part.clone(), want)
+        assert torch.equal(got.buffer, want.buffer)
 
 
 def projection_case(T, d, m, seed, spread=0.0, src=0):
