@@ -25,8 +25,7 @@
 // the maxima, sums and accumulators are joined through shared memory (one token, 141
 // sources of 640: 8.2 us, 17.7 with the warps of one CTA).
 //
-// General kernel (wider rows): a CTA a token; the scores of all sources, their
-// softmax, then the weighted sum, reading the rows twice.
+// General kernel (wider rows): a CTA a token, the rows read twice.
 #include <math.h>
 
 #include "q8.cuh"
@@ -425,83 +424,128 @@ __global__ void __launch_bounds__(Q8Read<K, S, C, L, NW>::kThreads, 1)
   if (!ok && lane == 0) atomicOr(&g_q8_read_timeout, 1u);
 }
 
-constexpr int kGenThreads = 256;
+// ---------------------------------------------------------------- general --
+// Rows of any width, a CTA a token. A warp takes every eighth source's score, with
+// u = (w or Q) gamma in shared memory; after the softmax a thread sums 16 features at a
+// time over all sources, which it reads again (from the L1 or L2, as a rule). Four loads of 16
+// codes a thread are in flight in both. 16384 x 4096, nine sources:
+// 274 us, 0.40 of the copy rate (753 with a word a lane and u from global memory); two decodings
+// of every code, and the latency of their loads, bound it.
+constexpr int kGenThreads = 256, kGenWarps = kGenThreads / 32, kGenBatch = 4;
 
-__global__ void __launch_bounds__(kGenThreads) q8_read_general_kernel(Q8ReadArgs a) {
+constexpr int64_t q8_general_smem(int n, int G) { return (n + 512ll * ((G + 3) / 4)) * 4; }
+
+__global__ void __launch_bounds__(kGenThreads, 4) q8_read_general_kernel(Q8ReadArgs a, int vec) {
   extern __shared__ __align__(16) float sm[];
-  const int G = (a.d + 127) / 128, Dp = 128 * G, n = a.n_src, d = a.d;
+  __shared__ float part[2][kGenWarps];
+  const int G = (a.d + 127) / 128, Dp = 128 * G, n = a.n_src, d = a.d, chunks = 8 * G, rounds = (chunks + 31) / 32;
   const int64_t source = q8_source_bytes(a.cap, d);
-  float* z = sm;          // [Dp]
-  float* p = sm + Dp;     // [n] scores, then weights
-  __shared__ float part[kGenThreads / 32];
+  // u: 16 features of a chunk as four vectors, 32 vectors apart, so that a warp's lanes read in a row.
+  float* u = sm;
+  float* z = sm;  // with a pre-norm, once u has been used: features as they come
+  float* p = sm + rounds * 512;  // scores, then weights
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
-  auto block_sum = [&](float x) {
-    x = warp_sum(x);
-    __syncthreads();
-    if (lane == 0) part[warp] = x;
-    __syncthreads();
-    float t = 0.f;
+  // Two sums or maxima in a row use different words, so one barrier each is enough.
+  auto block_join = [&](float x, int which, bool largest) {
 #pragma unroll
-    for (int i = 0; i < kGenThreads / 32; ++i) t += part[i];
-    return t;
+    for (int o = 16; o > 0; o >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, x, o);
+      x = largest ? fmaxf(x, y) : x + y;
+    }
+    if (lane == 0) part[which][warp] = x;
+    __syncthreads();
+    x = part[which][0];
+#pragma unroll
+    for (int i = 1; i < kGenWarps; ++i) x = largest ? fmaxf(x, part[which][i]) : x + part[which][i];
+    return x;
   };
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const unsigned char* rows = static_cast<const unsigned char*>(a.rows) + t * Dp;
     const unsigned char* tails = static_cast<const unsigned char*>(a.rows) + a.cap * Dp + t * q8_tail_bytes(G);
-    const float* q = a.w ? a.w : a.Q + t * d;
-    for (int i = warp; i < n; i += kGenThreads / 32) {
-      const unsigned char *r = rows + i * source, *tail = tails + i * source;
-      float dot = 0.f;
-      for (int w = lane; w < Dp / 4; w += 32) {
-        float2 v0, v1;
-        decode4(*reinterpret_cast<const uint32_t*>(r + 4 * w), v0, v1);
-        const float s = q8_scale(tail[w >> 5]);
-        float x = 0.f;
-        if (4 * w < d) x += v0.x * (q[4 * w] * kQueryDown * a.gamma[4 * w]);
-        if (4 * w + 1 < d) x += v0.y * (q[4 * w + 1] * kQueryDown * a.gamma[4 * w + 1]);
-        if (4 * w + 2 < d) x += v1.x * (q[4 * w + 2] * kQueryDown * a.gamma[4 * w + 2]);
-        if (4 * w + 3 < d) x += v1.y * (q[4 * w + 3] * kQueryDown * a.gamma[4 * w + 3]);
-        dot = fmaf(x, s, dot);
+    if (a.Q || a.pre.gamma || t == blockIdx.x) {
+      const float* q = a.w ? a.w : a.Q + t * d;
+      for (int k = threadIdx.x; k < rounds * 512; k += kGenThreads) {
+        const int c = k >> 4;
+        u[((c >> 5) * 4 + (k >> 2 & 3)) * 128 + (c & 31) * 4 + (k & 3)] = k < d ? q[k] * kQueryDown * a.gamma[k] : 0.f;
       }
-      dot = warp_sum(dot);
-      if (lane == 0) p[i] = dot * (rsqrtf(*reinterpret_cast<const float*>(tail + q8_mean_offset(G)) + a.eps) * kScoreUp);
     }
     __syncthreads();
-    float m = -3.402823466e38f;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, p[i]);
-    __syncthreads();
-    float l = 0.f;
-    for (int i = threadIdx.x; i < n; i += kGenThreads) l += p[i] = __expf(p[i] - m);
-    const float inv = 1.0f / block_sum(l);  // its barriers also order p
-    float q2 = 0.f;
-    for (int w = threadIdx.x; w < Dp / 4; w += kGenThreads) {
-      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-      for (int i = 0; i < n; ++i) {
-        const unsigned char *r = rows + i * source, *tail = tails + i * source;
-        float2 v0, v1;
-        decode4(*reinterpret_cast<const uint32_t*>(r + 4 * w), v0, v1);
-        const float ps = p[i] * q8_scale(tail[w >> 5]);
-        acc0 = ffma2(v0, make_float2(ps, ps), acc0);
-        acc1 = ffma2(v1, make_float2(ps, ps), acc1);
-      }
-      const float o[4] = {acc0.x * inv, acc0.y * inv, acc1.x * inv, acc1.y * inv};
+    for (int i = warp; i < n; i += kGenWarps) {
+      const unsigned char *r = rows + i * source, *tail = tails + i * source;
+      float2 dot = make_float2(0.f, 0.f);
+      for (int c0 = 0; c0 < rounds; c0 += kGenBatch) {
+        uint4 code[kGenBatch];
+        uint32_t e[kGenBatch];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int k = 4 * w + e;
-        q2 = fmaf(o[e], o[e], q2);
-        z[k] = o[e];
-        if (a.out && k < d) {
-          if (a.out_bf16)
-            static_cast<bf16*>(a.out)[t * d + k] = __float2bfloat16_rn(o[e]);
-          else
-            static_cast<float*>(a.out)[t * d + k] = o[e];
+        for (int b = 0; b < kGenBatch; ++b) {
+          const int c = (c0 + b) * 32 + lane;
+          code[b] = c < chunks ? *reinterpret_cast<const uint4*>(r + c * 16) : make_uint4(0, 0, 0, 0);
+          e[b] = c < chunks ? tail[c >> 3] : 1u;
+        }
+#pragma unroll
+        for (int b = 0; b < kGenBatch; ++b) {
+          if (c0 + b >= rounds) break;
+          float2 v[8], x = make_float2(0.f, 0.f);
+          decode16(code[b], v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 w = *reinterpret_cast<const float4*>(u + ((c0 + b) * 4 + k) * 128 + lane * 4);
+            x = ffma2(v[2 * k], make_float2(w.x, w.y), x);
+            x = ffma2(v[2 * k + 1], make_float2(w.z, w.w), x);
+          }
+          const float s = q8_scale(e[b]);
+          dot = ffma2(x, make_float2(s, s), dot);
         }
       }
+      const float x = warp_sum(dot.x + dot.y);
+      if (lane == 0) p[i] = x * (rsqrtf(*reinterpret_cast<const float*>(tail + q8_mean_offset(G)) + a.eps) * kScoreUp);
+    }
+    __syncthreads();
+    float m = -3.402823466e38f;  // finite, so that a score of -inf has weight 0
+    for (int i = threadIdx.x; i < n; i += kGenThreads) m = fmaxf(m, p[i]);
+    m = block_join(m, 0, true);
+    float l = 0.f;
+    for (int i = threadIdx.x; i < n; i += kGenThreads) l += p[i] = __expf(p[i] - m);
+    const float inv = 1.0f / block_join(l, 1, false);  // its barrier also orders p
+    float q2 = 0.f;
+    for (int c = threadIdx.x; c < chunks; c += kGenThreads) {
+      float2 acc[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = make_float2(0.f, 0.f);
+      for (int i0 = 0; i0 < n; i0 += kGenBatch) {
+        uint4 code[kGenBatch];
+        uint32_t e[kGenBatch];
+#pragma unroll
+        for (int b = 0; b < kGenBatch; ++b) {
+          const bool in = i0 + b < n;
+          code[b] = in ? *reinterpret_cast<const uint4*>(rows + (i0 + b) * source + c * 16) : make_uint4(0, 0, 0, 0);
+          e[b] = in ? tails[(i0 + b) * source + (c >> 3)] : 1u;
+        }
+#pragma unroll
+        for (int b = 0; b < kGenBatch; ++b) {
+          if (i0 + b >= n) break;
+          const float ps = p[i0 + b] * q8_scale(e[b]);
+          float2 v[8];
+          decode16(code[b], v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[k] = ffma2(v[k], make_float2(ps, ps), acc[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        acc[k] = fmul2(acc[k], make_float2(inv, inv));
+        q2 = fmaf(acc[k].x, acc[k].x, q2);
+        q2 = fmaf(acc[k].y, acc[k].y, q2);
+      }
+      if (a.out) put16(a.out, a.out_bf16, t, c * 16, d, vec != 0, acc);
+      if (a.pre.gamma)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) *reinterpret_cast<float2*>(z + c * 16 + 2 * k) = acc[k];
     }
     if (a.pre.gamma) {
-      const float rr = rsqrtf(block_sum(q2) / static_cast<float>(d) + a.pre.eps);
+      const float rr = rsqrtf(block_join(q2, 0, false) / static_cast<float>(d) + a.pre.eps);
       for (int k = threadIdx.x; k < d; k += kGenThreads) {
         const float o = a.pre.gamma[k] * (z[k] * rr);
         if (a.out_bf16)
@@ -510,7 +554,7 @@ __global__ void __launch_bounds__(kGenThreads) q8_read_general_kernel(Q8ReadArgs
           static_cast<float*>(a.pre.out)[t * d + k] = o;
       }
     }
-    __syncthreads();
+    __syncthreads();  // p, z and the joins' words are free again
   }
 }
 
@@ -561,14 +605,15 @@ cudaError_t launch_cl(const Q8ReadArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_general(const Q8ReadArgs& a, cudaStream_t s) {
-  const int64_t smem = (static_cast<int64_t>(a.n_src) + 128 * q8_groups(a.d)) * 4;
+  const int64_t smem = q8_general_smem(a.n_src, q8_groups(a.d));
   if (smem > 200 * 1024) return cudaErrorInvalidValue;
   const void* fn = reinterpret_cast<const void*>(&q8_read_general_kernel);
   cudaError_t e = allow_dynamic_smem(fn, 200 * 1024);
   if (e != cudaSuccess) return e;
-  const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
+  const int vec = a.d % (a.out_bf16 ? 8 : 4) == 0 && aligned16(a.out);
+  const int64_t cap = static_cast<int64_t>(sm_count()) * 4;
   return launch_pdl(q8_read_general_kernel, static_cast<unsigned>(a.T < cap ? a.T : cap), kGenThreads, static_cast<int>(smem), s,
-                    a);
+                    a, vec);
 }
 
 }  // namespace

@@ -237,7 +237,7 @@ int attnres_q8_read(const void* rows, int64_t cap, int32_t n, int64_t T, int32_t
  *               out_normed.
  * Outputs overlap nothing. d up to 2048 takes streaming kernels; wider rows
  * take a general one, for which ATTNRES_ERR_UNSUPPORTED means that
- * 4 (n_src + 128 G) bytes are over 200 KB.
+ * 4 (n_src + 512 ceil(G / 4)) bytes are over 200 KB.
  */
 int attnres_full_fwd_q8(const void* rows, int64_t cap, int32_t n_src, int64_t T, int32_t d,
                         const float* w, const float* Q, const float* gamma, float eps,

@@ -206,6 +206,15 @@ def test_full_read_clusters(n, T):
         read_case(n, T, d, "f32", "token" if T % 2 else "fixed", T % 3 == 0, n + T)
 
 
+@pytest.mark.parametrize("d", [2176, 3000, 4096, 5120, 8200, 16384])
+def test_full_read_wide(d):
+    """Rows past the streaming kernel: fewer and more sources than warps, more tokens than CTAs at once, each query and output."""
+    read_case(3, 700, d, "bf16", "fixed", False, d)
+    read_case(17, 21, d, "f32", "token", True, d + 1)
+    read_case(64, 2, d, "bf16", "fixed", True, d + 2, keep=False)
+    read_case(9, 650, d, "f32", "fixed", True, d + 3)
+
+
 def test_broken_rows_in_clusters():
     """NaN in one of many sources, and a token whose other sources have weight 0."""
     n, T, d = 141, 3, 640
@@ -342,7 +351,7 @@ def test_scores_apart():
 def test_broken_rows_stay_to_themselves():
     """A token with a NaN in one source is NaN; its neighbours, in the same warp or not, are what they were. A score of
     -inf has weight 0, zero rows have score 0."""
-    for n, T, d in ((5, 37, 512), (9, 37, 1024), (5, 2, 2048), (3, 5000, 256), (20, 1, 384)):
+    for n, T, d in ((5, 37, 512), (9, 37, 1024), (5, 2, 2048), (3, 5000, 256), (20, 1, 384), (9, 7, 2600)):
         x = _q8.history(n, T, d, gen(2), DEV, loud=False)
         w, gamma = torch.randn(d, generator=gen(3), device=DEV) / d ** 0.5, torch.ones(d, device=DEV)
         rows = ar.Q8Rows(n, T, d, device=DEV)
