@@ -38,10 +38,11 @@ __device__ unsigned int g_q8_read_timeout = 0;
 
 constexpr int kMaxStages = 8;
 constexpr int kSmemMax = 226 * 1024;
-// A query is multiplied with codes of up to 448 before their scale, so it is taken
-// 2^-16 times as large and the score 2^16: no finite product of a value and a
-// query overflows.
-constexpr float kQueryDown = 1.0f / 65536.0f, kScoreUp = 65536.0f;
+// A query is multiplied with values of up to 2^128 and the products are added up, so it is taken
+// 2^-32 times as large and the score 2^32: no sum over a row overflows as long as the query's
+// magnitudes (times gamma) add up to less than 2^32. (Below, a product of an ordinary query
+// and of a row whose squares are still normal numbers, 2^-63 in size, is far from the smallest.)
+constexpr float kQueryDown = 0x1p-32f, kScoreUp = 0x1p32f;
 
 // 16 values into features [k0, k0 + 16) of a row of d features; `vec`: whole
 // 16-byte vectors. The values may be strided pairs of registers.

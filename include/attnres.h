@@ -177,7 +177,8 @@ int attnres_full_fwd_dynq(const void* V, int64_t src_stride, int32_t n_src, int6
  * at 240, so that v_k stays finite. An element that is not finite becomes NaN.
  * With the row goes mean_k v_k^2 (fp32), the mean square its key RMSNorm needs
  * in every read (infinite, and the row's score 0, where squares of its values
- * add up past fp32's range: magnitudes of some 1e19).
+ * add up past fp32's range: magnitudes of some 1e19; for queries whose
+ * magnitudes, times gamma, add up to less than 2^32).
  *
  * A source is `cap` rows in attnres_q8_source_bytes(cap, d) bytes, with G = ceil(d / 128):
  *   cap rows of 128 G bytes: the codes, zero from feature d on;

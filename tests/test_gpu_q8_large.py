@@ -101,6 +101,18 @@ def test_large_sources_among_high_scores(T, d):
         check(x, torch.full((d,), score / d, device=DEV), gamma)
 
 
+@pytest.mark.parametrize("T,d", [(2, 300), (300, 1024), (2433, 1160), (2, 2048), (700, 2048), (5, 2304), (700, 4096)])
+def test_products_of_large_rows_with_the_query(T, d):
+    """Rows of 3e38 of one sign and queries whose magnitudes add up to 2^20: the score is 0, not what is left of an
+    infinite product."""
+    g = gen(T + d + 3)
+    gamma = torch.ones(d, device=DEV)
+    x = torch.zeros(3, T, d, device=DEV)
+    x[1] = 3e38 * (0.9 + 0.1 * torch.rand(T, d, generator=g, device=DEV))
+    for scale in (2.0 ** 20 / d, -(2.0 ** 20) / d):
+        check(x, torch.full((d,), scale, device=DEV), gamma)
+
+
 def test_tiny_sources_keep_their_bits():
     """Values of 1e-36 to 1e-37, whose scores are 0 beside eps: the weights lose nothing beside such scales."""
     for T, d in ((3, 640), (1500, 640), (2433, 1160), (5, 2304)):
