@@ -131,7 +131,9 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t
 // Programmatic dependent launch. A kernel launched with programmatic stream
 // serialization may start while the previous kernel in the stream is still
 // running; pdl_wait() blocks until that kernel has completed and its memory
-// is visible, so every global access of a kernel comes after it. pdl_trigger()
+// is visible, so every global access of a kernel comes after it (by plain loads:
+// the read-only path, __ldg, is for memory nobody writes while the kernel is
+// resident, and the compiler may move it ahead of the wait). pdl_trigger()
 // lets the next kernel's CTAs be scheduled as this grid's CTAs retire.
 // Both are no-ops for a kernel launched without the attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

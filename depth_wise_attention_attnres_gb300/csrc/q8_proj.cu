@@ -58,11 +58,11 @@ __global__ void __launch_bounds__(kRowThreads) q8_proj_rows_kernel(const unsigne
 #pragma unroll
       for (int c = 0; c < kRowCols; ++c) {
         const int64_t j = j0 + c < m ? j0 + c : m - 1;
-        wc[c] = __ldg(reinterpret_cast<const uint4*>(W8 + j * (128 * G)) + ch);
+        wc[c] = reinterpret_cast<const uint4*>(W8 + j * (128 * G))[ch];
       }
 #pragma unroll
       for (int t = 0; t < kRowTokens; ++t)
-        xc[t] = t < nt ? __ldg(reinterpret_cast<const uint4*>(rows + (t0 + t) * (128 * G)) + ch) : make_uint4(0, 0, 0, 0);
+        xc[t] = t < nt ? reinterpret_cast<const uint4*>(rows + (t0 + t) * (128 * G))[ch] : make_uint4(0, 0, 0, 0);
       const uint32_t eb = ex[(j0 >> 7) * exrow + (ch >> 3)];  // 4 columns lie in one block
       float2 w[kRowCols][8];
 #pragma unroll
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t next[7];
     auto fetch = [&] {
 #pragma unroll
-      for (int c = 0; c < 7; ++c) next[c] = __ldg(at7[c]++);
+      for (int c = 0; c < 7; ++c) next[c] = *at7[c]++;
     };
     if (mine > 0) {
       point(0);

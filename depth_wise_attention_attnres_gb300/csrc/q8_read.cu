@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(Q8Read<K, S, C, L, NW>::kThreads, 1)
       const int k = ((i >> 2) * L + j) * 16 + (i & 3) * 4;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (qvec) {
-        if (k < d) x = __ldg(reinterpret_cast<const float4*>(q + k));
+        if (k < d) x = *reinterpret_cast<const float4*>(q + k);
       } else {
         if (k < d) x.x = q[k];
         if (k + 1 < d) x.y = q[k + 1];
