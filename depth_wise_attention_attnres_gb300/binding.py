@@ -596,40 +596,65 @@ def attnres_q8_weight_bytes(m: int, d: int) -> int:
     return int(lib().attnres_q8_weight_bytes(m, d))
 
 
-class Q8Rows:
+class _Q8Storage:
+    """A uint8 tensor `buffer` and views of it. Another of its shape may take its place (on any CUDA device): calls go to
+    the storage there is, and views are kept only until `buffer` is looked at or set, and then made again."""
+
+    def __init__(self, shape: tuple, device):
+        self._shape = shape
+        self.buffer = torch.zeros(shape, dtype=torch.uint8, device="cuda" if device is None else device)
+
+    @property
+    def buffer(self) -> torch.Tensor:
+        self._drop_views()
+        return self._buffer
+
+    @buffer.setter
+    def buffer(self, buffer: torch.Tensor) -> None:
+        if buffer.dtype != torch.uint8 or tuple(buffer.shape) != self._shape or not buffer.is_contiguous():
+            raise ValueError(f"the buffer must be contiguous uint8 {list(self._shape)}, got {buffer.dtype} "
+                             f"{list(buffer.shape)}")
+        if not buffer.is_cuda:
+            raise ValueError("the buffer must be on a CUDA device")
+        self._drop_views()
+        self._buffer = buffer
+        self.device = buffer.get_device()
+
+    def _drop_views(self) -> None:
+        for name in ("codes", "tails", "exponents", "mean_square"):
+            self.__dict__.pop(name, None)
+
+    @property
+    def pointer(self) -> int:
+        return self._buffer.data_ptr()
+
+
+class Q8Rows(_Q8Storage):
     """n sources of T rows of d features in 8 bits: an AttnRes history, or (n = 1) hidden states.
 
     Owns its storage (`buffer`, uint8 [n, attnres_q8_source_bytes(T, d)], zero
-    at first, which must keep its size). `codes` (float8_e4m3fn [n, T, d]),
-    `exponents` (uint8 [n, T, ceil(d / 128)]: the scale of a group is
-    2^(exponent - 127)) and `mean_square` (fp32 [n, T]) are views of it. Calls
-    use the first rows, as many as their [T, d] argument has."""
+    at first). `codes` (float8_e4m3fn [n, T, d]), `exponents` (uint8 [n, T, ceil(d / 128)]:
+    the scale of a group is 2^(exponent - 127)) and `mean_square` (fp32 [n, T])
+    are views of it. Calls use the first rows, as many as their [T, d] argument has."""
 
     def __init__(self, n: int, T: int, d: int, device=None):
         source = attnres_q8_source_bytes(T, d)
         if n < 1 or source < 0:
             raise ValueError("n and d must be at least 1, T at least 0")
         self.n, self.T, self.d, self.source = n, T, d, source
-        self.buffer = torch.zeros(n, source, dtype=torch.uint8, device="cuda" if device is None else device)
-        if not self.buffer.is_cuda:
-            raise ValueError("rows must be on a CUDA device")
-        self.device = self.buffer.get_device()
-
-    @property
-    def pointer(self) -> int:
-        return self.buffer.data_ptr()
+        super().__init__((n, source), device)
 
     @functools.cached_property
     def codes(self) -> torch.Tensor:
         width = -(-self.d // Q8_GROUP) * Q8_GROUP
-        return self.buffer[:, :self.T * width].unflatten(1, (self.T, width))[..., :self.d].view(torch.float8_e4m3fn)
+        return self._buffer[:, :self.T * width].unflatten(1, (self.T, width))[..., :self.d].view(torch.float8_e4m3fn)
 
     @functools.cached_property
     def tails(self) -> torch.Tensor:
         """What goes with each row's codes (uint8 [n, T, bytes])."""
         groups = -(-self.d // Q8_GROUP)
         at, size = self.T * groups * Q8_GROUP, (-(-groups // 4) * 4 + 4 + 15) // 16 * 16
-        return self.buffer[:, at:at + self.T * size].unflatten(1, (self.T, size))
+        return self._buffer[:, at:at + self.T * size].unflatten(1, (self.T, size))
 
     @functools.cached_property
     def exponents(self) -> torch.Tensor:
@@ -641,35 +666,28 @@ class Q8Rows:
         return self.tails[..., at:at + 4].view(torch.float32)[..., 0]
 
 
-class Q8Weight:
+class Q8Weight(_Q8Storage):
     """A weight matrix [m, d] in 8 bits, one scale for each block of 128 x 128: attnres_q8_weight fills it.
 
     `codes` (float8_e4m3fn [m, d]) and `exponents` (uint8 [ceil(m / 128),
-    ceil(d / 128)]) are views of its `buffer` (zero at first)."""
+    ceil(d / 128)]) are views of its `buffer` (uint8 [attnres_q8_weight_bytes(m, d)], zero at first)."""
 
     def __init__(self, m: int, d: int, device=None):
         size = attnres_q8_weight_bytes(m, d)
         if size < 0:
             raise ValueError("m and d must be at least 1")
         self.m, self.d = m, d
-        self.buffer = torch.zeros(size, dtype=torch.uint8, device="cuda" if device is None else device)
-        if not self.buffer.is_cuda:
-            raise ValueError("weights must be on a CUDA device")
-        self.device = self.buffer.get_device()
-
-    @property
-    def pointer(self) -> int:
-        return self.buffer.data_ptr()
+        super().__init__((size,), device)
 
     @functools.cached_property
     def codes(self) -> torch.Tensor:
         width = -(-self.d // Q8_GROUP) * Q8_GROUP
-        return self.buffer[:self.m * width].view(self.m, width)[:, :self.d].view(torch.float8_e4m3fn)
+        return self._buffer[:self.m * width].view(self.m, width)[:, :self.d].view(torch.float8_e4m3fn)
 
     @functools.cached_property
     def exponents(self) -> torch.Tensor:
         groups = -(-self.d // Q8_GROUP)
-        return self.buffer[self.m * groups * Q8_GROUP:].view(-1, -(-groups // 16) * 16)[:, :groups]
+        return self._buffer[self.m * groups * Q8_GROUP:].view(-1, -(-groups // 16) * 16)[:, :groups]
 
 
 def _q8_side(name: str, x: torch.Tensor, rows: Q8Rows, src: int) -> tuple[int, int, int]:
