@@ -908,6 +908,7 @@ def attnres_test_fail_launch(after: int) -> int:
 
 # Kernels whose copy producer attnres_test_withhold_stage can starve.
 WITHHOLD_NONE, WITHHOLD_FULL, WITHHOLD_STAGE1_TC, WITHHOLD_MERGE, WITHHOLD_RESIDUAL, WITHHOLD_Q8_READ = 0, 1, 2, 3, 4, 5
+WITHHOLD_Q8_PROJ = 6
 
 
 def attnres_test_withhold_stage(kernel: int, index: int = 0) -> None:

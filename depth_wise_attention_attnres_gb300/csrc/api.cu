@@ -792,7 +792,7 @@ int attnres_query_projection_q8(const void* rows, int64_t cap, int64_t T, int32_
   if (T > kMaxElements / m || !W8 || !aligned16(W8) || !Q || off_element(Q, 4)) return ATTNRES_ERR_INVALID_ARG;
   const Range rq = range_of(Q, T * m * 4);
   if (overlap(rq, rr) || overlap(rq, range_of(W8, bytes))) return ATTNRES_ERR_INVALID_ARG;
-  return launched([&] { return launch_q8_proj(rows, cap, T, d, W8, m, Q, as_stream(stream)); });
+  return launched([&] { return launch_q8_proj(rows, cap, T, d, W8, m, Q, withhold_for(kWithholdQ8Proj), as_stream(stream)); });
 }
 
 int attnres_rmsnorm(const void* x, int64_t T, int32_t d, int32_t dtype, const float* gamma, float eps, void* out,

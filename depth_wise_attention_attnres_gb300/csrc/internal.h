@@ -329,14 +329,16 @@ cudaError_t launch_q8_write(const Q8Rows& a, cudaStream_t s);
 cudaError_t launch_q8_back(const Q8Rows& a, cudaStream_t s);
 cudaError_t launch_q8_weight(const void* W, int m, int d, int is_bf16, void* W8, cudaStream_t s);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
-cudaError_t launch_q8_proj(const void* rows, int64_t cap, int64_t T, int d, const void* W8, int m, float* Q, cudaStream_t s);
+// withhold: test hook of the tensor-core kernel, the stage of each CTA to leave unfilled, or -1.
+cudaError_t launch_q8_proj(const void* rows, int64_t cap, int64_t T, int d, const void* W8, int m, float* Q, int64_t withhold,
+                           cudaStream_t s);
 cudaError_t take_timeout_q8_read(unsigned int* flag);
 cudaError_t take_timeout_q8_proj(unsigned int* flag);
 
 // Failure-path test hooks (api.cu), off by default. Which producer, if any,
 // withholds a copy: the tile index to leave unissued, or -1.
 enum WithholdKernel { kWithholdNone = 0, kWithholdFull = 1, kWithholdStage1Tc = 2, kWithholdMerge = 3, kWithholdResidual = 4,
-                      kWithholdQ8Read = 5, kWithholdLast = kWithholdQ8Read };
+                      kWithholdQ8Read = 5, kWithholdQ8Proj = 6, kWithholdLast = kWithholdQ8Proj };
 int64_t withhold_for(WithholdKernel k);
 
 // Device-side timeout records of each kernel file: read and clear (blocking).

@@ -224,7 +224,8 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
 template <int BN, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     q8_proj_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const unsigned char* tails, int64_t T, int d, const unsigned char* W8, int m, float* Q, int vec) {
+                      const unsigned char* tails, int64_t T, int d, const unsigned char* W8, int m, float* Q, int vec,
+                      int64_t withhold) {
   using G_ = Tile<BN, CG>;
   constexpr int kS = G_::kStages, kStageBytes = G_::kStageBytes;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -382,8 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t fb = smem_u32(&full_bar[s]);
           const uint32_t st = smem_u32(smem + s * kStageBytes);
-          const int nb = G - kt < G_::kBlocks ? G - kt : G_::kBlocks;
-          if (rank == 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(nb * CG * G_::kBlockBytes));
+          // The test hook leaves a stage unfilled, in both CTAs of a pair.
+          const int nb = issued == withhold ? 0 : (G - kt < G_::kBlocks ? G - kt : G_::kBlocks);
+          if (rank == 0 && nb > 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(nb * CG * G_::kBlockBytes));
           for (int b = 0; b < nb; ++b) {
             const uint32_t at = st + static_cast<uint32_t>(b * G_::kBlockBytes);
             if constexpr (CG == 1) {
@@ -402,14 +404,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok) {
-        atomicOr(&g_q8_proj_timeout, 1u);
-        // The even CTA's full barriers count both CTAs' copies; once the
-        // phases it armed complete, no copy of either CTA is in flight.
-        if (rank == 0)
-          for (int64_t it = issued > kS ? issued - kS : 0; it < issued; ++it)
-            (void)wait_bar<CG>(smem_u32(&full_bar[it % kS]), static_cast<uint32_t>((it / kS) & 1));
-      }
+      // The even CTA's full barriers count both CTAs' copies; once the phases
+      // it armed complete, no copy of either CTA is in flight. Waited for on every path: this
+      // warp may have issued all its stages when another one's wait runs out.
+      if (rank == 0)
+        for (int64_t it = issued > kS ? issued - kS : 0; it < issued; ++it)
+          if (it != withhold) ok &= wait_bar<CG>(smem_u32(&full_bar[it % kS]), static_cast<uint32_t>((it / kS) & 1));
+      if (!ok) atomicOr(&g_q8_proj_timeout, 1u);
     }
     __syncwarp();
   } else if (warp == kIssuer) {
@@ -595,7 +596,8 @@ int tc_units() {
 }
 
 template <int BN, int CG>
-cudaError_t launch_tc(const void* rows, int64_t cap, int64_t T, int d, const void* W8, int m, float* Q, cudaStream_t s) {
+cudaError_t launch_tc(const void* rows, int64_t cap, int64_t T, int d, const void* W8, int m, float* Q, int64_t withhold,
+                      cudaStream_t s) {
   using G_ = Tile<BN, CG>;
   alignas(64) CUtensorMap ma, mb;
   const int G = q8_groups(d);
@@ -612,7 +614,7 @@ cudaError_t launch_tc(const void* rows, int64_t cap, int64_t T, int d, const voi
   cudaLaunchAttribute attr[2];
   tc_config<BN, CG>(cfg, attr, units, s);
   return cudaLaunchKernelEx(&cfg, kernel, ma, mb, static_cast<const unsigned char*>(rows) + cap * (128 * G), T, d,
-                            static_cast<const unsigned char*>(W8), m, Q, m % 4 == 0 && aligned16(Q) ? 1 : 0);
+                            static_cast<const unsigned char*>(W8), m, Q, m % 4 == 0 && aligned16(Q) ? 1 : 0, withhold);
 }
 
 template <int KS>
@@ -638,7 +640,8 @@ bool rows_are_sooner(int64_t T, int G, int m) {
 
 }  // namespace
 
-cudaError_t launch_q8_proj(const void* rows, int64_t cap, int64_t T, int d, const void* W8, int m, float* Q, cudaStream_t s) {
+cudaError_t launch_q8_proj(const void* rows, int64_t cap, int64_t T, int d, const void* W8, int m, float* Q, int64_t withhold,
+                           cudaStream_t s) {
   if (!rows_are_sooner(T, q8_groups(d), m) && T < (int64_t{1} << 31) - 2 * kBM && tensor_map_encode_fn()) {
     // Wide tiles shared by pairs when every pair gets one (8192 x 896: 12.0 us,
     // 13.1 with 128 columns a CTA; 32749 x 2048: 105, 167). A block of a tile takes a CTA
@@ -647,9 +650,9 @@ cudaError_t launch_q8_proj(const void* rows, int64_t cap, int64_t T, int d, cons
     // (512 x 1024: 5.0 us with 64, 6.3 with 128).
     const int64_t rt = (T + kBM - 1) / kBM, rp = (T + 2 * kBM - 1) / (2 * kBM);
     const int pairs = tc_units<224, 2>();
-    if (pairs > 0 && rp * ((m + 223) / 224) >= pairs) return launch_tc<224, 2>(rows, cap, T, d, W8, m, Q, s);
-    if (rt * ((m + 63) / 64) <= sm_count()) return launch_tc<64, 1>(rows, cap, T, d, W8, m, Q, s);
-    return launch_tc<128, 1>(rows, cap, T, d, W8, m, Q, s);
+    if (pairs > 0 && rp * ((m + 223) / 224) >= pairs) return launch_tc<224, 2>(rows, cap, T, d, W8, m, Q, withhold, s);
+    if (rt * ((m + 63) / 64) <= sm_count()) return launch_tc<64, 1>(rows, cap, T, d, W8, m, Q, withhold, s);
+    return launch_tc<128, 1>(rows, cap, T, d, W8, m, Q, withhold, s);
   }
   const int G = q8_groups(d);
   if (G <= 4) return launch_rows<1>(rows, cap, T, d, W8, m, Q, s);

@@ -791,10 +791,11 @@ int64_t attnres_test_fail_launch(int64_t after);
  * merge (index counts each CTA's tiles; tiles fetched before the previous
  * kernel finishes, in a Block pass, are never withheld), 4 = the gated residual
  * and its backward (index counts each team's rows), 5 = the streaming read over
- * 8-bit rows (index counts each CTA's stages, of one or more sources). Every CTA
- * (4: team) with more than `index` copies withholds its copy number `index`; its
- * other copies are issued and waited for before the CTA exits. Stays set until
- * changed.
+ * 8-bit rows (index counts each CTA's stages, of one or more sources), 6 = the
+ * 8-bit projection on tensor cores (index counts each CTA's stages, of one or
+ * two blocks of 128 features). Every CTA (4: team) with more than `index` copies
+ * withholds its copy number `index`; its other copies are issued and waited for
+ * before the CTA exits. Stays set until changed.
  * Returns ATTNRES_ERR_INVALID_ARG for an unknown kernel or a negative index.
  */
 int attnres_test_withhold_stage(int32_t kernel, int64_t index);
