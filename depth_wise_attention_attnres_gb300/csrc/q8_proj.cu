@@ -7,11 +7,14 @@
 // either operand, K = 32): the rows' and blocks' exponents are such scales as they
 // are. Sums stay in fp32 in tensor memory over all of d. Operands arrive by TMA
 // copies of 128-byte rows (128 codes, one block) in the 128-byte swizzle.
-// 32749 x 2048 x 2048: 105 us, 2.6 PFLOP/s, 0.68 of twice the measured bf16 rate;
-// the MMAs alone, issued without a wait, take 66, and what is between them
-// (waits, commits, the scales' slots) the rest: with a block a stage it was 116.
-// (Summing each block unscaled and adding it, scaled, in registers was measured
-// first: 205 us, bound by the warps that read tensor memory.)
+// 32749 x 2048 x 2048: 105 to 107 us alone (2.6 PFLOP/s, 0.67 of twice the measured bf16
+// rate), 121 to 123 in a row of calls (2.3). The MMAs alone, with no copies, waits, scales or
+// stores, take 66, with their commits 74. Which of the rest bounds it has not been told apart:
+// with one block a stage (116 us), bringing back the operands' copies and the waits for them was the
+// largest step, to 102, and the scales took it to 110; the copies are 1.26 GB through
+// the L2, 14 TB/s together with the results. Two blocks a stage, with half the waits
+// and commits, took it to 107. (Summing each block unscaled and adding it, scaled, in registers
+// was measured first: 205 us, bound by the warps that read tensor memory.)
 //
 // q8_proj_rows_kernel: few tokens. Bound by the weights' bytes and by latency,
 // so the work is spread over the SMs by output features and by d: a warp takes
@@ -647,7 +650,9 @@ cudaError_t launch_q8_proj(const void* rows, int64_t cap, int64_t T, int d, cons
     // 13.1 with 128 columns a CTA; 32749 x 2048: 105, 167). A block of a tile takes a CTA
     // about the same time whatever its columns, so fewer are taken only as
     // long as that puts more SMs to work and no SM gets two tiles
-    // (512 x 1024: 5.0 us with 64, 6.3 with 128).
+    // (512 x 1024: 5.0 us with 64, 6.3 with 128). 224 is the widest that leaves tensor memory for
+    // two accumulators and the scales; the last column tile takes as long however few columns
+    // are left (1024 and 2048 outputs: 9 % more than they need, 512: 31 %, 256: 75 %).
     const int64_t rt = (T + kBM - 1) / kBM, rp = (T + 2 * kBM - 1) / (2 * kBM);
     const int pairs = tc_units<224, 2>();
     if (pairs > 0 && rp * ((m + 223) / 224) >= pairs) return launch_tc<224, 2>(rows, cap, T, d, W8, m, Q, withhold, s);

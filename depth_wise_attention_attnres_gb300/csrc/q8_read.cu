@@ -12,11 +12,13 @@
 //
 // It is bound by instructions, not bytes: a code takes half a conversion to fp16,
 // one to fp32 and two half multiply-adds (pairs), and u, values and accumulators
-// take most of the registers, so an SM has 7 to 15 warps, which issue in 40 % of the
-// cycles. What helped was less around a source: several sources a stage (64 x 8192 x 896:
-// 178 us with one source a stage, 123 with six), a rescaling only when the maximum
+// take most of the registers, so an SM has 7 to 15 warps, which issue in 44 % of the
+// cycles. (So half the bytes of bf16 rows are not half the time: 64 x 8192 x 896 takes 117 us,
+// the read of bf16 rows 155; 141 x 32768 x 640 798 and 854.) What helped was less around a
+// source: several sources a stage (64 x 8192 x 896 with the pre-norm: 178 us with one source
+// a stage, 123 with six, 119 now), a rescaling only when the maximum
 // has grown by 8, and gains from shared memory (8192 x 896, 33 sources, a query for
-// each token: 105 us with scalar loads of gamma and query, 83 now). Scores by the tensor cores, with
+// each token: 105 us with scalar loads of gamma and query, 82 now). Scores by the tensor cores, with
 // the values weighted here, took 161 us and more; their operands have to be decoded
 // and laid out anew.
 //
@@ -438,7 +440,7 @@ __global__ void __launch_bounds__(Q8Read<K, S, C, L, NW>::kThreads, 1)
 // u = (w or Q) gamma in shared memory; after the softmax a thread sums 16 features at a
 // time over all sources, which it reads again (from the L1 or L2, as a rule). Four loads of 16
 // codes a thread are in flight in both. 16384 x 4096, nine sources:
-// 274 us, 0.40 of the copy rate (753 with a word a lane and u from global memory); two decodings
+// 276 us, 0.40 of the copy rate (753 with a word a lane and u from global memory); two decodings
 // of every code, and the latency of their loads, bound it.
 constexpr int kGenThreads = 256, kGenWarps = kGenThreads / 32, kGenBatch = 4;
 
@@ -644,8 +646,8 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
   const int G = q8_groups(a.d);
   // In each line the last C step holds codes: 8 G > (C - 1) L. Few tokens: a
   // token's sources spread over many warps and CTAs, so few to a stage (9 sources:
-  // 228 x 640 in 6.0 us, 7.7 by the kernels below; 33: 228 x 2048 in 12.5 and 14.8, 228 x 640
-  // in 9.9 and 8.0, 300 x 640 in 10.1 and 8.2).
+  // 228 x 640 in 6.0 us, 7.8 by the kernels below; 33: 228 x 2048 in 12.7 and 14.4, 228 x 640
+  // in 10.0 and 8.0, 300 x 640 in 10.1 and 8.1).
   const int sms = sm_count();
   if (a.T <= 3 * sms / 2) {
     if (G <= 4) return launch_cl<2, 2, 1, 32, 15, true>(a, s);
@@ -653,6 +655,9 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
     if (G <= 12) return launch_cl<1, 1, 3, 32, 7, true>(a, s);
     if (G <= 16) return launch_cl<1, 1, 4, 32, 7, true>(a, s);
   }
+  // Warps: 11 where a lane's state fits their 168 registers (C = 3 spills up to 80 bytes, C = 2 with
+  // two sources at a time 56), 7 of up to 255 registers otherwise. With C = 3 and L = 16 7 are sooner done
+  // (141 x 8192 x 640: 205 us, 208 with 11 and five sources a stage), with L = 32 11 (33 x 8192 x 1216: 100, 114 with 7).
   auto rounds = [&](int tile) { return (a.T + static_cast<int64_t>(sms) * tile - 1) / (static_cast<int64_t>(sms) * tile) * tile; };
   switch (G) {
     case 1: return launch_cl<6, 1, 2, 4, 11>(a, s);
@@ -664,7 +669,7 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
     case 8:
       // Tiles of 14 tokens, or of 11 where their last round leaves fewer SMs
       // idle and no tokens are shared by warps of the first (64 sources of 896: 1200 tokens
-      // 34.4 us and 29.6, 2000 tokens 35.7 and 47.1, 850 tokens 23.3 and 28.9).
+      // 30.8 us and 27.1, 2000 tokens 34.7 and 45.8, 850 tokens 20.9 and 26.9).
       return a.T <= 6 * sms || rounds(14) * 20 <= rounds(11) * 21 ? launch_cl<6, 1, 4, 16, 7>(a, s)
                                                                   : launch_cl<4, 2, 2, 32, 11>(a, s);
     case 9: case 10: case 11: case 12: return launch_cl<5, 1, 3, 32, 11>(a, s);

@@ -161,8 +161,10 @@ int attnres_full_fwd_dynq(const void* V, int64_t src_stride, int32_t n_src, int6
 
 /*
  * 8-bit rows. The history of a Full read, and the hidden states its queries are
- * projected from, may be held in 8 bits: half the bytes of bf16, and the read
- * is bound by the history's bytes. The pages have no counterpart; they name the
+ * projected from, may be held in 8 bits: half the bytes of bf16. A read, bound
+ * by the conversion of the codes, takes as long as one of bf16 rows (3 sources)
+ * or less (by 7 % for 141 sources of 640 features, a quarter to a third at most
+ * other sizes). The pages have no counterpart; they name the
  * history's memory as the cost of Full AttnRes (DepthBench reading notes,
  * section 4.7 and Fig. 11).
  *
@@ -212,7 +214,9 @@ int attnres_q8_write(const void* x, int64_t x_stride, int32_t n, int64_t T, int3
 /*
  * attnres_q8_read - the values 8-bit rows stand for: out = c * 2^e. In bf16
  * they are exact (codes have four significant bits) down to bf16's smallest
- * number, so attnres_full_bwd over them is the backward of attnres_full_fwd_q8.
+ * number, so attnres_full_bwd over them is the backward of attnres_full_fwd_q8
+ * with the shared query w, up to z (the pre-norm's is attnres_rmsnorm_bwd).
+ * There is no backward for the queries of tokens, Q.
  *
  *   rows, cap, n, T, d   as attnres_q8_write.
  *   out         device, n slices [T, d] of out_dtype, out_stride elements
@@ -236,8 +240,12 @@ int attnres_q8_read(const void* rows, int64_t cap, int32_t n, int64_t T, int32_t
  *               or both NULL.
  *   out         device, [T, d] of out_dtype; NULL (z not stored) only with
  *               out_normed.
- * Outputs overlap nothing. d up to 2048 takes streaming kernels; wider rows
- * take a general one, for which ATTNRES_ERR_UNSUPPORTED means that
+ * Outputs overlap nothing. Which kernel runs, and how many warps and CTAs share
+ * a token's sources, depends on T, n_src and d; so do the last bits of z.
+ * Nothing overflows on the way to z, which is finite where the values and the
+ * scores are; the pre-norm of a z whose squares add up past fp32's range is 0.
+ * d up to 2048 takes streaming kernels; wider rows take a general one, for
+ * which ATTNRES_ERR_UNSUPPORTED means that
  * 4 (n_src + 512 ceil(G / 4)) bytes are over 200 KB.
  */
 int attnres_full_fwd_q8(const void* rows, int64_t cap, int32_t n_src, int64_t T, int32_t d,
@@ -263,8 +271,12 @@ int64_t attnres_q8_weight_bytes(int32_t m, int32_t d);
 /*
  * attnres_query_projection_q8 - the input-dependent query's projection
  * (attnres_query_projection) of 8-bit rows by an 8-bit weight matrix:
- * Q[t, j] = sum_k v[t, k] W[j, k], with products of codes summed in fp32 over
- * each block of 128 features and the blocks' sums scaled and added in fp32.
+ * Q[t, j] = sum_k v[t, k] W[j, k], summed in fp32 in an order that is not
+ * specified: with G = ceil(d / 128) the result is within (d + 2 G + 4) 2^-24 of
+ * sum_k |v[t, k] W[j, k]|. (On tensor cores products of 32 features, scaled, are
+ * added to one sum over all of d; for few tokens the sums of 16 features are
+ * scaled and added.) Which kernel runs, and so the last bits, depends on T, d
+ * and m.
  *
  *   rows, cap   device, one source of cap >= T rows of d features.
  *   W8          device, [m, d] as attnres_q8_weight laid it out, 16-byte aligned. m need not be

@@ -113,6 +113,20 @@ def test_products_of_large_rows_with_the_query(T, d):
         check(x, torch.full((d,), scale, device=DEV), gamma)
 
 
+@pytest.mark.parametrize("T,d", [(2, 640), (2433, 1160), (5, 2304)])
+def test_the_pre_norm_of_a_large_result(T, d):
+    """A z whose squares add up past fp32's range has the pre-norm 0, beside tokens whose z is ordinary."""
+    x = torch.ones(2, T, d, device=DEV)
+    x[:, 1] = 3e38
+    rows = ar.attnres_q8_write(x, ar.Q8Rows(2, T, d, device=DEV))
+    one, out, normed = torch.ones(d, device=DEV), torch.empty(T, d, device=DEV), torch.empty(T, d, device=DEV)
+    ar.attnres_full_fwd_q8(rows, 2, one / d, one, 1e-6, out, gamma_pre=one, eps_pre=0.0, out_normed=normed)
+    back = ar.attnres_q8_read(rows, torch.empty(2, T, d, device=DEV))
+    assert ((out.double() / back[0].double() - 1).abs() <= 2.0 ** -20).all()
+    ordinary = torch.arange(T, device=DEV) != 1
+    assert not normed[1].any() and ((normed[ordinary] - 1).abs() <= 2.0 ** -16).all()
+
+
 def test_tiny_sources_keep_their_bits():
     """Values of 1e-36 to 1e-37, whose scores are 0 beside eps: the weights lose nothing beside such scales."""
     for T, d in ((3, 640), (1500, 640), (2433, 1160), (5, 2304)):
